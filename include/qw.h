@@ -416,6 +416,206 @@ int qw_gptq_quantize_pack(int bits, int64_t group, int64_t n, int64_t k,
                           void* work, int64_t work_bytes, void* stream);
 
 /*
+ * Block-scaled 8-bit floating point (e4m3).
+ *
+ *   code      one byte per value: OCP e4m3 (1 sign, 4 exponent, 3 mantissa
+ *             bits, no infinity, largest value 448).
+ *   blocks    QW_BLOCK = 128 consecutive values of the reduction axis k, of
+ *             `block_rows` consecutive rows: 128 (128 x 128 blocks, for
+ *             weights) or 1 (1 x 128, for activations, gradients and weights
+ *             with a scale of their own in every output channel).  The last
+ *             block of an axis holds what is left of it.
+ *   scale     one fp32 per block: S = max|w| / 448, an IEEE fp32 division; 1
+ *             where that is zero.
+ *   value     code = e4m3(clip(fl32(w / S), -448, 448)), rounded to nearest
+ *             even; the value it stands for is code * S.
+ *   layout    codes [n][kp] with kp = qw_block_pitch(k), k rounded up to
+ *             whole blocks; the bytes behind k are zero.  scales
+ *             [ceil(n / block_rows)][kp / 128].  Every row starts a 128-byte
+ *             line, so no k needs a kernel of its own.
+ *   `codes` pointers are 16-byte aligned (QW_EARG otherwise); all others may
+ *   have the alignment of their type.
+ *   `type`, `x_type`, `y_type`: QW_F32 or QW_BF16 (bit patterns), QW_EARG
+ *   otherwise; y is rounded once, to nearest even, from the fp32 sums.
+ *
+ * Transposing a weight and quantizing again moves its 128 x 128 blocks, codes
+ * and scales unchanged: the gradient with regard to a product's input is
+ * qw_block_gemm with the transposed weight.  The gradient with regard to the
+ * weight is qw_block_gemm of the transposed output gradient and the transposed
+ * input, both quantized with block_rows 1.
+ */
+#define QW_BLOCK 128
+enum qw_type { QW_F32 = 0, QW_BF16 = 1 };
+
+/* Bytes of one row of codes (-1 if k is invalid). */
+int64_t qw_block_pitch(int64_t k);
+
+/* Number of scales of an n x k matrix (-1 if invalid). */
+int64_t qw_block_num_scales(int block_rows, int64_t n, int64_t k);
+
+/*
+ * Quantize `count` matrices that lie one after another.
+ *   w       [count][n][k]                               (read)
+ *   codes   [count][n][qw_block_pitch(k)]               (written)
+ *   scales  [count][qw_block_num_scales(...)]           (written)
+ * block_rows is 1 or 128 (QW_EARG otherwise).  One pass over w.
+ */
+int qw_block_quantize(int block_rows, int64_t count, int64_t n, int64_t k, int type,
+                      const void* w, uint8_t* codes, float* scales, void* stream);
+
+/*
+ * Quantize the gated product of an MLP's two halves with 1 x 128 blocks:
+ *   h       fp32 or bf16 [rows][2 f]: gate | up         (read)
+ *   v       = gate / (1 + exp(-gate)) * up, in fp32
+ *   codes   [rows][qw_block_pitch(f)], scales [rows][...] of v  (written)
+ * `used` (DEVICE int32, may be NULL): how many of the rows there are; the
+ * others are neither read nor written.
+ */
+int qw_block_quantize_swiglu(int64_t rows, int64_t f, int type, const void* h,
+                             const int32_t* used, uint8_t* codes, float* scales,
+                             void* stream);
+
+/* Values of `count` matrices of codes: out fp32 [count][n][k] =
+ * fl32(code * S). */
+int qw_block_unpack(int block_rows, int64_t count, int64_t n, int64_t k,
+                    const uint8_t* codes, const float* scales, float* out, void* stream);
+
+/*
+ * Product of two quantized matrices on the 8-bit matrix cores:
+ *   y[r][i] = sum_b sx[r][b] * sw[i / block_rows][b] * sum_{j in b} x[r][j] w[i][j]
+ *   codes, scales       the weight, n x k               (read)
+ *   x_codes, x_scales   m rows of k values, 1 x 128     (read)
+ *   y                   [m][n]                          (written), m >= 0
+ * A block of 128 is summed before its scales are applied; sums are held in
+ * fp32.  Deterministic: the same call gives the same bits, and rows of x do not
+ * influence each other.
+ *   y_type QW_F32   on the bf16 matrix cores, which take the codes exactly:
+ *                   error <= 1e-5 * sum_j |x[r][j] * w[i][j]|
+ *   y_type QW_BF16  on the 8-bit cores, twice as fast; they keep 13 bits below
+ *                   the largest of 8 products that they add at a time:
+ *                   error <= 1e-3 * sum_j |x[r][j] * w[i][j]| (about 1e-5 of
+ *                   y's size for values of similar size), and y's rounding
+ */
+int qw_block_gemm(int block_rows, int64_t n, int64_t k, const uint8_t* codes,
+                  const float* scales, int64_t m, const uint8_t* x_codes,
+                  const float* x_scales, int y_type, void* y, void* stream);
+
+/*
+ * The same with float activations, quantized on the way (1 x 128 blocks):
+ * qw_block_quantize into `work` and qw_block_gemm, or one kernel that
+ * quantizes as it loads for few rows of x; the codes are the same either way.
+ *   x [m][k] (read),  y [m][n] (written),
+ *   work: qw_block_matmul_work_bytes(m, k) bytes, 16-byte aligned (QW_EWORK).
+ */
+int64_t qw_block_matmul_work_bytes(int64_t m, int64_t k);
+int qw_block_matmul(int block_rows, int64_t n, int64_t k, const uint8_t* codes,
+                    const float* scales, int64_t m, int x_type, const void* x,
+                    int y_type, void* y, void* work, int64_t work_bytes, void* stream);
+
+/*
+ * The product of rows sorted by expert with each expert's own weight:
+ *   codes, scales  `experts` weights of n x k one after another  (read)
+ *   offsets   DEVICE int32 [experts + 1]: rows offsets[e] .. offsets[e+1]-1
+ *             are multiplied by weight e (nondecreasing; as qw_moe_sort writes
+ *             them).  Values outside [0, rows] are clamped to it.
+ *   x_codes, x_scales  `rows` rows of k values, 1 x 128          (read)
+ *   y         [rows][n]; rows that no expert has are left as they are.
+ */
+int qw_block_gemm_grouped(int block_rows, int64_t experts, int64_t n, int64_t k,
+                          const uint8_t* codes, const float* scales, int64_t rows,
+                          const uint8_t* x_codes, const float* x_scales,
+                          const int32_t* offsets, int y_type, void* y, void* stream);
+
+/*
+ * Tokens sorted by expert and back (the data movement of a layer that sends
+ * each of t tokens to topk of its experts).
+ *
+ * A slot is one (token, choice) pair, numbered token * topk + choice.  All
+ * index arrays are DEVICE arrays.  t * topk is at most QW_MOE_MAX_SLOTS
+ * (QW_ESHAPE), 1 <= experts <= QW_MOE_MAX_EXPERTS and topk >= 1 (QW_EARG).
+ */
+#define QW_MOE_MAX_EXPERTS 512
+#define QW_MOE_MAX_SLOTS (1ll << 30)
+
+/* Work bytes for qw_moe_sort (-1 if invalid). */
+int64_t qw_moe_sort_work_bytes(int64_t t, int64_t topk, int64_t experts);
+
+/*
+ * Stable sort of the slots by expert.
+ *   ids      [t][topk], int32 or int64 by `id_bytes` (4 or 8, QW_EARG)  (read)
+ *            An id outside [0, experts) takes its slot out: padding, or an
+ *            expert of another process.
+ *   pos      int32 [t][topk]: the slot's row in expert order, -1 if out (written)
+ *   order    int32 [t * topk]: the slot of each row, -1 behind the last
+ *            row (written; may be NULL)
+ *   offsets  int32 [experts + 1]: an expert's first row; the last entry is
+ *            the number of rows (written)
+ */
+int qw_moe_sort(int64_t t, int64_t topk, int64_t experts, int id_bytes, const void* ids,
+                int32_t* pos, int32_t* order, int32_t* offsets, void* work,
+                int64_t work_bytes, void* stream);
+
+/*
+ * Token rows into expert order: xs[pos[i][j]] = x[i].
+ *   x [t][d] (read), pos [t][topk] (read), xs [rows][d] (written)
+ * A position outside [0, rows) is skipped; rows without a slot are left as
+ * they are.  Positions must differ from each other.
+ */
+int qw_moe_gather(int64_t t, int64_t topk, int64_t d, int64_t rows, int type,
+                  const void* x, const int32_t* pos, void* xs, void* stream);
+
+/* The same with the rows quantized on the way (1 x 128 blocks): codes
+ * [rows][qw_block_pitch(d)], scales [rows][qw_block_pitch(d) / 128]. */
+int qw_moe_gather_block(int64_t t, int64_t topk, int64_t d, int64_t rows, int type,
+                        const void* x, const int32_t* pos, uint8_t* codes, float* scales,
+                        void* stream);
+
+/*
+ * Rows back to their tokens: y[i] = sum_j weights[i][j] * ys[pos[i][j]], in
+ * fp32, j in order, rounded once.
+ *   ys [rows][d] of `type` (read), weights fp32 [t][topk] or NULL (all 1),
+ *   y [t][d] of `y_type` (written; zero for a token without rows)
+ * The row and the weight of a slot whose position is outside [0, rows) are not
+ * looked at.  With weights NULL and dxs for ys it is qw_moe_gather's gradient.
+ */
+int qw_moe_combine(int64_t t, int64_t topk, int64_t d, int64_t rows, int type,
+                   const void* ys, const int32_t* pos, const float* weights, int y_type,
+                   void* y, void* stream);
+
+/*
+ * Gradients of qw_moe_combine for the output gradient dy [t][d]:
+ *   dys[pos[i][j]] = weights[i][j] * dy[i]   [rows][d] (written; may be NULL)
+ *   dweights[i][j] = sum dy[i] * ys[pos[i][j]]  fp32 [t][topk], 0 for a slot
+ *                    without a row (written; may be NULL, then ys may be too)
+ * dy, ys and dys have `type`; rows without a slot are left as they are.
+ * weights may be NULL (all 1).
+ */
+int qw_moe_combine_backward(int64_t t, int64_t topk, int64_t d, int64_t rows, int type,
+                            const void* dy, const void* ys, const int32_t* pos,
+                            const float* weights, void* dys, float* dweights,
+                            void* stream);
+
+/*
+ * A gated expert MLP, the calls above in one:
+ *   y[i] = sum_j weights[i][j] * D_e Q(silu(g) * u),  [g | u] = G_e Q(x[i]),
+ *   e = ids[i][j], Q the 1 x 128 quantizer
+ *   gate_up  `experts` weights of 2 f x d   (gate rows, then up rows)
+ *   down     `experts` weights of d x f
+ *   x [t][d], ids [t][topk] as in qw_moe_sort, weights fp32 [t][topk] or NULL
+ *   y [t][d]
+ *   work: qw_moe_mlp_work_bytes(...) bytes, 16-byte aligned (QW_EWORK)
+ * block_rows is that of both weights.  Both products run on the 8-bit cores
+ * (see qw_block_gemm) with fp32 results: what they drop is far below the
+ * rounding of the hidden values to codes.
+ */
+int64_t qw_moe_mlp_work_bytes(int64_t t, int64_t topk, int64_t experts, int64_t d, int64_t f);
+int qw_moe_mlp(int block_rows, int64_t experts, int64_t d, int64_t f,
+               const uint8_t* gate_up, const float* gate_up_scales, const uint8_t* down,
+               const float* down_scales, int64_t t, int64_t topk, int x_type,
+               const void* x, int id_bytes, const void* ids, const float* weights,
+               int y_type, void* y, void* work, int64_t work_bytes, void* stream);
+
+/*
  * Diagnostic: which kernel family a call with these arguments would take
  * (1 = streaming/tiled fast kernel, 2 = block-per-group kernel, 3 = generic
  * kernel, 4 = matrix-core GEMV) or a negative status for invalid arguments.

@@ -15,7 +15,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqw.so")
-SOURCES = ["qw_api.hip", "quantize.hip", "gemv.hip", "gemm.hip", "gptq.hip"]
+SOURCES = ["qw_api.hip", "quantize.hip", "gemv.hip", "gemm.hip", "gptq.hip",
+           "block.hip", "block_gemm.hip", "moe.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -1,0 +1,133 @@
+// e4m3 codes with a scale per block of 128 values: device code shared by the
+// kernels that make or read them (block.hip, block_gemm.hip, moe.hip).
+#pragma once
+
+#include "qw_internal.h"
+
+namespace qw {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kTop = 448.0f;  // largest e4m3 value
+
+// A block's scale from its max|w|: IEEE fp32 division, 1 for a zero result.
+__device__ __forceinline__ float block_scale(float amax) {
+  const float s = amax / kTop;
+  return s == 0.0f ? 1.0f : s;
+}
+
+__device__ __forceinline__ float clip_top(float v) { return fminf(fmaxf(v, -kTop), kTop); }
+
+// Codes of 4 values already divided by their scale, first value in the low
+// byte.  The conversion rounds to nearest even; values are within +-448, so
+// it never saturates.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(clip_top(a), clip_top(b), 0, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(clip_top(c), clip_top(d), r, true);
+  return (uint32_t)r;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint16_t to_bf16(float v) {
+  return __builtin_bit_cast(uint16_t, (__bf16)v);  // round to nearest even
+}
+__device__ __forceinline__ uint32_t to_bf16x2(float a, float b) {
+  return (uint32_t)to_bf16(a) | (uint32_t)to_bf16(b) << 16;
+}
+
+// One element of either type.
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t* p) {
+  return __uint_as_float((uint32_t)*p << 16);
+}
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = to_bf16(v); }
+
+// 8 consecutive elements at a 16-byte aligned address.
+__device__ __forceinline__ void load8(const float* p, float v[8]) {
+  const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = a[i];
+    v[4 + i] = b[i];
+  }
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float v[8]) {
+  const u32x4 a = *(const u32x4*)p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(a[i]);
+    v[2 * i + 1] = bf16_hi(a[i]);
+  }
+}
+
+// Elements [j, j + 8) of a row of k, zero from k on; VEC: the row is 16-byte
+// aligned and k % 8 == 0, so the 8 are all there or none is.
+template <bool VEC, typename T>
+__device__ __forceinline__ void load8_of_row(const T* row, int64_t j, int64_t k, float v[8]) {
+  if constexpr (VEC) {
+    if (j < k) {
+      load8(row + j, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = j + i < k ? load1(row + j + i) : 0.0f;
+  }
+}
+
+// The same for a store.
+__device__ __forceinline__ void store8(float* p, const float v[8]) {
+  *(f32x4*)p = f32x4{v[0], v[1], v[2], v[3]};
+  *(f32x4*)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float v[8]) {
+  *(u32x4*)p = u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
+                     to_bf16x2(v[6], v[7])};
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store8_of_row(T* row, int64_t j, int64_t k, const float v[8]) {
+  if constexpr (VEC) {
+    if (j < k) store8(row + j, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i < k) store1(row + j + i, v[i]);
+  }
+}
+
+__device__ __forceinline__ float amax8(const float v[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  return m;
+}
+
+// Max over the aligned run of 16 lanes that this lane is in.
+__device__ __forceinline__ float max16(float m) {
+#pragma unroll
+  for (int h = 1; h < 16; h <<= 1) m = fmaxf(m, __shfl_xor(m, h));
+  return m;
+}
+
+// The codes of 8 values with scale s.
+__device__ __forceinline__ u32x2 codes8(const float v[8], float s) {
+  return u32x2{codes4(v[0] / s, v[1] / s, v[2] / s, v[3] / s),
+               codes4(v[4] / s, v[5] / s, v[6] / s, v[7] / s)};
+}
+
+// Thread blocks for `items` of work, `per` to a block: the kernels' loops take
+// what is beyond 2^22 blocks (a launch holds fewer than 2^32 threads).
+inline unsigned grid_for(int64_t items, int per) {
+  const int64_t blocks = (items + per - 1) / per;
+  return (unsigned)(blocks < (1 << 22) ? blocks : 1 << 22);
+}
+
+}  // namespace qw

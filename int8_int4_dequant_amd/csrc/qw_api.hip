@@ -446,6 +446,331 @@ int qw_gptq_quantize_pack(int bits, int64_t group, int64_t n, int64_t k, const f
                                               (hipStream_t)stream));
 }
 
+// ------------------------------------------------- block-scaled e4m3 codes
+
+}  // extern "C"
+
+namespace {
+
+bool type_ok(int type) { return type == QW_F32 || type == QW_BF16; }
+
+// block_rows and the sizes of `count` matrices of n x k (their code rows
+// included); `shape` is the status of sizes out of range.
+int check_block(int brows, int64_t count, int64_t n, int64_t k) {
+  if (brows != 1 && brows != QW_BLOCK) return QW_EARG;
+  if (!within(n, k) || !within(n, qw::pitch(k))) return QW_ESHAPE;
+  // n first rounded up to whole blocks, so that the number of scales fits too
+  if (!within(count, n) || !within(count * n, qw::pitch(k))) return QW_ESHAPE;
+  return QW_OK;
+}
+
+// x or y side of a product: m rows of n outputs and of k inputs.
+int check_rows(int64_t m, int64_t n, int64_t k) {
+  return within(m, n) && within(m, k) && within(m, qw::pitch(k)) ? QW_OK : QW_EM;
+}
+
+int check_moe(int64_t t, int64_t topk, int64_t d, int64_t rows) {
+  if (topk < 1) return QW_EARG;
+  if (!within(t, topk, QW_MOE_MAX_SLOTS)) return QW_ESHAPE;
+  if (rows < 0 || rows > QW_MOE_MAX_SLOTS) return QW_ESHAPE;
+  if (!within(d, 1) || !within(t, qw::pitch(d)) || !within(rows, qw::pitch(d)))
+    return QW_ESHAPE;
+  return QW_OK;
+}
+
+// A part of a work buffer, 256-byte aligned relative to its start.
+struct Carve {
+  int64_t at = 0;
+  int64_t take(int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  }
+};
+
+// A grouped product of checked arguments; exact: see BlockGemm.
+int grouped(int brows, int64_t experts, int64_t n, int64_t k, const uint8_t* codes,
+            const float* scales, int64_t rows, const uint8_t* xc, const float* xs,
+            const int32_t* offsets, int y_type, void* y, bool exact, void* stream) {
+  if (rows * n == 0) return QW_OK;
+  const qw::BlockGemm g = {brows, n, k, rows, codes, scales, -1, nullptr, xc, xs,
+                           y_type, y, exact};
+  return record(qw::launch_block_gemm_grouped(g, experts, offsets, (hipStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t qw_block_pitch(int64_t k) { return within(k, 1) ? qw::pitch(k) : -1; }
+
+int64_t qw_block_num_scales(int block_rows, int64_t n, int64_t k) {
+  if (check_block(block_rows, 1, n, k) != QW_OK) return -1;
+  return qw::block_scales(block_rows, n, k);
+}
+
+int qw_block_quantize(int block_rows, int64_t count, int64_t n, int64_t k, int type,
+                      const void* w, uint8_t* codes, float* scales, void* stream) {
+  int st = check_block(block_rows, count, n, k);
+  if (st != QW_OK) return st;
+  if (!type_ok(type)) return QW_EARG;
+  if (count * n * k == 0) return QW_OK;
+  if (!w || !codes || !scales) return QW_ENULL;
+  if (!qw::aligned(codes, 16)) return QW_EARG;
+  return record(qw::launch_block_quantize(block_rows, count, n, k, type, w, codes, scales,
+                                          (hipStream_t)stream));
+}
+
+int qw_block_quantize_swiglu(int64_t rows, int64_t f, int type, const void* h,
+                             const int32_t* used, uint8_t* codes, float* scales,
+                             void* stream) {
+  int st = check_block(1, 1, rows, f);
+  if (st != QW_OK) return st;
+  if (!within(rows, f, QW_MAX_ELEMENTS / 2)) return QW_ESHAPE;
+  if (!type_ok(type)) return QW_EARG;
+  if (rows * f == 0) return QW_OK;
+  if (!h || !codes || !scales) return QW_ENULL;
+  if (!qw::aligned(codes, 16)) return QW_EARG;
+  return record(qw::launch_block_quantize_swiglu(rows, f, type, h, used, codes, scales,
+                                                 (hipStream_t)stream));
+}
+
+int qw_block_unpack(int block_rows, int64_t count, int64_t n, int64_t k, const uint8_t* codes,
+                    const float* scales, float* out, void* stream) {
+  int st = check_block(block_rows, count, n, k);
+  if (st != QW_OK) return st;
+  if (count * n * k == 0) return QW_OK;
+  if (!codes || !scales || !out) return QW_ENULL;
+  if (!qw::aligned(codes, 16)) return QW_EARG;
+  return record(qw::launch_block_unpack(block_rows, count, n, k, codes, scales, out,
+                                        (hipStream_t)stream));
+}
+
+int qw_block_gemm(int block_rows, int64_t n, int64_t k, const uint8_t* codes,
+                  const float* scales, int64_t m, const uint8_t* x_codes,
+                  const float* x_scales, int y_type, void* y, void* stream) {
+  int st = check_block(block_rows, 1, n, k);
+  if (st != QW_OK) return st;
+  st = check_rows(m, n, k);
+  if (st != QW_OK) return st;
+  if (!type_ok(y_type)) return QW_EARG;
+  if (m * n == 0) return QW_OK;
+  if (!y || (k > 0 && (!codes || !scales || !x_codes || !x_scales))) return QW_ENULL;
+  if (!qw::aligned(codes, 16) || !qw::aligned(x_codes, 16)) return QW_EARG;
+  qw::BlockGemm g = {block_rows, n, k, m, codes, scales, -1, nullptr, x_codes, x_scales,
+                     y_type, y, y_type == QW_F32};
+  return record(qw::launch_block_gemm(g, (hipStream_t)stream));
+}
+
+int64_t qw_block_matmul_work_bytes(int64_t m, int64_t k) {
+  if (check_rows(m, 1, k) != QW_OK) return -1;
+  if (m <= qw::kBlockFusedMaxM) return 0;
+  Carve c;
+  c.take(m * qw::pitch(k));
+  c.take(qw::block_scales(1, m, k) * 4);
+  return c.at;
+}
+
+int qw_block_matmul(int block_rows, int64_t n, int64_t k, const uint8_t* codes,
+                    const float* scales, int64_t m, int x_type, const void* x, int y_type,
+                    void* y, void* work, int64_t work_bytes, void* stream) {
+  int st = check_block(block_rows, 1, n, k);
+  if (st != QW_OK) return st;
+  st = check_rows(m, n, k);
+  if (st != QW_OK) return st;
+  if (!type_ok(x_type) || !type_ok(y_type)) return QW_EARG;
+  if (m * n == 0) return QW_OK;
+  if (!y || (k > 0 && (!codes || !scales || !x))) return QW_ENULL;
+  if (!qw::aligned(codes, 16)) return QW_EARG;
+  qw::BlockGemm g = {block_rows, n, k, m, codes, scales, x_type, x, nullptr, nullptr,
+                     y_type, y, y_type == QW_F32};
+  if (m > qw::kBlockFusedMaxM) {
+    const int64_t need = qw_block_matmul_work_bytes(m, k);
+    if (need > 0 && (!work || work_bytes < need || !qw::aligned(work, 16))) return QW_EWORK;
+    Carve c;
+    uint8_t* xc = (uint8_t*)work + c.take(m * qw::pitch(k));
+    float* xs = (float*)((uint8_t*)work + c.take(0));
+    if (k > 0) {
+      const hipError_t e = qw::launch_block_quantize(1, 1, m, k, x_type, x, xc, xs,
+                                                     (hipStream_t)stream);
+      if (e != hipSuccess) return record(e);
+    }
+    g.x_type = -1;
+    g.x = nullptr;
+    g.xc = xc;
+    g.xs = xs;
+  }
+  return record(qw::launch_block_gemm(g, (hipStream_t)stream));
+}
+
+int qw_block_gemm_grouped(int block_rows, int64_t experts, int64_t n, int64_t k,
+                          const uint8_t* codes, const float* scales, int64_t rows,
+                          const uint8_t* x_codes, const float* x_scales,
+                          const int32_t* offsets, int y_type, void* y, void* stream) {
+  if (experts < 1 || experts > QW_MOE_MAX_EXPERTS) return QW_EARG;
+  int st = check_block(block_rows, experts, n, k);
+  if (st != QW_OK) return st;
+  if (rows < 0 || rows > QW_MOE_MAX_SLOTS) return QW_EM;
+  st = check_rows(rows, n, k);
+  if (st != QW_OK) return st;
+  if (!type_ok(y_type)) return QW_EARG;
+  if (rows * n == 0) return QW_OK;
+  if (!y || !offsets || (k > 0 && (!codes || !scales || !x_codes || !x_scales)))
+    return QW_ENULL;
+  if (!qw::aligned(codes, 16) || !qw::aligned(x_codes, 16)) return QW_EARG;
+  return grouped(block_rows, experts, n, k, codes, scales, rows, x_codes, x_scales, offsets,
+                 y_type, y, y_type == QW_F32, stream);
+}
+
+// ------------------------------------------ tokens sorted by expert and back
+
+int64_t qw_moe_sort_work_bytes(int64_t t, int64_t topk, int64_t experts) {
+  if (topk < 1 || experts < 1 || experts > QW_MOE_MAX_EXPERTS ||
+      !within(t, topk, QW_MOE_MAX_SLOTS))
+    return -1;
+  return qw::moe_sort_work_bytes(t * topk, experts);
+}
+
+int qw_moe_sort(int64_t t, int64_t topk, int64_t experts, int id_bytes, const void* ids,
+                int32_t* pos, int32_t* order, int32_t* offsets, void* work,
+                int64_t work_bytes, void* stream) {
+  if (topk < 1 || experts < 1 || experts > QW_MOE_MAX_EXPERTS) return QW_EARG;
+  if (id_bytes != 4 && id_bytes != 8) return QW_EARG;
+  if (!within(t, topk, QW_MOE_MAX_SLOTS)) return QW_ESHAPE;
+  if (!offsets || (t > 0 && (!ids || !pos))) return QW_ENULL;
+  const int64_t need = qw_moe_sort_work_bytes(t, topk, experts);
+  if (need > 0 && (!work || work_bytes < need || !qw::aligned(work, 4))) return QW_EWORK;
+  return record(qw::launch_moe_sort(t * topk, experts, id_bytes, ids, pos, order, offsets, work,
+                                    (hipStream_t)stream));
+}
+
+int qw_moe_gather(int64_t t, int64_t topk, int64_t d, int64_t rows, int type, const void* x,
+                  const int32_t* pos, void* xs, void* stream) {
+  int st = check_moe(t, topk, d, rows);
+  if (st != QW_OK) return st;
+  if (!type_ok(type)) return QW_EARG;
+  if (t * d == 0 || rows == 0) return QW_OK;
+  if (!x || !pos || !xs) return QW_ENULL;
+  return record(qw::launch_moe_gather(t, topk, d, rows, type, x, pos, xs, (hipStream_t)stream));
+}
+
+int qw_moe_gather_block(int64_t t, int64_t topk, int64_t d, int64_t rows, int type,
+                        const void* x, const int32_t* pos, uint8_t* codes, float* scales,
+                        void* stream) {
+  int st = check_moe(t, topk, d, rows);
+  if (st != QW_OK) return st;
+  if (!type_ok(type)) return QW_EARG;
+  if (t * d == 0 || rows == 0) return QW_OK;
+  if (!x || !pos || !codes || !scales) return QW_ENULL;
+  if (!qw::aligned(codes, 16)) return QW_EARG;
+  return record(qw::launch_moe_gather_block(t, topk, d, rows, type, x, pos, codes, scales,
+                                            (hipStream_t)stream));
+}
+
+int qw_moe_combine(int64_t t, int64_t topk, int64_t d, int64_t rows, int type, const void* ys,
+                   const int32_t* pos, const float* weights, int y_type, void* y,
+                   void* stream) {
+  int st = check_moe(t, topk, d, rows);
+  if (st != QW_OK) return st;
+  if (!type_ok(type) || !type_ok(y_type)) return QW_EARG;
+  if (t * d == 0) return QW_OK;
+  if (!pos || !y || (rows > 0 && !ys)) return QW_ENULL;
+  return record(qw::launch_moe_combine(t, topk, d, rows, type, ys, pos, weights, y_type, y,
+                                       (hipStream_t)stream));
+}
+
+int qw_moe_combine_backward(int64_t t, int64_t topk, int64_t d, int64_t rows, int type,
+                            const void* dy, const void* ys, const int32_t* pos,
+                            const float* weights, void* dys, float* dweights, void* stream) {
+  int st = check_moe(t, topk, d, rows);
+  if (st != QW_OK) return st;
+  if (!type_ok(type)) return QW_EARG;
+  if (t == 0) return QW_OK;
+  if (!pos || (d > 0 && !dy) || (dweights && rows > 0 && d > 0 && !ys)) return QW_ENULL;
+  if (!dys && !dweights) return QW_OK;
+  return record(qw::launch_moe_combine_backward(t, topk, d, rows, type, dy, ys, pos, weights,
+                                                dys, dweights, (hipStream_t)stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// The buffers of qw_moe_mlp in its work buffer.
+struct MlpWork {
+  int64_t pos, offsets, sort, xc, xs, h, hc, hs, ys, bytes;
+  MlpWork(int64_t t, int64_t topk, int64_t experts, int64_t d, int64_t f) {
+    const int64_t rows = t * topk;
+    Carve c;
+    pos = c.take(rows * 4);
+    offsets = c.take((experts + 1) * 4);
+    sort = c.take(qw::moe_sort_work_bytes(rows, experts));
+    xc = c.take(rows * qw::pitch(d));
+    xs = c.take(qw::block_scales(1, rows, d) * 4);
+    h = c.take(rows * 2 * f * 4);
+    hc = c.take(rows * qw::pitch(f));
+    hs = c.take(qw::block_scales(1, rows, f) * 4);
+    ys = c.take(rows * d * 4);
+    bytes = c.at;
+  }
+};
+
+int check_mlp(int64_t t, int64_t topk, int64_t experts, int64_t d, int64_t f) {
+  if (topk < 1 || experts < 1 || experts > QW_MOE_MAX_EXPERTS) return QW_EARG;
+  if (!within(t, topk, QW_MOE_MAX_SLOTS) || !within(d, 1) || !within(f, 2)) return QW_ESHAPE;
+  if (!within(t * topk, qw::pitch(d)) || !within(t * topk, 2 * qw::pitch(f))) return QW_ESHAPE;
+  return QW_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t qw_moe_mlp_work_bytes(int64_t t, int64_t topk, int64_t experts, int64_t d, int64_t f) {
+  if (check_mlp(t, topk, experts, d, f) != QW_OK) return -1;
+  return MlpWork(t, topk, experts, d, f).bytes;
+}
+
+int qw_moe_mlp(int block_rows, int64_t experts, int64_t d, int64_t f, const uint8_t* gate_up,
+               const float* gate_up_scales, const uint8_t* down, const float* down_scales,
+               int64_t t, int64_t topk, int x_type, const void* x, int id_bytes,
+               const void* ids, const float* weights, int y_type, void* y, void* work,
+               int64_t work_bytes, void* stream) {
+  int st = check_mlp(t, topk, experts, d, f);
+  if (st != QW_OK) return st;
+  st = check_block(block_rows, experts, 2 * f, d);
+  if (st != QW_OK) return st;
+  st = check_block(block_rows, experts, d, f);
+  if (st != QW_OK) return st;
+  if (!type_ok(x_type) || !type_ok(y_type) || (id_bytes != 4 && id_bytes != 8)) return QW_EARG;
+  if (t * d == 0) return QW_OK;
+  if (!x || !ids || !y || (f > 0 && (!gate_up || !gate_up_scales || !down || !down_scales)))
+    return QW_ENULL;
+  if (!qw::aligned(gate_up, 16) || !qw::aligned(down, 16)) return QW_EARG;
+  const MlpWork at(t, topk, experts, d, f);
+  if (!work || work_bytes < at.bytes || !qw::aligned(work, 16)) return QW_EWORK;
+  uint8_t* const b = (uint8_t*)work;
+  const int64_t rows = t * topk;
+  int32_t* const pos = (int32_t*)(b + at.pos);
+  int32_t* const offsets = (int32_t*)(b + at.offsets);
+  st = qw_moe_sort(t, topk, experts, id_bytes, ids, pos, nullptr, offsets, b + at.sort,
+                   at.xc - at.sort, stream);
+  if (st != QW_OK) return st;
+  st = qw_moe_gather_block(t, topk, d, rows, x_type, x, pos, b + at.xc, (float*)(b + at.xs),
+                           stream);
+  if (st != QW_OK) return st;
+  st = grouped(block_rows, experts, 2 * f, d, gate_up, gate_up_scales, rows, b + at.xc,
+               (const float*)(b + at.xs), offsets, QW_F32, b + at.h, false, stream);
+  if (st != QW_OK) return st;
+  st = qw_block_quantize_swiglu(rows, f, QW_F32, b + at.h, offsets + experts, b + at.hc,
+                                (float*)(b + at.hs), stream);
+  if (st != QW_OK) return st;
+  st = grouped(block_rows, experts, d, f, down, down_scales, rows, b + at.hc,
+               (const float*)(b + at.hs), offsets, QW_F32, b + at.ys, false, stream);
+  if (st != QW_OK) return st;
+  return qw_moe_combine(t, topk, d, rows, QW_F32, b + at.ys, pos, weights, y_type, y, stream);
+}
+
 // Which kernel family a call with these arguments would take (1 = fast,
 // 2 = block, 3 = generic, 4 = matrix-core GEMV; for op 5, 1 = GEMV and
 // 2 = GEMM; negative = invalid arguments).  Used by the tests to make sure

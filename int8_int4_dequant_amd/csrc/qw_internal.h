@@ -58,6 +58,60 @@ hipError_t launch_gptq_quantize_pack(const Mat& mt, const float* w, const double
                                      uint8_t* payload, float* scales, void* work,
                                      hipStream_t stream);
 
+// Block-scaled e4m3 (block.hip).  `brows` is 1 or QW_BLOCK; codes are 16-byte
+// aligned rows of pitch(k) bytes.
+inline int64_t pitch(int64_t k) { return (k + QW_BLOCK - 1) / QW_BLOCK * QW_BLOCK; }
+inline int64_t block_scales(int brows, int64_t n, int64_t k) {
+  return (n + brows - 1) / brows * (pitch(k) / QW_BLOCK);
+}
+hipError_t launch_block_quantize(int brows, int64_t count, int64_t n, int64_t k, int type,
+                                 const void* w, uint8_t* codes, float* scales,
+                                 hipStream_t stream);
+hipError_t launch_block_quantize_swiglu(int64_t rows, int64_t f, int type, const void* h,
+                                        const int32_t* used, uint8_t* codes, float* scales,
+                                        hipStream_t stream);
+hipError_t launch_block_unpack(int brows, int64_t count, int64_t n, int64_t k,
+                               const uint8_t* codes, const float* scales, float* out,
+                               hipStream_t stream);
+// Rows of float x up to which launch_block_gemm quantizes them itself.
+constexpr int kBlockFusedMaxM = 16;
+// One product.  x_type: QW_F32 or QW_BF16 (x, at most kBlockFusedMaxM rows) or
+// -1 (xc and xs).
+struct BlockGemm {
+  int brows;
+  int64_t n, k, m;
+  const uint8_t* codes;
+  const float* scales;
+  int x_type;
+  const void* x;
+  const uint8_t* xc;
+  const float* xs;
+  int y_type;
+  void* y;
+  bool exact;  // fp32 y: on the bf16 cores (only a grouped product may go without)
+};
+hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t stream);
+hipError_t launch_block_gemm_grouped(const BlockGemm& g, int64_t experts,
+                                     const int32_t* offsets, hipStream_t stream);
+
+// Tokens sorted by expert and back (moe.hip).
+int64_t moe_sort_work_bytes(int64_t slots, int64_t experts);
+hipError_t launch_moe_sort(int64_t slots, int64_t experts, int id_bytes, const void* ids,
+                           int32_t* pos, int32_t* order, int32_t* offsets, void* work,
+                           hipStream_t stream);
+hipError_t launch_moe_gather(int64_t t, int64_t topk, int64_t d, int64_t rows, int type,
+                             const void* x, const int32_t* pos, void* xs, hipStream_t stream);
+hipError_t launch_moe_gather_block(int64_t t, int64_t topk, int64_t d, int64_t rows, int type,
+                                   const void* x, const int32_t* pos, uint8_t* codes,
+                                   float* scales, hipStream_t stream);
+hipError_t launch_moe_combine(int64_t t, int64_t topk, int64_t d, int64_t rows, int type,
+                              const void* ys, const int32_t* pos, const float* weights,
+                              int y_type, void* y, hipStream_t stream);
+hipError_t launch_moe_combine_backward(int64_t t, int64_t topk, int64_t d, int64_t rows,
+                                       int type, const void* dy, const void* ys,
+                                       const int32_t* pos, const float* weights, void* dys,
+                                       float* dweights, hipStream_t stream);
+
 // Which kernel family a call takes (exposed for tests through qw_debug_path).
 enum Path { PATH_NONE = 0, PATH_FAST = 1, PATH_BLOCK = 2, PATH_GENERIC = 3, PATH_MATRIX = 4 };
 int quantize_path(const Mat& mt, const float* w, const uint8_t* payload);

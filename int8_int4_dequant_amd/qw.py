@@ -13,6 +13,7 @@ and returns a record shaped like the pages' ``pack`` result:
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -36,13 +37,26 @@ EXPORTS = ["qw_payload_bytes", "qw_num_scales", "qw_status_string", "qw_last_err
            "qw_matmul_noalloc",
            "qw_debug_path",
            "qw_gptq_hessian_work_bytes", "qw_gptq_hessian", "qw_gptq_factor_work_bytes",
-           "qw_gptq_factor", "qw_gptq_quantize_work_bytes", "qw_gptq_quantize_pack"]
+           "qw_gptq_factor", "qw_gptq_quantize_work_bytes", "qw_gptq_quantize_pack",
+           "qw_block_pitch", "qw_block_num_scales", "qw_block_quantize",
+           "qw_block_quantize_swiglu", "qw_block_unpack", "qw_block_gemm",
+           "qw_block_matmul_work_bytes", "qw_block_matmul", "qw_block_gemm_grouped",
+           "qw_moe_sort_work_bytes", "qw_moe_sort", "qw_moe_gather", "qw_moe_gather_block",
+           "qw_moe_combine", "qw_moe_combine_backward", "qw_moe_mlp_work_bytes", "qw_moe_mlp"]
 
 
 # Rows up to which qw_matmul runs the codes GEMV (QW_MATMUL_GEMV_MAX_M in qw.h).
 MATMUL_GEMV_MAX_M = 4
 # Bytes of the static scratch of qw_matmul_noalloc (QW_MATMUL_NOALLOC_MAX_BYTES).
 MATMUL_NOALLOC_MAX_BYTES = 32 << 20
+
+# Values per scale along a row of block-scaled e4m3 codes (QW_BLOCK).
+BLOCK = 128
+# QW_F32 and QW_BF16 (enum qw_type), by tensor type.
+TYPES = {torch.float32: 0, torch.bfloat16: 1}
+# Most experts and slots of the expert calls (QW_MOE_MAX_EXPERTS, QW_MOE_MAX_SLOTS).
+MOE_MAX_EXPERTS = 512
+MOE_MAX_SLOTS = 1 << 30
 
 
 class QwQuantDesc(ctypes.Structure):
@@ -137,6 +151,41 @@ def lib():
     L.qw_gptq_quantize_work_bytes.restype = i64
     L.qw_gptq_quantize_pack.argtypes = [i32, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp]
     L.qw_gptq_quantize_pack.restype = i32
+    L.qw_block_pitch.argtypes = [i64]
+    L.qw_block_pitch.restype = i64
+    L.qw_block_num_scales.argtypes = [i32, i64, i64]
+    L.qw_block_num_scales.restype = i64
+    L.qw_block_quantize.argtypes = [i32, i64, i64, i64, i32, vp, vp, vp, vp]
+    L.qw_block_quantize.restype = i32
+    L.qw_block_quantize_swiglu.argtypes = [i64, i64, i32, vp, vp, vp, vp, vp]
+    L.qw_block_quantize_swiglu.restype = i32
+    L.qw_block_unpack.argtypes = [i32, i64, i64, i64, vp, vp, vp, vp]
+    L.qw_block_unpack.restype = i32
+    L.qw_block_gemm.argtypes = [i32, i64, i64, vp, vp, i64, vp, vp, i32, vp, vp]
+    L.qw_block_gemm.restype = i32
+    L.qw_block_matmul_work_bytes.argtypes = [i64, i64]
+    L.qw_block_matmul_work_bytes.restype = i64
+    L.qw_block_matmul.argtypes = [i32, i64, i64, vp, vp, i64, i32, vp, i32, vp, vp, i64, vp]
+    L.qw_block_matmul.restype = i32
+    L.qw_block_gemm_grouped.argtypes = [i32, i64, i64, i64, vp, vp, i64, vp, vp, vp, i32, vp, vp]
+    L.qw_block_gemm_grouped.restype = i32
+    L.qw_moe_sort_work_bytes.argtypes = [i64, i64, i64]
+    L.qw_moe_sort_work_bytes.restype = i64
+    L.qw_moe_sort.argtypes = [i64, i64, i64, i32, vp, vp, vp, vp, vp, i64, vp]
+    L.qw_moe_sort.restype = i32
+    L.qw_moe_gather.argtypes = [i64, i64, i64, i64, i32, vp, vp, vp, vp]
+    L.qw_moe_gather.restype = i32
+    L.qw_moe_gather_block.argtypes = [i64, i64, i64, i64, i32, vp, vp, vp, vp, vp]
+    L.qw_moe_gather_block.restype = i32
+    L.qw_moe_combine.argtypes = [i64, i64, i64, i64, i32, vp, vp, vp, i32, vp, vp]
+    L.qw_moe_combine.restype = i32
+    L.qw_moe_combine_backward.argtypes = [i64, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp]
+    L.qw_moe_combine_backward.restype = i32
+    L.qw_moe_mlp_work_bytes.argtypes = [i64, i64, i64, i64, i64]
+    L.qw_moe_mlp_work_bytes.restype = i64
+    L.qw_moe_mlp.argtypes = [i32, i64, i64, i64, vp, vp, vp, vp, i64, i64, i32, vp, i32, vp, vp,
+                             i32, vp, vp, i64, vp]
+    L.qw_moe_mlp.restype = i32
     _lib = L
     return L
 
@@ -287,6 +336,95 @@ def qw_gptq_quantize_pack(bits, group, n, k, w, u, payload, scales, work, work_b
                           stream=None):
     return lib().qw_gptq_quantize_pack(bits, group, n, k, _ptr(w), _ptr(u), _ptr(payload),
                                        _ptr(scales), _ptr(work), work_bytes, _stream(stream))
+
+
+def qw_block_pitch(k):
+    return lib().qw_block_pitch(k)
+
+
+def qw_block_num_scales(block_rows, n, k):
+    return lib().qw_block_num_scales(block_rows, n, k)
+
+
+def qw_block_quantize(block_rows, count, n, k, type, w, codes, scales, stream=None):
+    return lib().qw_block_quantize(block_rows, count, n, k, type, _ptr(w), _ptr(codes),
+                                   _ptr(scales), _stream(stream))
+
+
+def qw_block_quantize_swiglu(rows, f, type, h, used, codes, scales, stream=None):
+    return lib().qw_block_quantize_swiglu(rows, f, type, _ptr(h), _ptr(used), _ptr(codes),
+                                          _ptr(scales), _stream(stream))
+
+
+def qw_block_unpack(block_rows, count, n, k, codes, scales, out, stream=None):
+    return lib().qw_block_unpack(block_rows, count, n, k, _ptr(codes), _ptr(scales), _ptr(out),
+                                 _stream(stream))
+
+
+def qw_block_gemm(block_rows, n, k, codes, scales, m, x_codes, x_scales, y_type, y, stream=None):
+    return lib().qw_block_gemm(block_rows, n, k, _ptr(codes), _ptr(scales), m, _ptr(x_codes),
+                               _ptr(x_scales), y_type, _ptr(y), _stream(stream))
+
+
+def qw_block_matmul_work_bytes(m, k):
+    return lib().qw_block_matmul_work_bytes(m, k)
+
+
+def qw_block_matmul(block_rows, n, k, codes, scales, m, x_type, x, y_type, y, work, work_bytes,
+                    stream=None):
+    return lib().qw_block_matmul(block_rows, n, k, _ptr(codes), _ptr(scales), m, x_type, _ptr(x),
+                                 y_type, _ptr(y), _ptr(work), work_bytes, _stream(stream))
+
+
+def qw_block_gemm_grouped(block_rows, experts, n, k, codes, scales, rows, x_codes, x_scales,
+                          offsets, y_type, y, stream=None):
+    return lib().qw_block_gemm_grouped(block_rows, experts, n, k, _ptr(codes), _ptr(scales), rows,
+                                       _ptr(x_codes), _ptr(x_scales), _ptr(offsets), y_type,
+                                       _ptr(y), _stream(stream))
+
+
+def qw_moe_sort_work_bytes(t, topk, experts):
+    return lib().qw_moe_sort_work_bytes(t, topk, experts)
+
+
+def qw_moe_sort(t, topk, experts, id_bytes, ids, pos, order, offsets, work, work_bytes,
+                stream=None):
+    return lib().qw_moe_sort(t, topk, experts, id_bytes, _ptr(ids), _ptr(pos), _ptr(order),
+                             _ptr(offsets), _ptr(work), work_bytes, _stream(stream))
+
+
+def qw_moe_gather(t, topk, d, rows, type, x, pos, xs, stream=None):
+    return lib().qw_moe_gather(t, topk, d, rows, type, _ptr(x), _ptr(pos), _ptr(xs),
+                               _stream(stream))
+
+
+def qw_moe_gather_block(t, topk, d, rows, type, x, pos, codes, scales, stream=None):
+    return lib().qw_moe_gather_block(t, topk, d, rows, type, _ptr(x), _ptr(pos), _ptr(codes),
+                                     _ptr(scales), _stream(stream))
+
+
+def qw_moe_combine(t, topk, d, rows, type, ys, pos, weights, y_type, y, stream=None):
+    return lib().qw_moe_combine(t, topk, d, rows, type, _ptr(ys), _ptr(pos), _ptr(weights),
+                                y_type, _ptr(y), _stream(stream))
+
+
+def qw_moe_combine_backward(t, topk, d, rows, type, dy, ys, pos, weights, dys, dweights,
+                            stream=None):
+    return lib().qw_moe_combine_backward(t, topk, d, rows, type, _ptr(dy), _ptr(ys), _ptr(pos),
+                                         _ptr(weights), _ptr(dys), _ptr(dweights),
+                                         _stream(stream))
+
+
+def qw_moe_mlp_work_bytes(t, topk, experts, d, f):
+    return lib().qw_moe_mlp_work_bytes(t, topk, experts, d, f)
+
+
+def qw_moe_mlp(block_rows, experts, d, f, gate_up, gate_up_scales, down, down_scales, t, topk,
+               x_type, x, id_bytes, ids, weights, y_type, y, work, work_bytes, stream=None):
+    return lib().qw_moe_mlp(block_rows, experts, d, f, _ptr(gate_up), _ptr(gate_up_scales),
+                            _ptr(down), _ptr(down_scales), t, topk, x_type, _ptr(x), id_bytes,
+                            _ptr(ids), _ptr(weights), y_type, _ptr(y), _ptr(work), work_bytes,
+                            _stream(stream))
 
 
 # -------------------------------------------------------- convenience layer
@@ -571,3 +709,383 @@ def gptq_quantize_pack(w, u, bits, group, stream=None):
 def gptq(w, h, bits, group, damp=0.01, stream=None):
     """The whole chain from an accumulated h: damping, factor, codes."""
     return gptq_quantize_pack(w, gptq_factor(h, damp, stream), bits, group, stream)
+
+
+# ------------------------------------------------- block-scaled e4m3 codes
+#
+# Records: ``{block_rows, shape, codes, scales}``, shape [n][k] (or
+# [experts][n][k]), codes float8_e4m3fn [.., n][pitch], scales fp32
+# [.., rows of blocks][pitch / 128].
+#
+# These calls run on the device that their tensors are on, and on its current
+# stream where none is given (`stream` is a keyword).
+
+
+def _rows_of_blocks(n, block_rows):
+    return (n + block_rows - 1) // block_rows
+
+
+def _pitch(k):
+    return (k + BLOCK - 1) // BLOCK * BLOCK
+
+
+def _type(t, what):
+    code = TYPES.get(t)
+    if code is None:
+        raise ValueError(f"{what} must be float32 or bfloat16, got {t}")
+    return code
+
+
+def _device_of(*ts):
+    """The one device that all tensors of a call are on (None entries aside)."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("libqw takes device tensors; a host tensor was passed")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and on {t.device}")
+    return dev
+
+
+def _run(dev, stream, call):
+    """call(stream) with ``dev`` as the current device (the library launches
+    on it)."""
+    if stream is not None and dev is not None and stream.device != dev:
+        raise ValueError(f"tensors on {dev} and a stream of {stream.device}")
+    if dev is None or dev.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(dev):
+        return call(_stream(stream))
+
+
+def _on_stream(f):
+    """``stream`` (a torch stream or a hipStream_t) as the current stream of
+    the whole call, so that what it allocates belongs to that stream too."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return f(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            return f(*args, stream=stream, **kwargs)
+    return call
+
+
+def _check_block(rec, what="record", dims=(2, 3)):
+    """Shape and block_rows of a block record whose codes and scales match
+    them; returns (experts, n, k, block_rows)."""
+    shape = [int(v) for v in rec["shape"]]
+    if len(shape) not in dims:
+        raise ValueError(f"{what}: shape {shape} has not {' or '.join(map(str, dims))} dimensions")
+    br = int(rec["block_rows"])
+    if br not in (1, BLOCK):
+        raise ValueError(f"{what}: block_rows must be 1 or {BLOCK}")
+    *lead, n, k = shape
+    e = lead[0] if lead else 1
+    kp = _pitch(k)
+    _check_tensor(rec["codes"], (torch.float8_e4m3fn, torch.uint8), e * n * kp, f"{what} codes")
+    _check_tensor(rec["scales"], torch.float32, e * _rows_of_blocks(n, br) * (kp // BLOCK),
+                  f"{what} scales")
+    return e, n, k, br
+
+
+def _empty_block(block_rows, shape, device):
+    *lead, n, k = shape
+    kp = _pitch(k)
+    return dict(block_rows=block_rows, shape=list(shape),
+                codes=torch.empty((*lead, n, kp), dtype=torch.float8_e4m3fn, device=device),
+                scales=torch.empty((*lead, _rows_of_blocks(n, block_rows), kp // BLOCK),
+                                   dtype=torch.float32, device=device))
+
+
+@_on_stream
+def block_quantize(w, block_rows=BLOCK, stream=None):
+    """Quantize a contiguous fp32 or bf16 device tensor [n][k] (or
+    [experts][n][k]) to e4m3 codes with a scale per block of ``block_rows`` x
+    128: 128 for weights, 1 for activations.  Returns a record."""
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3) or not w.is_contiguous():
+        raise ValueError("w must be a contiguous [n][k] or [experts][n][k] tensor")
+    t = _type(w.dtype, "w")
+    if block_rows not in (1, BLOCK):
+        raise ValueError(f"block_rows must be 1 or {BLOCK}")
+    dev = _device_of(w)
+    rec = _empty_block(block_rows, tuple(w.shape), dev)
+    *lead, n, k = rec["shape"]
+    _check(_run(dev, stream, lambda s: qw_block_quantize(
+        block_rows, lead[0] if lead else 1, n, k, t, w, rec["codes"], rec["scales"], s)),
+        "qw_block_quantize")
+    return rec
+
+
+@_on_stream
+def block_quantize_swiglu(h, used=None, stream=None):
+    """Record (1 x 128 blocks) of silu(gate) * up for h [rows][2 f], gate the
+    first f columns.  ``used``: a device int32 tensor of one element, the
+    number of rows there are; the others' codes are not written."""
+    if not isinstance(h, torch.Tensor) or h.dim() != 2 or h.shape[1] % 2 or not h.is_contiguous():
+        raise ValueError("h must be a contiguous [rows][2 f] tensor")
+    t = _type(h.dtype, "h")
+    if used is not None:
+        _check_tensor(used, torch.int32, 1, "used")
+    rows, f = h.shape[0], h.shape[1] // 2
+    dev = _device_of(h, used)
+    rec = _empty_block(1, (rows, f), dev)
+    _check(_run(dev, stream, lambda s: qw_block_quantize_swiglu(
+        rows, f, t, h, used, rec["codes"], rec["scales"], s)), "qw_block_quantize_swiglu")
+    return rec
+
+
+@_on_stream
+def block_unpack(rec, out=None, stream=None):
+    """The fp32 values that a record's codes stand for."""
+    e, n, k, br = _check_block(rec)
+    shape = tuple(int(v) for v in rec["shape"])
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=rec["codes"].device)
+    _check_tensor(out, torch.float32, e * n * k, "out", shape)
+    dev = _device_of(rec["codes"], rec["scales"], out)
+    _check(_run(dev, stream, lambda s: qw_block_unpack(br, e, n, k, rec["codes"], rec["scales"],
+                                                       out, s)), "qw_block_unpack")
+    return out
+
+
+def _output(out, shape, dtype, device, what="out"):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _type(out.dtype, what)
+    n = 1
+    for v in shape:
+        n *= v
+    return _check_tensor(out, out.dtype if dtype is None else dtype, n, what, shape)
+
+
+@_on_stream
+def block_gemm(rec, x, out=None, out_dtype=torch.float32, stream=None):
+    """y [m][n] = x . W^T of two records: ``rec`` the weight [n][k], ``x`` m
+    rows of k values with 1 x 128 blocks."""
+    _, n, k, br = _check_block(rec, "record", (2,))
+    _, m, kx, bx = _check_block(x, "x", (2,))
+    if kx != k or bx != 1:
+        raise ValueError(f"x must be a record of [m][{k}] with block_rows 1")
+    out = _output(out, (m, n), out_dtype, x["codes"].device)
+    dev = _device_of(rec["codes"], rec["scales"], x["codes"], x["scales"], out)
+    _check(_run(dev, stream, lambda s: qw_block_gemm(
+        br, n, k, rec["codes"], rec["scales"], m, x["codes"], x["scales"],
+        _type(out.dtype, "out"), out, s)), "qw_block_gemm")
+    return out
+
+
+@_on_stream
+def block_matmul(rec, x, out=None, out_dtype=None, work=None, stream=None):
+    """Float x [m][k] (fp32 or bf16, any m), quantized on the way with 1 x 128
+    blocks, times a record's weight; returns y [m][n] of x's type (or
+    ``out_dtype``)."""
+    _, n, k, br = _check_block(rec, "record", (2,))
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != k:
+        raise ValueError("x must be a contiguous [m][k] tensor")
+    m = x.shape[0]
+    xt = _type(x.dtype, "x")
+    _check_tensor(x, x.dtype, m * k, "x")
+    out = _output(out, (m, n), out_dtype or (x.dtype if out is None else out.dtype), x.device)
+    dev = _device_of(rec["codes"], rec["scales"], x, out, work)
+    need = lib().qw_block_matmul_work_bytes(m, k)
+    if work is None and need > 0:
+        work = _work(need, dev)
+    wb = _work_bytes(work)
+    _check(_run(dev, stream, lambda s: qw_block_matmul(
+        br, n, k, rec["codes"], rec["scales"], m, xt, x, _type(out.dtype, "out"), out, work, wb,
+        s)), "qw_block_matmul")
+    return out
+
+
+def _work_bytes(work):
+    if work is None:
+        return 0
+    if not isinstance(work, torch.Tensor) or not work.is_contiguous():
+        raise ValueError("work must be a contiguous tensor")
+    return work.numel() * work.element_size()
+
+
+@_on_stream
+def block_gemm_grouped(rec, x, offsets, out=None, out_dtype=torch.float32, stream=None):
+    """Rows sorted by expert times each expert's weight: ``rec`` [experts][n][k],
+    ``x`` a record of [rows][k] with 1 x 128 blocks, ``offsets`` device int32
+    [experts + 1] (moe_sort).  Rows that no expert has are left as they are
+    in ``out``."""
+    e, n, k, br = _check_block(rec, "record", (3,))
+    _, rows, kx, bx = _check_block(x, "x", (2,))
+    if kx != k or bx != 1:
+        raise ValueError(f"x must be a record of [rows][{k}] with block_rows 1")
+    _check_tensor(offsets, torch.int32, e + 1, "offsets")
+    out = _output(out, (rows, n), out_dtype, x["codes"].device)
+    dev = _device_of(rec["codes"], rec["scales"], x["codes"], x["scales"], offsets, out)
+    _check(_run(dev, stream, lambda s: qw_block_gemm_grouped(
+        br, e, n, k, rec["codes"], rec["scales"], rows, x["codes"], x["scales"], offsets,
+        _type(out.dtype, "out"), out, s)), "qw_block_gemm_grouped")
+    return out
+
+
+# ------------------------------------------ tokens sorted by expert and back
+
+
+_IDS = {torch.int32: 4, torch.int64: 8}
+
+
+def _check_ids(ids):
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.dtype not in _IDS \
+            or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 or int64 [t][topk] tensor")
+    return int(ids.shape[0]), int(ids.shape[1]), _IDS[ids.dtype]
+
+
+@_on_stream
+def moe_sort(ids, experts, order=True, work=None, stream=None):
+    """Stable sort of the slots of ids [t][topk] by expert; an id outside
+    [0, experts) takes its slot out.  Returns ``{pos, order, offsets}``: pos
+    [t][topk] the slot's row (-1 if out), order [t * topk] the row's slot (-1
+    behind the last row; None if ``order`` is false), offsets [experts + 1]."""
+    t, topk, nbytes = _check_ids(ids)
+    dev = _device_of(ids, work)
+    need = lib().qw_moe_sort_work_bytes(t, topk, experts)
+    if work is None and need > 0:
+        work = _work(need, dev)
+    wb = _work_bytes(work)
+    pos = torch.empty((t, topk), dtype=torch.int32, device=dev)
+    back = torch.empty(t * topk, dtype=torch.int32, device=dev) if order else None
+    offsets = torch.empty(max(0, experts) + 1, dtype=torch.int32, device=dev)
+    _check(_run(dev, stream, lambda s: qw_moe_sort(t, topk, experts, nbytes, ids, pos, back,
+                                                   offsets, work, wb, s)), "qw_moe_sort")
+    return dict(pos=pos, order=back, offsets=offsets)
+
+
+def _check_pos(route, t=None):
+    pos = route["pos"]
+    if not isinstance(pos, torch.Tensor) or pos.dim() != 2 or (t is not None and pos.shape[0] != t):
+        raise ValueError(f"pos must be an int32 [{'t' if t is None else t}][topk] tensor")
+    _check_tensor(pos, torch.int32, pos.numel(), "pos")
+    return pos, int(pos.shape[0]), int(pos.shape[1])
+
+
+def _check_matrix(x, what, rows=None, cols=None, dtype=None):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_contiguous() \
+            or (rows is not None and x.shape[0] != rows) or (cols is not None and x.shape[1] != cols):
+        raise ValueError(f"{what} must be a contiguous [{'rows' if rows is None else rows}]"
+                         f"[{'d' if cols is None else cols}] tensor")
+    if dtype is not None and x.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {x.dtype}")
+    return _type(x.dtype, what)
+
+
+@_on_stream
+def moe_gather(x, route, out=None, stream=None):
+    """Token rows x [t][d] into expert order, out [rows][d] (t * topk rows if
+    not given); a row without a slot is left as it is."""
+    xt = _check_matrix(x, "x")
+    t, d = x.shape
+    pos, _, topk = _check_pos(route, t)
+    if out is None:
+        out = torch.empty((t * topk, d), dtype=x.dtype, device=x.device)
+    _check_matrix(out, "out", None, d, x.dtype)
+    dev = _device_of(x, pos, out)
+    _check(_run(dev, stream, lambda s: qw_moe_gather(t, topk, d, out.shape[0], xt, x, pos, out,
+                                                     s)), "qw_moe_gather")
+    return out
+
+
+@_on_stream
+def moe_gather_block(x, route, rows=None, stream=None):
+    """Token rows x [t][d] into expert order as a record of [rows][d] (t *
+    topk rows if not given) with 1 x 128 blocks; the codes of a row without a
+    slot are not written."""
+    xt = _check_matrix(x, "x")
+    t, d = x.shape
+    pos, _, topk = _check_pos(route, t)
+    rows = t * topk if rows is None else int(rows)
+    if rows < 0:
+        raise ValueError("rows must not be negative")
+    dev = _device_of(x, pos)
+    rec = _empty_block(1, (rows, d), dev)
+    _check(_run(dev, stream, lambda s: qw_moe_gather_block(
+        t, topk, d, rows, xt, x, pos, rec["codes"], rec["scales"], s)), "qw_moe_gather_block")
+    return rec
+
+
+@_on_stream
+def moe_combine(ys, route, weights=None, out=None, out_dtype=None, stream=None):
+    """y [t][d] = sum over a token's slots of weights [t][topk] (fp32; all 1
+    if None) times their rows of ys [rows][d]; of ys' type or ``out_dtype``."""
+    yt = _check_matrix(ys, "ys")
+    rows, d = ys.shape
+    pos, t, topk = _check_pos(route)
+    if weights is not None:
+        _check_tensor(weights, torch.float32, t * topk, "weights", (t, topk))
+    out = _output(out, (t, d), out_dtype or (ys.dtype if out is None else out.dtype), ys.device)
+    dev = _device_of(ys, pos, weights, out)
+    _check(_run(dev, stream, lambda s: qw_moe_combine(
+        t, topk, d, rows, yt, ys, pos, weights, _type(out.dtype, "out"), out, s)),
+        "qw_moe_combine")
+    return out
+
+
+@_on_stream
+def moe_gather_backward(dxs, route, out=None, stream=None):
+    """Gradient of moe_gather: dx [t][d], each token's sum of its rows of dxs."""
+    return moe_combine(dxs, route, None, out, stream=stream)
+
+
+@_on_stream
+def moe_combine_backward(dy, ys, route, weights=None, dys=None, dweights=None, stream=None):
+    """Gradients of moe_combine for dy [t][d]: (dys [rows][d], dweights fp32
+    [t][topk]).  dy and ys have one type; rows of dys without a slot are left
+    as they are."""
+    yt = _check_matrix(ys, "ys")
+    rows, d = ys.shape
+    pos, t, topk = _check_pos(route)
+    _check_matrix(dy, "dy", t, d, ys.dtype)
+    if weights is not None:
+        _check_tensor(weights, torch.float32, t * topk, "weights", (t, topk))
+    if dys is None:
+        dys = torch.empty_like(ys)
+    _check_matrix(dys, "dys", rows, d, ys.dtype)
+    if dweights is None:
+        dweights = torch.empty((t, topk), dtype=torch.float32, device=dy.device)
+    _check_tensor(dweights, torch.float32, t * topk, "dweights", (t, topk))
+    dev = _device_of(dy, ys, pos, weights, dys, dweights)
+    _check(_run(dev, stream, lambda s: qw_moe_combine_backward(
+        t, topk, d, rows, yt, dy, ys, pos, weights, dys, dweights, s)),
+        "qw_moe_combine_backward")
+    return dys, dweights
+
+
+@_on_stream
+def moe_mlp(gate_up, down, x, ids, weights=None, out=None, out_dtype=None, work=None,
+            stream=None):
+    """A gated expert MLP in one call: x [t][d] (fp32 or bf16), ids [t][topk],
+    weights fp32 [t][topk]; ``gate_up`` a record of [experts][2 f][d] (gate
+    rows, then up rows), ``down`` of [experts][d][f].  y [t][d] of x's type or
+    ``out_dtype``."""
+    e, f2, d, br = _check_block(gate_up, "gate_up", (3,))
+    ed, dd, f, bd = _check_block(down, "down", (3,))
+    if ed != e or dd != d or f2 != 2 * f or bd != br:
+        raise ValueError("gate_up must be [experts][2 f][d] and down [experts][d][f], with the "
+                         "same block_rows")
+    t, topk, nbytes = _check_ids(ids)
+    xt = _check_matrix(x, "x", t, d)
+    if weights is not None:
+        _check_tensor(weights, torch.float32, t * topk, "weights", (t, topk))
+    out = _output(out, (t, d), out_dtype or (x.dtype if out is None else out.dtype), x.device)
+    dev = _device_of(gate_up["codes"], gate_up["scales"], down["codes"], down["scales"], x, ids,
+                     weights, out, work)
+    need = lib().qw_moe_mlp_work_bytes(t, topk, e, d, f)
+    if work is None and need > 0:
+        work = _work(need, dev)
+    wb = _work_bytes(work)
+    _check(_run(dev, stream, lambda s: qw_moe_mlp(
+        br, e, d, f, gate_up["codes"], gate_up["scales"], down["codes"], down["scales"], t, topk,
+        xt, x, nbytes, ids, weights, _type(out.dtype, "out"), out, work, wb, s)), "qw_moe_mlp")
+    return out
