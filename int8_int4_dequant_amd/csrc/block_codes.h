@@ -48,6 +48,12 @@ __device__ __forceinline__ float load1(const uint16_t* p) {
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = to_bf16(v); }
 
+// 4 consecutive elements, aligned to their size.
+__device__ __forceinline__ void store4(float* p, f32x4 v) { *(f32x4*)p = v; }
+__device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
+  *(u32x2*)p = u32x2{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3])};
+}
+
 // 8 consecutive elements at a 16-byte aligned address.
 __device__ __forceinline__ void load8(const float* p, float v[8]) {
   const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
