@@ -43,7 +43,7 @@ struct GemmArgs {
   int kb;             // blocks along k
   int64_t nb;         // rows of scales of one weight
   int64_t tiles_m, tiles;
-  int s_vec;          // 4 scales of a row may be loaded as one
+  int64_t chunks;     // stream kernel: blocks that share the weight rows of one tile of x
   int y_vec;          // 4 outputs of a row at a time may be stored as one
 };
 
@@ -87,8 +87,22 @@ __device__ __forceinline__ f32x4 dot128(const Frag<true>& a, const Frag<true>& b
   return d;
 }
 
+// Two products with the same weight fragment, their steps in turn.
+__device__ __forceinline__ void dot128x2(const Frag<false>& a, const Frag<false>* b, f32x4* d) {
+  d[0] = mfma128(a.v, b[0].v);
+  d[1] = mfma128(a.v, b[1].v);
+}
+__device__ __forceinline__ void dot128x2(const Frag<true>& a, const Frag<true>* b, f32x4* d) {
+  d[0] = d[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      d[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b[u].v[i], d[u], 0, 0, 0);
+}
+
 __device__ __forceinline__ i32x8 fragment(const uint8_t* p) {
-  const u32x4 lo = *(const u32x4*)p, hi = *(const u32x4*)(p + 64);
+  const u32x4_la lo = *(const u32x4_la*)p, hi = *(const u32x4_la*)(p + 64);
   return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w,
                (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
@@ -126,46 +140,13 @@ __device__ __forceinline__ bool grouped_tile(const GemmArgs& a, int64_t tm, int 
   return false;
 }
 
-// The x fragment of one lane from float values: 32 values of token row p (its
-// 1 x 128 block at j), quantized with the block's scale, which the 4 lanes of
-// the token find together.
-template <bool VEC, typename T>
-__device__ __forceinline__ i32x8 quantized_fragment(const T* row, int64_t j, int64_t k, int q,
-                                                    bool have, float& s) {
-  float v[4][8];
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t at = j + (i >> 1) * 64 + 16 * q + (i & 1) * 8;
-    if (have) {
-      load8_of_row<VEC>(row, at, k, v[i]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[i][c] = 0.0f;
-    }
-    m = fmaxf(m, amax8(v[i]));
-  }
-  m = fmaxf(m, __shfl_xor(m, 16));
-  m = fmaxf(m, __shfl_xor(m, 32));
-  s = block_scale(m);
-  i32x8 f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const u32x2 c = codes8(v[i], s);
-    f[2 * i] = (int)c.x;
-    f[2 * i + 1] = (int)c.y;
-  }
-  return f;
-}
-
 template <typename XT> struct is_codes { static constexpr bool value = false; };
 template <> struct is_codes<uint8_t> { static constexpr bool value = true; };
 
 // A block computes 16 NT weight rows x 16 MT tokens; its WV waves take every
 // WV-th block of k, straight from memory into registers, and add their sums
 // through LDS.
-template <int NT, int MT, int WV, bool EXACT, bool BROWS1, bool GROUPED, bool VEC, typename XT,
-          typename YT>
+template <int NT, int MT, int WV, bool EXACT, bool BROWS1, bool GROUPED, typename YT>
 __global__ __launch_bounds__(WV * 64) void gemm_direct(GemmArgs a) {
   constexpr int BN = 16 * NT, BM = 16 * MT, LD = BN + 4;
   __shared__ float part[WV][BM][LD];
@@ -188,20 +169,13 @@ __global__ __launch_bounds__(WV * 64) void gemm_direct(GemmArgs a) {
       for (int c = 0; c < 4; ++c)
         wsp[i][c] = BROWS1 ? ws + min(n0 + 16 * i + 4 * q + c, a.n - 1) * a.kb
                            : ws + n0 / QW_BLOCK * a.kb;
-    const XT* xp[MT];
+    const uint8_t* xp[MT];
     const float* sxp[MT];
-    bool have[MT];
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       const int64_t row = min(m0 + 16 * j + r, end - 1);
-      have[j] = m0 + 16 * j + r < end;
-      if constexpr (is_codes<XT>::value) {
-        xp[j] = (const XT*)a.x + row * a.kp + q * 16;
-        sxp[j] = a.xs + row * a.kb;
-      } else {
-        xp[j] = (const XT*)a.x + row * a.k;
-        sxp[j] = nullptr;
-      }
+      xp[j] = (const uint8_t*)a.x + row * a.kp + q * 16;
+      sxp[j] = a.xs + row * a.kb;
     }
     f32x4 acc[NT][MT] = {};
     for (int b = wave; b < a.kb; b += WV) {
@@ -210,15 +184,8 @@ __global__ __launch_bounds__(WV * 64) void gemm_direct(GemmArgs a) {
       for (int i = 0; i < NT; ++i) wf[i] = Frag<EXACT>(fragment(wp[i] + (int64_t)b * QW_BLOCK));
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        float sx;
-        i32x8 xc;
-        if constexpr (is_codes<XT>::value) {
-          xc = fragment(xp[j] + (int64_t)b * QW_BLOCK);
-          sx = sxp[j][b];
-        } else {
-          xc = quantized_fragment<VEC>(xp[j], (int64_t)b * QW_BLOCK, a.k, q, have[j], sx);
-        }
-        const Frag<EXACT> xf(xc);
+        const float sx = sxp[j][b];
+        const Frag<EXACT> xf(fragment(xp[j] + (int64_t)b * QW_BLOCK));
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           const f32x4 d = dot128(wf[i], xf);
@@ -246,7 +213,7 @@ __global__ __launch_bounds__(WV * 64) void gemm_direct(GemmArgs a) {
   }
 }
 
-template <int NT, int MT, int WV, bool GROUPED, bool VEC, typename XT>
+template <int NT, int MT, int WV, bool GROUPED>
 hipError_t run_direct(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   constexpr int BN = 16 * NT, BM = 16 * MT;
   a.tiles_m = GROUPED ? std::min(a.m, (a.m + a.experts * (int64_t)(BM - 1)) / BM)
@@ -255,8 +222,8 @@ hipError_t run_direct(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   // a launch holds fewer than 2^32 threads: the kernel's loop takes the rest
   const unsigned grid = (unsigned)std::min<int64_t>(a.tiles, 1 << 21);
   auto go = [&](auto exact, auto brows1, auto y) {
-    gemm_direct<NT, MT, WV, decltype(exact)::value, decltype(brows1)::value, GROUPED, VEC, XT,
-                decltype(y)><<<grid, WV * 64, 0, stream>>>(a);
+    gemm_direct<NT, MT, WV, decltype(exact)::value, decltype(brows1)::value, GROUPED, decltype(y)>
+        <<<grid, WV * 64, 0, stream>>>(a);
   };
   using std::true_type;
   using std::false_type;
@@ -303,9 +270,17 @@ __device__ __forceinline__ void copy_to_lds(i32x4 buffer, uint32_t voff, uint32_
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :: "s"(lds), "v"(voff), "s"(buffer), "s"(soff) : "memory");
 }
-// This wave's copies and LDS accesses are done, and so are the block's.
+// The same, 4 bytes a lane.
+__device__ __forceinline__ void copy4_to_lds(i32x4 buffer, uint32_t voff, uint32_t soff,
+                                             uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :: "s"(lds), "v"(voff), "s"(buffer), "s"(soff) : "memory");
+}
+// This wave's copies but the LEFT newest, and its LDS accesses, are done, and
+// so are the block's.
+template <int LEFT>
 __device__ __forceinline__ void landed() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "i"(LEFT) : "memory");
 }
 
 __device__ __forceinline__ i32x8 lds_fragment(const uint8_t* lds, int row, int q) {
@@ -331,17 +306,18 @@ __device__ __forceinline__ void tile_place(int64_t block, int64_t tiles, int64_t
   tm = band * 8 + in_band - tn * height;
 }
 
-template <int NF, int MF, bool EXACT, bool BROWS1, bool GROUPED, typename YT>
+template <int NF, int MF, int STAGES, bool EXACT, bool BROWS1, bool GROUPED, typename YT>
 __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
   constexpr int BN = 32 * NF, BM = 64 * MF, ROWS = BN + BM;
   constexpr int SEGS = ROWS / 8 / kTileWaves;  // 8-row pieces of a wave
   static_assert(QW_BLOCK % (16 * NF) == 0, "a wave's weight rows lie in one 128 x 128 block");
   static_assert(ROWS / 8 % kTileWaves == 0 && MF % 2 == 0, "whole pieces and pairs");
-  __shared__ __align__(1024) uint8_t lds[2][ROWS * 128];
   // scales of 4 blocks of k at a time (a scale's line of memory holds its
   // row's next ones), of the tile's tokens and then of its rows of blocks
-  constexpr int WROWS = BROWS1 ? BN : 2;
-  __shared__ __align__(16) float scales[2][4][BM + WROWS];
+  constexpr int SROWS = BM + (BROWS1 ? BN : 64);
+  static_assert(SROWS / 64 <= kTileWaves, "64 rows of scales a wave");
+  __shared__ __align__(1024) uint8_t lds[STAGES][ROWS * 128];
+  __shared__ __align__(16) float scales[2][4][SROWS];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wm = (wave & 3) * 16 * MF, wn = (wave >> 2) * 16 * NF;
@@ -356,10 +332,12 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
                                (uint32_t)(min(a.n - n0, (int64_t)BN) * a.kp));
   const i32x4 xbuf = buffer_of((const uint8_t*)a.x + m0 * a.kp, (uint32_t)((end - m0) * a.kp));
   const float* ws = a.scales + expert * a.nb * a.kb;
-  const int t = threadIdx.x;
-  const float* my_scales =
-      t < BM ? a.xs + min(m0 + t, end - 1) * a.kb
-             : ws + (BROWS1 ? min(n0 + t - BM, a.n - 1) : min(n0 / QW_BLOCK + t - BM, a.nb - 1)) * a.kb;
+  const int64_t srow = BROWS1 ? n0 : n0 / QW_BLOCK;
+  const i32x4 sbuf = wave * 64 < BM
+      ? buffer_of(a.xs + m0 * a.kb, (uint32_t)((end - m0) * a.kb * 4))
+      : buffer_of(ws + srow * a.kb,
+                  (uint32_t)(min(a.nb - srow, (int64_t)(BROWS1 ? BN : 2)) * a.kb * 4));
+  const uint32_t soff = (uint32_t)(wave * 64 + lane - (wave * 64 < BM ? 0 : BM)) * a.kb * 4;
   uint32_t voff[SEGS];
 #pragma unroll
   for (int s = 0; s < SEGS; ++s) {
@@ -368,32 +346,26 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
     voff[s] = (uint32_t)(row < BN ? row : row - BN) * kp + c * 16;
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0];
-  auto fetch = [&](int b, int buf) {
-#pragma unroll
-    for (int s = 0; s < SEGS; ++s) {
-      const int seg = wave + kTileWaves * s;
-      copy_to_lds(seg * 8 < BN ? wbuf : xbuf, voff[s], (uint32_t)b * 128,
-                  lds0 + buf * (ROWS * 128) + seg * 1024);
-    }
+  const uint32_t lds1 =
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&scales[0][0][0];
+  // Piece s of block b.  Behind the last block there is nothing to read, but the
+  // copy is issued all the same (as zeros, from an empty buffer): a branch
+  // would part the products from the scaling that runs beside them.
+  auto fetch = [&](int b, int buf, int s) {
+    i32x4 from = s < BN / 64 ? wbuf : xbuf;
+    from.z = b < a.kb ? from.z : 0;
+    const int seg = wave + kTileWaves * s;
+    copy_to_lds(from, voff[s], (uint32_t)b * 128, lds0 + buf * (ROWS * 128) + seg * 1024);
   };
   f32x4 acc[NF][MF] = {};
   if (a.kb > 0) {
-    float s4[4];
-    auto load_scales = [&](int b) {
-      if (t >= BM + WROWS) return;
-      if (a.s_vec) {
-        const f32x4 v = *(const f32x4*)(my_scales + b);
+    auto fetch_scales = [&](int b) {  // of the 4 blocks from b on
+      if (wave < SROWS / 64) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s4[c] = v[c];
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) s4[c] = my_scales[min(b + c, a.kb - 1)];
+        for (int c = 0; c < 4; ++c)
+          copy4_to_lds(sbuf, soff, (uint32_t)(b + c) * 4,
+                       lds1 + (((b >> 2) & 1) * 4 + c) * (SROWS * 4) + wave * 256);
       }
-    };
-    auto keep_scales = [&](int b) {
-      if (t >= BM + WROWS) return;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) scales[(b >> 2) & 1][c][t] = s4[c];
     };
     // The scales that block b's products are multiplied with: read from LDS
     // with the first fragments, joined behind the first products.
@@ -404,49 +376,54 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
 #pragma unroll
       for (int j = 0; j < MF; ++j) sx[j] = sc[wm + 16 * j + r];
     };
-    load_scales(0);
-    fetch(0, 0);
-    keep_scales(0);
-    landed();
-    if (a.kb > 1) fetch(1, 1);
+    fetch_scales(0);
+#pragma unroll
+    for (int c = 0; c < STAGES - 1; ++c)
+#pragma unroll
+      for (int p = 0; p < SEGS; ++p)
+        fetch(c, c, p);
+    landed<0>();
     take_scales(0);
+    i32x8 xr[MF];    // token fragments as they are read, and as the products take them
     Frag<EXACT> xf[MF];
 #pragma unroll
-    for (int j = 0; j < MF; ++j)
-      xf[j] = Frag<EXACT>(lds_fragment(lds[0] + (BN + wm) * 128, 16 * j + r, q));
-    i32x8 next = lds_fragment(lds[0] + wn * 128, r, q);
+    for (int j = 0; j < MF; ++j) xr[j] = lds_fragment(lds[0] + (BN + wm) * 128, 16 * j + r, q);
+    xf[0] = Frag<EXACT>(xr[0]);
+    xf[1] = Frag<EXACT>(xr[1]);
+    i32x8 wr = lds_fragment(lds[0] + wn * 128, r, q);  // and the weight fragment
+    Frag<EXACT> wf(wr);
     // a pair of products is scaled and added while the next pair runs on the
     // matrix cores: d with the scales ps (and psw) is the last pair
     f32x4 d[2] = {}, psw = {};
     float ps[2] = {};
+    int buf = 0;  // b % STAGES
     for (int b = 0; b < a.kb; ++b) {
-      const int buf = b & 1;
       const uint8_t* wl = lds[buf] + wn * 128;
-      const bool more = (b & 3) == 0 && b + 4 < a.kb;
-      if (more) load_scales(b + 4);
+      const int buf1 = buf + 1 < STAGES ? buf + 1 : 0;    // of block b + 1
+      const int buf2 = buf > 0 ? buf - 1 : STAGES - 1;    // of block b + STAGES - 1
+      if ((b & 3) == 0 && b + 4 < a.kb) fetch_scales(b + 4);
       f32x4 sw4 = {};
 #pragma unroll
       for (int i = 0; i < NF; ++i) {
-        const Frag<EXACT> wf(next);
         if constexpr (BROWS1) sw4 = *(const f32x4*)&scales[(b >> 2) & 1][b & 3][BM + wn + 16 * i + 4 * q];
         if (i + 1 < NF) {
-          next = lds_fragment(wl, 16 * (i + 1) + r, q);
+          wr = lds_fragment(wl, 16 * (i + 1) + r, q);
         } else {
           // The wave holds all that it needs of this buffer: once every wave
-          // does, it takes the copy after next; and the other buffer is whole.
-          landed();
-          if (more) keep_scales(b + 4);  // these have landed too
-          if (b + 2 < a.kb) fetch(b + 2, buf);
-          next = lds_fragment(lds[buf ^ 1] + wn * 128, r, q);
+          // does, the next step fills it again; and the next buffer is whole.
+          // Scales of other blocks that are on their way only make the wait
+          // longer: they are older than the copies it leaves.
+          landed<(STAGES - 2) * SEGS>();
+          wr = lds_fragment(lds[buf1] + wn * 128, r, q);
         }
 #pragma unroll
         for (int j = 0; j < MF; j += 2) {
           f32x4 e[2];
+          dot128x2(wf, &xf[j], e);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            e[u] = dot128(wf, xf[j + u]);
             if (i == NF - 1)
-              xf[j + u] = Frag<EXACT>(lds_fragment(lds[buf ^ 1] + (BN + wm) * 128, 16 * (j + u) + r, q));
+              xr[j + u] = lds_fragment(lds[buf1] + (BN + wm) * 128, 16 * (j + u) + r, q);
           }
           f32x4* to = j > 0 ? &acc[i][j - 2] : &acc[i > 0 ? i - 1 : NF - 1][MF - 2];
 #pragma unroll
@@ -456,11 +433,28 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
               to[u][c] = __builtin_fmaf(d[u][c], BROWS1 ? ps[u] * psw[c] : ps[u], to[u][c]);
             asm volatile("" : "+v"(to[u]));  // here, not after all the products
           }
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            __builtin_amdgcn_sched_group_barrier(0x8, EXACT ? 4 : 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x2, (BROWS1 ? 8 : 4) + (EXACT ? 8 : 0), 0);
+          // what the next pair takes
+          if (j + 2 < MF) {
+            if (i == 0) {
+              xf[j + 2] = Frag<EXACT>(xr[j + 2]);
+              xf[j + 3] = Frag<EXACT>(xr[j + 3]);
+            }
+          } else {
+            wf = Frag<EXACT>(wr);
+            if (i == NF - 1) {
+              xf[0] = Frag<EXACT>(xr[0]);
+              xf[1] = Frag<EXACT>(xr[1]);
+            }
           }
+#pragma unroll
+          for (int u = 0; u < (EXACT ? 8 : 2); ++u) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x2, EXACT ? 5 : BROWS1 ? 8 : 4, 0);
+          }
+          // the next block's copies, a piece with every pair: all at once they
+          // would hold up the reads behind them
+          if (i * (MF / 2) + j / 2 < SEGS)
+            fetch(b + STAGES - 1, buf2, i * (MF / 2) + j / 2);
           __builtin_amdgcn_sched_barrier(0);
           if (i == 0 && j == 0) {
 #pragma unroll
@@ -475,6 +469,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
           if (i == NF - 1 && j + 2 == MF) take_scales(b + 1);
         }
       }
+      buf = buf1;
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -502,16 +497,15 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
   }
 }
 
-template <int NF, int MF, bool GROUPED>
+template <int NF, int MF, int STAGES, bool GROUPED>
 hipError_t run_tiled(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   constexpr int BN = 32 * NF, BM = 64 * MF;
   a.tiles_m = GROUPED ? std::min(a.m, (a.m + a.experts * (int64_t)(BM - 1)) / BM)
                       : (a.m + BM - 1) / BM;
   a.tiles = a.tiles_m * ((a.n + BN - 1) / BN);
-  a.s_vec = a.kb % 4 == 0 && aligned(a.xs, 16) && aligned(a.scales, 16);
   a.y_vec = g.n % 4 == 0 && aligned(g.y, g.y_type == QW_BF16 ? 8 : 16);
   auto go = [&](auto exact, auto brows1, auto y) {
-    gemm_tiled<NF, MF, decltype(exact)::value, decltype(brows1)::value, GROUPED, decltype(y)>
+    gemm_tiled<NF, MF, STAGES, decltype(exact)::value, decltype(brows1)::value, GROUPED, decltype(y)>
         <<<(unsigned)a.tiles, kTileWaves * 64, 0, stream>>>(a);
   };
   using std::true_type;
@@ -524,6 +518,191 @@ hipError_t run_tiled(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   else if constexpr (GROUPED)
     one ? go(false_type{}, true_type{}, 0.0f) : go(false_type{}, false_type{}, 0.0f);
   return hipGetLastError();
+}
+
+// ------------------------------------------------------------ stream kernel
+//
+// For up to 16 rows of x (or of x per expert): bound by reading the weight
+// once.  Each of a block's WV waves owns KPW consecutive blocks of k.  It
+// quantizes (or loads) its part of x once, keeps it in registers, and streams
+// its part of 16 weight rows after 16 weight rows past it; a weight fragment
+// is replaced by a later one as soon as its product is issued, so that RING
+// fragments (2 KiB each) are always on their way.  The waves' sums meet in
+// LDS, once per 16 rows.  Float x costs each block one pass over its own rows
+// of x instead of a launch.
+
+// This wave's part of float x as fragments: 16 lanes quantize a block of k of a
+// token, as quantize_rows does, 4 tokens and 2 blocks at a time; the codes
+// change lanes through 4 KiB of LDS of the wave's own.
+template <int KPW, bool VEC, typename T>
+__device__ __forceinline__ void quantize_part(const GemmArgs& a, int64_t m0, int64_t end, int k0,
+                                              uint8_t (*lds)[16][128], float (*scale)[16],
+                                              int lane, i32x8* xf, float* sx) {
+  const int r = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int g = 0; g < KPW; g += 2) {
+    constexpr int W = 2;
+    for (int64_t row = m0 + q; row - q < end; row += 4) {
+      float v[W][8];
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const int64_t j = (int64_t)(k0 + g + i) * QW_BLOCK + r * 8;
+        load8_of_row<VEC>((const T*)a.x + min(row, end - 1) * a.k, j, a.k, v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const float s = block_scale(max16(amax8(v[i])));
+        *(u32x2_la*)&lds[i][(int)(row - m0)][r * 8] = codes8(v[i], s);
+        scale[i][(int)(row - m0)] = s;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      xf[g + i] = fragment(&lds[i][r][q * 16]);
+      sx[g + i] = scale[i][r];
+    }
+  }
+}
+
+template <int KPW, int WV, bool EXACT, bool BROWS1, bool GROUPED, bool VEC, typename XT,
+          typename YT>
+__global__ __launch_bounds__(WV * 64) void gemm_stream(GemmArgs a) {
+  __shared__ __align__(16) float part[2][WV][16][20];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int64_t chunk = blockIdx.x / a.tiles_m;
+  int64_t m0 = blockIdx.x % a.tiles_m * 16, end = min(m0 + 16, a.m);
+  int expert = 0;
+  if (GROUPED && !grouped_tile(a, blockIdx.x % a.tiles_m, 16, expert, m0, end)) return;
+  const int64_t tiles_n = (a.n + 15) / 16;
+  const int k0 = wave * KPW;
+  const uint8_t* wc = a.codes + expert * a.n * a.kp + q * 16;
+  const float* ws = a.scales + expert * a.nb * a.kb;
+  int koff[KPW];  // byte offset of this wave's blocks of k; the last one again behind the end
+#pragma unroll
+  for (int i = 0; i < KPW; ++i) koff[i] = min(k0 + i, a.kb - 1) * QW_BLOCK;
+  constexpr int RING = KPW > 8 ? KPW / 2 : KPW;  // weight fragments on their way
+  i32x8 w[RING];
+  // scales of a tile: of the wave's blocks one per lane, or 4 rows' per lane
+  float sw[BROWS1 ? KPW : 1][4];
+  auto load = [&](int64_t tile, int i) {
+    w[i % RING] = fragment(wc + min(tile * 16 + r, a.n - 1) * a.kp + koff[i]);
+  };
+  auto load_scales = [&](int64_t tile) {
+    if constexpr (BROWS1) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float* row = ws + min(tile * 16 + 4 * q + c, a.n - 1) * a.kb;
+#pragma unroll
+        for (int i = 0; i < KPW; ++i) sw[i][c] = row[min(k0 + i, a.kb - 1)];
+      }
+    } else {
+      sw[0][0] = ws[tile / (QW_BLOCK / 16) * a.kb + min(k0 + lane % KPW, a.kb - 1)];
+    }
+  };
+  int64_t tile = chunk;
+  load_scales(tile);
+#pragma unroll
+  for (int i = 0; i < RING; ++i) load(tile, i);
+  i32x8 xf[KPW];
+  float sx[KPW];
+  if constexpr (is_codes<XT>::value) {
+    const int64_t row = min(m0 + r, end - 1);
+#pragma unroll
+    for (int i = 0; i < KPW; ++i) {
+      xf[i] = fragment((const uint8_t*)a.x + row * a.kp + q * 16 + koff[i]);
+      sx[i] = a.xs[row * a.kb + min(k0 + i, a.kb - 1)];
+    }
+  } else {
+    constexpr int W = 2;
+    __shared__ __align__(16) uint8_t codes[WV][W][16][128];
+    __shared__ float scale[WV][W][16];
+    quantize_part<KPW, VEC, XT>(a, m0, end, k0, codes[wave], scale[wave], lane, xf, sx);
+  }
+  const bool have = m0 + r < end;
+#pragma unroll
+  for (int i = 0; i < KPW; ++i)
+    if (!have || k0 + i >= a.kb) {
+      xf[i] = i32x8{};
+      sx[i] = 0.0f;
+    }
+  int buf = 0;
+  auto step = [&](auto more) {
+    constexpr bool MORE = decltype(more)::value;  // a tile after this one
+    float s[BROWS1 ? KPW : 1][4];
+#pragma unroll
+    for (int i = 0; i < (BROWS1 ? KPW : 1); ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[i][c] = sw[i][c];
+    if (MORE) load_scales(tile + a.chunks);
+    f32x4 acc = {};
+#pragma unroll
+    for (int i = 0; i < KPW; ++i) {
+      if (EXACT) asm volatile("" : "+v"(xf[i]));  // converted anew: as codes it takes half the registers
+      const f32x4 d = dot128(Frag<EXACT>(w[i % RING]), Frag<EXACT>(xf[i]));
+      if (i + RING < KPW)
+        load(tile, i + RING);
+      else if (MORE)
+        load(tile + a.chunks, i + RING - KPW);
+      const float one = BROWS1 ? 1.0f
+                               : __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s[0][0]), i));
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        acc[c] = __builtin_fmaf(d[c], sx[i] * (BROWS1 ? s[BROWS1 ? i : 0][c] : one), acc[c]);
+    }
+    *(f32x4*)&part[buf][wave][r][4 * q] = acc;
+    // The weight's loads stay on their way.  One barrier a tile: the other
+    // buffer is written next, and read no later than the next barrier.
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const int t = threadIdx.x >> 4, c = threadIdx.x & 15;
+    if (t < 16 && m0 + t < end && tile * 16 + c < a.n) {
+      float sum = part[buf][0][t][c];
+#pragma unroll
+      for (int v = 1; v < WV; ++v) sum += part[buf][v][t][c];
+      store1((YT*)a.y + (m0 + t) * a.n + tile * 16 + c, sum);
+    }
+    buf ^= 1;
+  };
+  for (; tile + a.chunks < tiles_n; tile += a.chunks) step(std::true_type{});
+  step(std::false_type{});
+}
+
+constexpr int kStreamWaves = 8;
+
+template <int KPW, bool GROUPED, bool VEC, typename XT>
+hipError_t run_stream(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
+  a.tiles_m = GROUPED ? std::min(a.m, (a.m + a.experts * (int64_t)15) / 16) : (a.m + 15) / 16;
+  const int64_t tiles_n = (a.n + 15) / 16;
+  // two blocks a compute unit where the registers allow it
+  const int64_t want = KPW <= 4 ? 512 : 256;
+  a.chunks = std::min(tiles_n, std::max<int64_t>(1, (want + a.tiles_m - 1) / a.tiles_m));
+  const unsigned grid = (unsigned)(a.chunks * a.tiles_m);
+  auto go = [&](auto exact, auto brows1, auto y) {
+    gemm_stream<KPW, kStreamWaves, decltype(exact)::value, decltype(brows1)::value, GROUPED, VEC,
+                XT, decltype(y)><<<grid, kStreamWaves * 64, 0, stream>>>(a);
+  };
+  using std::true_type;
+  using std::false_type;
+  const bool one = g.brows == 1;
+  if (g.y_type == QW_BF16)
+    one ? go(false_type{}, true_type{}, uint16_t{}) : go(false_type{}, false_type{}, uint16_t{});
+  else if (g.exact)
+    one ? go(true_type{}, true_type{}, 0.0f) : go(true_type{}, false_type{}, 0.0f);
+  else if constexpr (GROUPED)
+    one ? go(false_type{}, true_type{}, 0.0f) : go(false_type{}, false_type{}, 0.0f);
+  return hipGetLastError();
+}
+
+// Most blocks of k that the stream kernel's waves hold.
+constexpr int kStreamMaxKb = 12 * kStreamWaves;
+
+template <bool GROUPED, bool VEC, typename XT>
+hipError_t run_stream(const GemmArgs& a, const BlockGemm& g, hipStream_t stream) {
+  const int each = (a.kb + kStreamWaves - 1) / kStreamWaves;
+  if (each <= 2) return run_stream<2, GROUPED, VEC, XT>(a, g, stream);
+  if (each <= 4) return run_stream<4, GROUPED, VEC, XT>(a, g, stream);
+  if (each <= 8) return run_stream<8, GROUPED, VEC, XT>(a, g, stream);
+  return run_stream<12, GROUPED, VEC, XT>(a, g, stream);
 }
 
 GemmArgs args_of(const BlockGemm& g) {
@@ -544,19 +723,24 @@ GemmArgs args_of(const BlockGemm& g) {
 
 }  // namespace
 
+bool block_gemm_fuses(int64_t m, int64_t k) {
+  return m <= 16 && pitch(k) <= kStreamMaxKb * QW_BLOCK;
+}
+
 hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t stream) {
   const GemmArgs a = args_of(g);
   if (g.x_type >= 0) {
     const bool vec = g.k % 8 == 0 && aligned(g.x, 16);
     if (g.x_type == QW_F32)
-      return vec ? run_direct<1, 1, 8, false, true, float>(a, g, stream)
-                 : run_direct<1, 1, 8, false, false, float>(a, g, stream);
-    return vec ? run_direct<1, 1, 8, false, true, uint16_t>(a, g, stream)
-               : run_direct<1, 1, 8, false, false, uint16_t>(a, g, stream);
+      return vec ? run_stream<false, true, float>(a, g, stream)
+                 : run_stream<false, false, float>(a, g, stream);
+    return vec ? run_stream<false, true, uint16_t>(a, g, stream)
+               : run_stream<false, false, uint16_t>(a, g, stream);
   }
-  if (g.m <= 16) return run_direct<1, 1, 8, false, true, uint8_t>(a, g, stream);
-  if (g.m > 128) return run_tiled<8, 4, false>(a, g, stream);
-  return run_direct<4, 4, 4, false, true, uint8_t>(a, g, stream);
+  if (block_gemm_fuses(g.m, g.k) && a.kb > 0) return run_stream<false, true, uint8_t>(a, g, stream);
+  if (g.m > 128) return run_tiled<8, 4, 2, false>(a, g, stream);
+  if (g.m <= 16) return run_direct<1, 1, 8, false>(a, g, stream);
+  return run_direct<4, 4, 4, false>(a, g, stream);
 }
 
 hipError_t launch_block_gemm_grouped(const BlockGemm& g, int64_t experts,
@@ -564,8 +748,10 @@ hipError_t launch_block_gemm_grouped(const BlockGemm& g, int64_t experts,
   GemmArgs a = args_of(g);
   a.experts = (int)experts;
   a.offsets = offsets;
-  if (g.m <= 16 * experts) return run_direct<1, 1, 8, true, true, uint8_t>(a, g, stream);
-  return run_direct<4, 4, 4, true, true, uint8_t>(a, g, stream);
+  if (g.m <= 16 * experts && a.kb > 0 && a.kb <= kStreamMaxKb)
+    return run_stream<true, true, uint8_t>(a, g, stream);
+  if (g.m <= 16 * experts) return run_direct<1, 1, 8, true>(a, g, stream);
+  return run_direct<4, 4, 4, true>(a, g, stream);
 }
 
 }  // namespace qw

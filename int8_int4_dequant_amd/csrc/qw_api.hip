@@ -564,7 +564,7 @@ int qw_block_gemm(int block_rows, int64_t n, int64_t k, const uint8_t* codes,
 
 int64_t qw_block_matmul_work_bytes(int64_t m, int64_t k) {
   if (check_rows(m, 1, k) != QW_OK) return -1;
-  if (m <= qw::kBlockFusedMaxM) return 0;
+  if (qw::block_gemm_fuses(m, k)) return 0;
   Carve c;
   c.take(m * qw::pitch(k));
   c.take(qw::block_scales(1, m, k) * 4);
@@ -584,7 +584,7 @@ int qw_block_matmul(int block_rows, int64_t n, int64_t k, const uint8_t* codes,
   if (!qw::aligned(codes, 16)) return QW_EARG;
   qw::BlockGemm g = {block_rows, n, k, m, codes, scales, x_type, x, nullptr, nullptr,
                      y_type, y, y_type == QW_F32};
-  if (m > qw::kBlockFusedMaxM) {
+  if (k == 0 || !qw::block_gemm_fuses(m, k)) {
     const int64_t need = qw_block_matmul_work_bytes(m, k);
     if (need > 0 && (!work || work_bytes < need || !qw::aligned(work, 16))) return QW_EWORK;
     Carve c;

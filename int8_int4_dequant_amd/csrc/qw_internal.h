@@ -73,10 +73,10 @@ hipError_t launch_block_quantize_swiglu(int64_t rows, int64_t f, int type, const
 hipError_t launch_block_unpack(int brows, int64_t count, int64_t n, int64_t k,
                                const uint8_t* codes, const float* scales, float* out,
                                hipStream_t stream);
-// Rows of float x up to which launch_block_gemm quantizes them itself.
-constexpr int kBlockFusedMaxM = 16;
-// One product.  x_type: QW_F32 or QW_BF16 (x, at most kBlockFusedMaxM rows) or
-// -1 (xc and xs).
+// Whether launch_block_gemm takes float x of these sizes (k > 0) and quantizes
+// it itself.
+bool block_gemm_fuses(int64_t m, int64_t k);
+// One product.  x_type: QW_F32 or QW_BF16 (x) or -1 (xc and xs).
 struct BlockGemm {
   int brows;
   int64_t n, k, m;

@@ -737,29 +737,39 @@ def _type(t, what):
 
 
 def _device_of(*ts):
-    """The one device that all tensors of a call are on (None entries aside)."""
+    """Index of the one device that all tensors of a call are on (None entries
+    aside)."""
     dev = None
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("libqw takes device tensors; a host tensor was passed")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and on {t.device}")
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError("libqw takes device tensors; a host tensor was passed")
+            if dev is not None:
+                raise ValueError(f"tensors on devices {dev} and {d}")
+            dev = d
     return dev
 
 
-def _run(dev, stream, call):
-    """call(stream) with ``dev`` as the current device (the library launches
-    on it)."""
-    if stream is not None and dev is not None and stream.device != dev:
-        raise ValueError(f"tensors on {dev} and a stream of {stream.device}")
-    if dev is None or dev.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(dev):
-        return call(_stream(stream))
+def _run(what, dev, stream, fn, *args):
+    """Calls the library with device ``dev`` as the current one (the library
+    launches on it) and the stream behind the arguments: tensors as their
+    addresses (0 for None and for empty ones)."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            raise ValueError(f"tensors on device {dev} and a stream of {stream.device}")
+        raw = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != QW_OK:
+        _check(status, what)
 
 
 def _on_stream(f):
@@ -776,22 +786,35 @@ def _on_stream(f):
     return call
 
 
+def _fits(t, dtypes, numel, what):
+    """_check_tensor, quick when all is well; the tensor's address."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.numel() != numel \
+            or not t.is_contiguous():
+        _check_tensor(t, dtypes, numel, what)
+    return t.data_ptr()
+
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+
+
 def _check_block(rec, what="record", dims=(2, 3)):
-    """Shape and block_rows of a block record whose codes and scales match
-    them; returns (experts, n, k, block_rows)."""
-    shape = [int(v) for v in rec["shape"]]
+    """Shape, block_rows and addresses of a block record whose codes and scales
+    match them: (experts, n, k, block_rows, codes, scales)."""
+    shape = rec["shape"]
     if len(shape) not in dims:
-        raise ValueError(f"{what}: shape {shape} has not {' or '.join(map(str, dims))} dimensions")
+        raise ValueError(f"{what}: shape {list(shape)} has not {' or '.join(map(str, dims))} "
+                         "dimensions")
     br = int(rec["block_rows"])
-    if br not in (1, BLOCK):
+    if br != 1 and br != BLOCK:
         raise ValueError(f"{what}: block_rows must be 1 or {BLOCK}")
-    *lead, n, k = shape
-    e = lead[0] if lead else 1
-    kp = _pitch(k)
-    _check_tensor(rec["codes"], (torch.float8_e4m3fn, torch.uint8), e * n * kp, f"{what} codes")
-    _check_tensor(rec["scales"], torch.float32, e * _rows_of_blocks(n, br) * (kp // BLOCK),
-                  f"{what} scales")
-    return e, n, k, br
+    e = int(shape[0]) if len(shape) == 3 else 1
+    n, k = int(shape[-2]), int(shape[-1])
+    kb = (k + BLOCK - 1) // BLOCK
+    codes = _fits(rec["codes"], _CODES, e * n * kb * BLOCK, "record codes")
+    scales = _fits(rec["scales"], _F32, e * ((n + br - 1) // br) * kb, "record scales")
+    return e, n, k, br, codes, scales
 
 
 def _empty_block(block_rows, shape, device):
@@ -814,11 +837,11 @@ def block_quantize(w, block_rows=BLOCK, stream=None):
     if block_rows not in (1, BLOCK):
         raise ValueError(f"block_rows must be 1 or {BLOCK}")
     dev = _device_of(w)
-    rec = _empty_block(block_rows, tuple(w.shape), dev)
-    *lead, n, k = rec["shape"]
-    _check(_run(dev, stream, lambda s: qw_block_quantize(
-        block_rows, lead[0] if lead else 1, n, k, t, w, rec["codes"], rec["scales"], s)),
-        "qw_block_quantize")
+    rec = _empty_block(block_rows, w.shape, w.device)
+    *lead, n, k = w.shape
+    _run("qw_block_quantize", dev, stream, lib().qw_block_quantize, block_rows,
+         lead[0] if lead else 1, n, k, t, w.data_ptr(), rec["codes"].data_ptr(),
+         rec["scales"].data_ptr())
     return rec
 
 
@@ -830,53 +853,51 @@ def block_quantize_swiglu(h, used=None, stream=None):
     if not isinstance(h, torch.Tensor) or h.dim() != 2 or h.shape[1] % 2 or not h.is_contiguous():
         raise ValueError("h must be a contiguous [rows][2 f] tensor")
     t = _type(h.dtype, "h")
-    if used is not None:
-        _check_tensor(used, torch.int32, 1, "used")
+    count = None if used is None else _fits(used, _I32, 1, "used")
     rows, f = h.shape[0], h.shape[1] // 2
     dev = _device_of(h, used)
-    rec = _empty_block(1, (rows, f), dev)
-    _check(_run(dev, stream, lambda s: qw_block_quantize_swiglu(
-        rows, f, t, h, used, rec["codes"], rec["scales"], s)), "qw_block_quantize_swiglu")
+    rec = _empty_block(1, (rows, f), h.device)
+    _run("qw_block_quantize_swiglu", dev, stream, lib().qw_block_quantize_swiglu, rows, f, t,
+         h.data_ptr(), count, rec["codes"].data_ptr(), rec["scales"].data_ptr())
     return rec
 
 
 @_on_stream
 def block_unpack(rec, out=None, stream=None):
     """The fp32 values that a record's codes stand for."""
-    e, n, k, br = _check_block(rec)
+    e, n, k, br, codes, scales = _check_block(rec)
     shape = tuple(int(v) for v in rec["shape"])
     if out is None:
         out = torch.empty(shape, dtype=torch.float32, device=rec["codes"].device)
     _check_tensor(out, torch.float32, e * n * k, "out", shape)
     dev = _device_of(rec["codes"], rec["scales"], out)
-    _check(_run(dev, stream, lambda s: qw_block_unpack(br, e, n, k, rec["codes"], rec["scales"],
-                                                       out, s)), "qw_block_unpack")
+    _run("qw_block_unpack", dev, stream, lib().qw_block_unpack, br, e, n, k, codes, scales,
+         out.data_ptr())
     return out
 
 
-def _output(out, shape, dtype, device, what="out"):
+def _output(out, rows, cols, dtype, like):
+    """``out`` checked, or a new [rows][cols] tensor of ``dtype`` on ``like``'s
+    device; and its type's code."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _type(out.dtype, what)
-    n = 1
-    for v in shape:
-        n *= v
-    return _check_tensor(out, out.dtype if dtype is None else dtype, n, what, shape)
+        out = torch.empty((rows, cols), dtype=dtype, device=like.device)
+    else:
+        _check_tensor(out, out.dtype if dtype is None else dtype, rows * cols, "out", (rows, cols))
+    return out, _type(out.dtype, "out")
 
 
 @_on_stream
 def block_gemm(rec, x, out=None, out_dtype=torch.float32, stream=None):
     """y [m][n] = x . W^T of two records: ``rec`` the weight [n][k], ``x`` m
     rows of k values with 1 x 128 blocks."""
-    _, n, k, br = _check_block(rec, "record", (2,))
-    _, m, kx, bx = _check_block(x, "x", (2,))
+    _, n, k, br, codes, scales = _check_block(rec, "record", (2,))
+    _, m, kx, bx, xc, xs = _check_block(x, "x", (2,))
     if kx != k or bx != 1:
         raise ValueError(f"x must be a record of [m][{k}] with block_rows 1")
-    out = _output(out, (m, n), out_dtype, x["codes"].device)
+    out, yt = _output(out, m, n, out_dtype, x["codes"])
     dev = _device_of(rec["codes"], rec["scales"], x["codes"], x["scales"], out)
-    _check(_run(dev, stream, lambda s: qw_block_gemm(
-        br, n, k, rec["codes"], rec["scales"], m, x["codes"], x["scales"],
-        _type(out.dtype, "out"), out, s)), "qw_block_gemm")
+    _run("qw_block_gemm", dev, stream, lib().qw_block_gemm, br, n, k, codes, scales, m, xc, xs,
+         yt, out.data_ptr())
     return out
 
 
@@ -885,30 +906,30 @@ def block_matmul(rec, x, out=None, out_dtype=None, work=None, stream=None):
     """Float x [m][k] (fp32 or bf16, any m), quantized on the way with 1 x 128
     blocks, times a record's weight; returns y [m][n] of x's type (or
     ``out_dtype``)."""
-    _, n, k, br = _check_block(rec, "record", (2,))
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != k:
-        raise ValueError("x must be a contiguous [m][k] tensor")
+    _, n, k, br, codes, scales = _check_block(rec, "record", (2,))
+    xt = _check_matrix(x, "x", None, k)
     m = x.shape[0]
-    xt = _type(x.dtype, "x")
-    _check_tensor(x, x.dtype, m * k, "x")
-    out = _output(out, (m, n), out_dtype or (x.dtype if out is None else out.dtype), x.device)
+    out, yt = _output(out, m, n, out_dtype or (x.dtype if out is None else None), x)
     dev = _device_of(rec["codes"], rec["scales"], x, out, work)
-    need = lib().qw_block_matmul_work_bytes(m, k)
-    if work is None and need > 0:
-        work = _work(need, dev)
-    wb = _work_bytes(work)
-    _check(_run(dev, stream, lambda s: qw_block_matmul(
-        br, n, k, rec["codes"], rec["scales"], m, xt, x, _type(out.dtype, "out"), out, work, wb,
-        s)), "qw_block_matmul")
+    work, wp, wb = _workspace(work, lib().qw_block_matmul_work_bytes(m, k), x)
+    _run("qw_block_matmul", dev, stream, lib().qw_block_matmul, br, n, k, codes, scales, m, xt,
+         x.data_ptr(), yt, out.data_ptr(), wp, wb)
     return out
 
 
-def _work_bytes(work):
+def _workspace(work, need, like):
+    """(work, address, bytes) of the caller's work buffer, or of a new one of
+    ``need`` bytes on ``like``'s device."""
     if work is None:
-        return 0
+        if need < 0:
+            raise ValueError("invalid shape for a work-size query")
+        if need == 0:
+            return None, None, 0
+        work = torch.empty(need, dtype=torch.uint8, device=like.device)
+        return work, work.data_ptr(), need
     if not isinstance(work, torch.Tensor) or not work.is_contiguous():
         raise ValueError("work must be a contiguous tensor")
-    return work.numel() * work.element_size()
+    return work, work.data_ptr(), work.numel() * work.element_size()
 
 
 @_on_stream
@@ -917,16 +938,15 @@ def block_gemm_grouped(rec, x, offsets, out=None, out_dtype=torch.float32, strea
     ``x`` a record of [rows][k] with 1 x 128 blocks, ``offsets`` device int32
     [experts + 1] (moe_sort).  Rows that no expert has are left as they are
     in ``out``."""
-    e, n, k, br = _check_block(rec, "record", (3,))
-    _, rows, kx, bx = _check_block(x, "x", (2,))
+    e, n, k, br, codes, scales = _check_block(rec, "record", (3,))
+    _, rows, kx, bx, xc, xs = _check_block(x, "x", (2,))
     if kx != k or bx != 1:
         raise ValueError(f"x must be a record of [rows][{k}] with block_rows 1")
-    _check_tensor(offsets, torch.int32, e + 1, "offsets")
-    out = _output(out, (rows, n), out_dtype, x["codes"].device)
+    first = _fits(offsets, _I32, e + 1, "offsets")
+    out, yt = _output(out, rows, n, out_dtype, x["codes"])
     dev = _device_of(rec["codes"], rec["scales"], x["codes"], x["scales"], offsets, out)
-    _check(_run(dev, stream, lambda s: qw_block_gemm_grouped(
-        br, e, n, k, rec["codes"], rec["scales"], rows, x["codes"], x["scales"], offsets,
-        _type(out.dtype, "out"), out, s)), "qw_block_gemm_grouped")
+    _run("qw_block_gemm_grouped", dev, stream, lib().qw_block_gemm_grouped, br, e, n, k, codes,
+         scales, rows, xc, xs, first, yt, out.data_ptr())
     return out
 
 
@@ -940,7 +960,7 @@ def _check_ids(ids):
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.dtype not in _IDS \
             or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 or int64 [t][topk] tensor")
-    return int(ids.shape[0]), int(ids.shape[1]), _IDS[ids.dtype]
+    return ids.shape[0], ids.shape[1], _IDS[ids.dtype]
 
 
 @_on_stream
@@ -951,27 +971,25 @@ def moe_sort(ids, experts, order=True, work=None, stream=None):
     behind the last row; None if ``order`` is false), offsets [experts + 1]."""
     t, topk, nbytes = _check_ids(ids)
     dev = _device_of(ids, work)
-    need = lib().qw_moe_sort_work_bytes(t, topk, experts)
-    if work is None and need > 0:
-        work = _work(need, dev)
-    wb = _work_bytes(work)
-    pos = torch.empty((t, topk), dtype=torch.int32, device=dev)
-    back = torch.empty(t * topk, dtype=torch.int32, device=dev) if order else None
-    offsets = torch.empty(max(0, experts) + 1, dtype=torch.int32, device=dev)
-    _check(_run(dev, stream, lambda s: qw_moe_sort(t, topk, experts, nbytes, ids, pos, back,
-                                                   offsets, work, wb, s)), "qw_moe_sort")
+    work, wp, wb = _workspace(work, lib().qw_moe_sort_work_bytes(t, topk, experts), ids)
+    pos = torch.empty((t, topk), dtype=torch.int32, device=ids.device)
+    back = torch.empty(t * topk, dtype=torch.int32, device=ids.device) if order else None
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+    _run("qw_moe_sort", dev, stream, lib().qw_moe_sort, t, topk, experts, nbytes, ids.data_ptr(),
+         pos.data_ptr(), back.data_ptr() if order else None, offsets.data_ptr(), wp, wb)
     return dict(pos=pos, order=back, offsets=offsets)
 
 
 def _check_pos(route, t=None):
     pos = route["pos"]
-    if not isinstance(pos, torch.Tensor) or pos.dim() != 2 or (t is not None and pos.shape[0] != t):
-        raise ValueError(f"pos must be an int32 [{'t' if t is None else t}][topk] tensor")
-    _check_tensor(pos, torch.int32, pos.numel(), "pos")
-    return pos, int(pos.shape[0]), int(pos.shape[1])
+    if not isinstance(pos, torch.Tensor) or pos.dim() != 2 or pos.dtype != torch.int32 \
+            or not pos.is_contiguous() or (t is not None and pos.shape[0] != t):
+        raise ValueError(f"pos must be a contiguous int32 [{'t' if t is None else t}][topk] tensor")
+    return pos, pos.shape[0], pos.shape[1]
 
 
 def _check_matrix(x, what, rows=None, cols=None, dtype=None):
+    """The type's code of a contiguous matrix of those sizes."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_contiguous() \
             or (rows is not None and x.shape[0] != rows) or (cols is not None and x.shape[1] != cols):
         raise ValueError(f"{what} must be a contiguous [{'rows' if rows is None else rows}]"
@@ -979,6 +997,13 @@ def _check_matrix(x, what, rows=None, cols=None, dtype=None):
     if dtype is not None and x.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}, got {x.dtype}")
     return _type(x.dtype, what)
+
+
+def _check_weights(weights, t, topk):
+    if weights is None:
+        return None
+    _check_tensor(weights, torch.float32, t * topk, "weights", (t, topk))
+    return weights.data_ptr()
 
 
 @_on_stream
@@ -992,8 +1017,8 @@ def moe_gather(x, route, out=None, stream=None):
         out = torch.empty((t * topk, d), dtype=x.dtype, device=x.device)
     _check_matrix(out, "out", None, d, x.dtype)
     dev = _device_of(x, pos, out)
-    _check(_run(dev, stream, lambda s: qw_moe_gather(t, topk, d, out.shape[0], xt, x, pos, out,
-                                                     s)), "qw_moe_gather")
+    _run("qw_moe_gather", dev, stream, lib().qw_moe_gather, t, topk, d, out.shape[0], xt,
+         x.data_ptr(), pos.data_ptr(), out.data_ptr())
     return out
 
 
@@ -1009,9 +1034,9 @@ def moe_gather_block(x, route, rows=None, stream=None):
     if rows < 0:
         raise ValueError("rows must not be negative")
     dev = _device_of(x, pos)
-    rec = _empty_block(1, (rows, d), dev)
-    _check(_run(dev, stream, lambda s: qw_moe_gather_block(
-        t, topk, d, rows, xt, x, pos, rec["codes"], rec["scales"], s)), "qw_moe_gather_block")
+    rec = _empty_block(1, (rows, d), x.device)
+    _run("qw_moe_gather_block", dev, stream, lib().qw_moe_gather_block, t, topk, d, rows, xt,
+         x.data_ptr(), pos.data_ptr(), rec["codes"].data_ptr(), rec["scales"].data_ptr())
     return rec
 
 
@@ -1019,23 +1044,20 @@ def moe_gather_block(x, route, rows=None, stream=None):
 def moe_combine(ys, route, weights=None, out=None, out_dtype=None, stream=None):
     """y [t][d] = sum over a token's slots of weights [t][topk] (fp32; all 1
     if None) times their rows of ys [rows][d]; of ys' type or ``out_dtype``."""
-    yt = _check_matrix(ys, "ys")
+    st = _check_matrix(ys, "ys")
     rows, d = ys.shape
     pos, t, topk = _check_pos(route)
-    if weights is not None:
-        _check_tensor(weights, torch.float32, t * topk, "weights", (t, topk))
-    out = _output(out, (t, d), out_dtype or (ys.dtype if out is None else out.dtype), ys.device)
+    wp = _check_weights(weights, t, topk)
+    out, yt = _output(out, t, d, out_dtype or (ys.dtype if out is None else None), ys)
     dev = _device_of(ys, pos, weights, out)
-    _check(_run(dev, stream, lambda s: qw_moe_combine(
-        t, topk, d, rows, yt, ys, pos, weights, _type(out.dtype, "out"), out, s)),
-        "qw_moe_combine")
+    _run("qw_moe_combine", dev, stream, lib().qw_moe_combine, t, topk, d, rows, st, ys.data_ptr(),
+         pos.data_ptr(), wp, yt, out.data_ptr())
     return out
 
 
-@_on_stream
 def moe_gather_backward(dxs, route, out=None, stream=None):
     """Gradient of moe_gather: dx [t][d], each token's sum of its rows of dxs."""
-    return moe_combine(dxs, route, None, out, stream=stream)
+    return moe_combine(dxs, route, None, out, None, stream=stream)
 
 
 @_on_stream
@@ -1043,12 +1065,11 @@ def moe_combine_backward(dy, ys, route, weights=None, dys=None, dweights=None, s
     """Gradients of moe_combine for dy [t][d]: (dys [rows][d], dweights fp32
     [t][topk]).  dy and ys have one type; rows of dys without a slot are left
     as they are."""
-    yt = _check_matrix(ys, "ys")
+    st = _check_matrix(ys, "ys")
     rows, d = ys.shape
     pos, t, topk = _check_pos(route)
     _check_matrix(dy, "dy", t, d, ys.dtype)
-    if weights is not None:
-        _check_tensor(weights, torch.float32, t * topk, "weights", (t, topk))
+    wp = _check_weights(weights, t, topk)
     if dys is None:
         dys = torch.empty_like(ys)
     _check_matrix(dys, "dys", rows, d, ys.dtype)
@@ -1056,9 +1077,9 @@ def moe_combine_backward(dy, ys, route, weights=None, dys=None, dweights=None, s
         dweights = torch.empty((t, topk), dtype=torch.float32, device=dy.device)
     _check_tensor(dweights, torch.float32, t * topk, "dweights", (t, topk))
     dev = _device_of(dy, ys, pos, weights, dys, dweights)
-    _check(_run(dev, stream, lambda s: qw_moe_combine_backward(
-        t, topk, d, rows, yt, dy, ys, pos, weights, dys, dweights, s)),
-        "qw_moe_combine_backward")
+    _run("qw_moe_combine_backward", dev, stream, lib().qw_moe_combine_backward, t, topk, d, rows,
+         st, dy.data_ptr(), ys.data_ptr(), pos.data_ptr(), wp, dys.data_ptr(),
+         dweights.data_ptr())
     return dys, dweights
 
 
@@ -1069,23 +1090,18 @@ def moe_mlp(gate_up, down, x, ids, weights=None, out=None, out_dtype=None, work=
     weights fp32 [t][topk]; ``gate_up`` a record of [experts][2 f][d] (gate
     rows, then up rows), ``down`` of [experts][d][f].  y [t][d] of x's type or
     ``out_dtype``."""
-    e, f2, d, br = _check_block(gate_up, "gate_up", (3,))
-    ed, dd, f, bd = _check_block(down, "down", (3,))
+    e, f2, d, br, gc, gs = _check_block(gate_up, "gate_up", (3,))
+    ed, dd, f, bd, dc, ds = _check_block(down, "down", (3,))
     if ed != e or dd != d or f2 != 2 * f or bd != br:
         raise ValueError("gate_up must be [experts][2 f][d] and down [experts][d][f], with the "
                          "same block_rows")
     t, topk, nbytes = _check_ids(ids)
     xt = _check_matrix(x, "x", t, d)
-    if weights is not None:
-        _check_tensor(weights, torch.float32, t * topk, "weights", (t, topk))
-    out = _output(out, (t, d), out_dtype or (x.dtype if out is None else out.dtype), x.device)
+    wp = _check_weights(weights, t, topk)
+    out, yt = _output(out, t, d, out_dtype or (x.dtype if out is None else None), x)
     dev = _device_of(gate_up["codes"], gate_up["scales"], down["codes"], down["scales"], x, ids,
                      weights, out, work)
-    need = lib().qw_moe_mlp_work_bytes(t, topk, e, d, f)
-    if work is None and need > 0:
-        work = _work(need, dev)
-    wb = _work_bytes(work)
-    _check(_run(dev, stream, lambda s: qw_moe_mlp(
-        br, e, d, f, gate_up["codes"], gate_up["scales"], down["codes"], down["scales"], t, topk,
-        xt, x, nbytes, ids, weights, _type(out.dtype, "out"), out, work, wb, s)), "qw_moe_mlp")
+    work, kp, kb = _workspace(work, lib().qw_moe_mlp_work_bytes(t, topk, e, d, f), x)
+    _run("qw_moe_mlp", dev, stream, lib().qw_moe_mlp, br, e, d, f, gc, gs, dc, ds, t, topk, xt,
+         x.data_ptr(), nbytes, ids.data_ptr(), wp, yt, out.data_ptr(), kp, kb)
     return out
