@@ -445,6 +445,8 @@ int qw_gptq_quantize_pack(int bits, int64_t group, int64_t n, int64_t k,
  * input, both quantized with block_rows 1.
  */
 #define QW_BLOCK 128
+/* Largest k of a product (QW_ESHAPE beyond). */
+#define QW_BLOCK_MAX_K (1ll << 22)
 enum qw_type { QW_F32 = 0, QW_BF16 = 1 };
 
 /* Bytes of one row of codes (-1 if k is invalid). */

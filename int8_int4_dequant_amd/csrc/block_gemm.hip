@@ -21,6 +21,7 @@
 #include "block_codes.h"
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 namespace qw {
@@ -38,7 +39,8 @@ struct GemmArgs {
   void* y;
   const int32_t* offsets;
   int experts;
-  int64_t n, k, m;
+  int64_t n, k, m;    // n: weight rows of this launch
+  int64_t ldy;        // outputs in a row of y
   int64_t kp;
   int kb;             // blocks along k
   int64_t nb;         // rows of scales of one weight
@@ -108,7 +110,8 @@ __device__ __forceinline__ i32x8 fragment(const uint8_t* p) {
 }
 
 // Rows [row, end) of the tm-th tile of `bm` rows, counted expert by expert;
-// false when there are fewer tiles.  The whole wave calls it.
+// false when there are fewer tiles.  The whole wave calls it; its results are
+// the same for all lanes (in scalar registers).
 __device__ __forceinline__ bool grouped_tile(const GemmArgs& a, int64_t tm, int bm, int& expert,
                                              int64_t& row, int64_t& end) {
   const int lane = threadIdx.x & 63;
@@ -127,12 +130,13 @@ __device__ __forceinline__ bool grouped_tile(const GemmArgs& a, int64_t tm, int 
       const int v = __shfl_up(upto, h);
       if (lane >= h) upto += v;
     }
-    const int total = __shfl(upto, 63);
+    const int total = __builtin_amdgcn_readlane(upto, 63);
     if (tm < before + total) {
       const int l = __builtin_ctzll(__ballot(tm < before + upto));
       expert = c + l;
-      row = __shfl(lo, l) + (tm - before - (__shfl(upto, l) - __shfl(tiles, l))) * bm;
-      end = min((int64_t)__shfl(hi, l), row + bm);
+      row = __builtin_amdgcn_readlane(lo, l) +
+            (tm - before - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(tiles, l))) * bm;
+      end = min((int64_t)__builtin_amdgcn_readlane(hi, l), row + bm);
       return true;
     }
     before += total;
@@ -143,13 +147,36 @@ __device__ __forceinline__ bool grouped_tile(const GemmArgs& a, int64_t tm, int 
 template <typename XT> struct is_codes { static constexpr bool value = false; };
 template <> struct is_codes<uint8_t> { static constexpr bool value = true; };
 
-// A block computes 16 NT weight rows x 16 MT tokens; its WV waves take every
-// WV-th block of k, straight from memory into registers, and add their sums
-// through LDS.
-template <int NT, int MT, int WV, bool EXACT, bool BROWS1, bool GROUPED, typename YT>
+// ------------------------------------------------------------ direct kernel
+//
+// For more rows than the stream kernel takes and too few tiles for the tiled
+// one: a block computes 16 NT weight rows x 16 MT tokens, its WV waves
+// share the blocks of k, take them straight from memory into registers, and add
+// their sums through LDS.  Bound by the latency of its loads: PD blocks of k are on
+// their way.  Behind the last block the loads go to an empty buffer and give
+// zeros without touching memory, so that no branch stands between them.
+
+__device__ __forceinline__ i32x8 buffer_fragment(__amdgpu_buffer_rsrc_t buf, uint32_t voff,
+                                                 uint32_t soff) {
+  const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(buf, voff, soff, 0);
+  const u32x4 hi = __builtin_amdgcn_raw_buffer_load_b128(buf, voff + 64, soff, 0);
+  return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w,
+               (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+}
+__device__ __forceinline__ float buffer_float(__amdgpu_buffer_rsrc_t buf, uint32_t voff,
+                                              uint32_t soff) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buf, voff, soff, 0));
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)(uint32_t)bytes, 0x00020000);
+}
+
+template <int NT, int MT, int WV, int PD, bool EXACT, bool BROWS1, bool GROUPED, typename YT>
 __global__ __launch_bounds__(WV * 64) void gemm_direct(GemmArgs a) {
   constexpr int BN = 16 * NT, BM = 16 * MT, LD = BN + 4;
-  __shared__ float part[WV][BM][LD];
+  constexpr int SW = BROWS1 ? 4 * NT : 1;  // weight scales a lane needs
+  static_assert(QW_BLOCK % BN == 0, "a block's weight rows lie in one 128 x 128 block");
+  __shared__ __align__(16) float part[WV][BM][LD];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
@@ -157,42 +184,57 @@ __global__ __launch_bounds__(WV * 64) void gemm_direct(GemmArgs a) {
     int64_t m0 = tile % a.tiles_m * BM, end = min(m0 + BM, a.m);
     int expert = 0;
     if (GROUPED && !grouped_tile(a, tile % a.tiles_m, BM, expert, m0, end)) continue;
-    const uint8_t* wc = a.codes + expert * a.n * a.kp + q * 16;
-    const float* ws = a.scales + expert * a.nb * a.kb;
-    const uint8_t* wp[NT];
+    const int64_t wrows = min(a.n - n0, (int64_t)BN), srow = BROWS1 ? n0 : n0 / QW_BLOCK;
+    const uint8_t* wbase = a.codes + (expert * a.n + n0) * a.kp;
+    const uint8_t* xbase = (const uint8_t*)a.x + m0 * a.kp;
+    const float* wsbase = a.scales + (expert * a.nb + srow) * a.kb;
+    const float* xsbase = a.xs + m0 * a.kb;
+    i32x8 w[PD][NT], x[PD][MT];
+    float sw[PD][SW], sx[PD][MT];
+    // A wave's blocks of k are consecutive ones: rows are often a power of two
+    // apart, and waves side by side would all ask the same few L2 channels.
+    const int each = (a.kb + WV - 1) / WV, first = wave * each;
+    const int last = min(first + each, a.kb);
+    auto load = [&](int b, int p) {
+      const bool in = b < last;
+      const auto wbuf = rsrc_of(wbase, in ? wrows * a.kp : 0);
+      const auto xbuf = rsrc_of(xbase, in ? (end - m0) * a.kp : 0);
+      const auto wsbuf = rsrc_of(wsbase, in ? (BROWS1 ? wrows : 1) * a.kb * 4 : 0);
+      const auto xsbuf = rsrc_of(xsbase, in ? (end - m0) * a.kb * 4 : 0);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) wp[i] = wc + min(n0 + 16 * i + r, a.n - 1) * a.kp;
-    const float* wsp[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        wsp[i][c] = BROWS1 ? ws + min(n0 + 16 * i + 4 * q + c, a.n - 1) * a.kb
-                           : ws + n0 / QW_BLOCK * a.kb;
-    const uint8_t* xp[MT];
-    const float* sxp[MT];
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const int64_t row = min(m0 + 16 * j + r, end - 1);
-      xp[j] = (const uint8_t*)a.x + row * a.kp + q * 16;
-      sxp[j] = a.xs + row * a.kb;
-    }
-    f32x4 acc[NT][MT] = {};
-    for (int b = wave; b < a.kb; b += WV) {
-      Frag<EXACT> wf[NT];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) wf[i] = Frag<EXACT>(fragment(wp[i] + (int64_t)b * QW_BLOCK));
+      for (int i = 0; i < NT; ++i)
+        w[p][i] = buffer_fragment(wbuf, (16 * i + r) * (uint32_t)a.kp + q * 16, b * QW_BLOCK);
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        const float sx = sxp[j][b];
-        const Frag<EXACT> xf(fragment(xp[j] + (int64_t)b * QW_BLOCK));
+        x[p][j] = buffer_fragment(xbuf, (16 * j + r) * (uint32_t)a.kp + q * 16, b * QW_BLOCK);
+        sx[p][j] = buffer_float(xsbuf, (16 * j + r) * a.kb * 4, b * 4);
+      }
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const f32x4 d = dot128(wf[i], xf);
+      for (int c = 0; c < SW; ++c)
+        sw[p][c] = buffer_float(wsbuf, BROWS1 ? (16 * (c / 4) + 4 * q + c % 4) * a.kb * 4 : 0, b * 4);
+    };
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            acc[i][j][c] = __builtin_fmaf(d[c], sx * wsp[i][c][b], acc[i][j][c]);
+    for (int p = 0; p < PD; ++p) load(first + p, p);
+    f32x4 acc[NT][MT] = {};
+    for (int b = first; b < last; b += PD) {
+#pragma unroll
+      for (int p = 0; p < PD; ++p) {
+        Frag<EXACT> wf[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) wf[i] = Frag<EXACT>(w[p][i]);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const Frag<EXACT> xf(x[p][j]);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const f32x4 d = dot128(wf[i], xf);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              acc[i][j][c] = __builtin_fmaf(d[c], sx[p][j] * sw[p][BROWS1 ? 4 * i + c : 0],
+                                            acc[i][j][c]);
+          }
         }
+        load(b + p + PD, p);
       }
     }
     __syncthreads();  // the last tile's sums have been read
@@ -206,14 +248,14 @@ __global__ __launch_bounds__(WV * 64) void gemm_direct(GemmArgs a) {
       if (m0 + t < end && n0 + c < a.n) {
         float s = part[0][t][c];
 #pragma unroll
-        for (int w = 1; w < WV; ++w) s += part[w][t][c];
-        store1((YT*)a.y + (m0 + t) * a.n + n0 + c, s);
+        for (int v = 1; v < WV; ++v) s += part[v][t][c];
+        store1((YT*)a.y + (m0 + t) * a.ldy + n0 + c, s);
       }
     }
   }
 }
 
-template <int NT, int MT, int WV, bool GROUPED>
+template <int NT, int MT, int WV, int PD, bool GROUPED>
 hipError_t run_direct(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   constexpr int BN = 16 * NT, BM = 16 * MT;
   a.tiles_m = GROUPED ? std::min(a.m, (a.m + a.experts * (int64_t)(BM - 1)) / BM)
@@ -222,7 +264,7 @@ hipError_t run_direct(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   // a launch holds fewer than 2^32 threads: the kernel's loop takes the rest
   const unsigned grid = (unsigned)std::min<int64_t>(a.tiles, 1 << 21);
   auto go = [&](auto exact, auto brows1, auto y) {
-    gemm_direct<NT, MT, WV, decltype(exact)::value, decltype(brows1)::value, GROUPED, decltype(y)>
+    gemm_direct<NT, MT, WV, PD, decltype(exact)::value, decltype(brows1)::value, GROUPED, decltype(y)>
         <<<grid, WV * 64, 0, stream>>>(a);
   };
   using std::true_type;
@@ -485,7 +527,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
 #pragma unroll
     for (int i = 0; i < NF; ++i) {
       const int64_t col = n0 + wn + 16 * i + 4 * q;
-      YT* y = (YT*)a.y + row * a.n + col;
+      YT* y = (YT*)a.y + row * a.ldy + col;
       if (a.y_vec) {
         if (col < a.n) store4(y, acc[i][j]);
       } else {
@@ -497,7 +539,8 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
   }
 }
 
-template <int NF, int MF, int STAGES, bool GROUPED>
+// EXACT: the bf16 cores' instances too.
+template <int NF, int MF, int STAGES, bool EXACT, bool GROUPED>
 hipError_t run_tiled(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   constexpr int BN = 32 * NF, BM = 64 * MF;
   a.tiles_m = GROUPED ? std::min(a.m, (a.m + a.experts * (int64_t)(BM - 1)) / BM)
@@ -513,10 +556,13 @@ hipError_t run_tiled(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   const bool one = g.brows == 1;
   if (g.y_type == QW_BF16)
     one ? go(false_type{}, true_type{}, uint16_t{}) : go(false_type{}, false_type{}, uint16_t{});
-  else if (g.exact)
-    one ? go(true_type{}, true_type{}, 0.0f) : go(true_type{}, false_type{}, 0.0f);
-  else if constexpr (GROUPED)
-    one ? go(false_type{}, true_type{}, 0.0f) : go(false_type{}, false_type{}, 0.0f);
+  else if constexpr (EXACT) {
+    if (g.exact) one ? go(true_type{}, true_type{}, 0.0f) : go(true_type{}, false_type{}, 0.0f);
+  }
+  if constexpr (GROUPED) {
+    if (g.y_type == QW_F32 && !g.exact)
+      one ? go(false_type{}, true_type{}, 0.0f) : go(false_type{}, false_type{}, 0.0f);
+  }
   return hipGetLastError();
 }
 
@@ -659,7 +705,7 @@ __global__ __launch_bounds__(WV * 64) void gemm_stream(GemmArgs a) {
       float sum = part[buf][0][t][c];
 #pragma unroll
       for (int v = 1; v < WV; ++v) sum += part[buf][v][t][c];
-      store1((YT*)a.y + (m0 + t) * a.n + tile * 16 + c, sum);
+      store1((YT*)a.y + (m0 + t) * a.ldy + tile * 16 + c, sum);
     }
     buf ^= 1;
   };
@@ -693,6 +739,10 @@ hipError_t run_stream(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Rows up to which the stream kernel quantizes x itself: each block pays for it
+// (4096 x 4096: 8.5 us at 1 row, 11.3 at 8, 16.8 at 16; with codes 6.4, 7.3
+// and 8.0, and 2.8 for a kernel that makes them).
+constexpr int kFusedMaxM = 8;
 // Most blocks of k that the stream kernel's waves hold.
 constexpr int kStreamMaxKb = 12 * kStreamWaves;
 
@@ -712,7 +762,7 @@ GemmArgs args_of(const BlockGemm& g) {
   a.x = g.x_type < 0 ? (const void*)g.xc : g.x;
   a.xs = g.xs;
   a.y = g.y;
-  a.n = g.n;
+  a.n = a.ldy = g.n;
   a.k = g.k;
   a.m = g.m;
   a.kp = pitch(g.k);
@@ -721,10 +771,96 @@ GemmArgs args_of(const BlockGemm& g) {
   return a;
 }
 
+// ---------------------------------------------------------------- choice
+//
+// Which kernel and tile: the one with the least estimated time, from what each
+// takes for a round of the 256 compute units.
+//   tiled   a block of k takes `step` us with all units at work: 256 x 256
+//           1.84, 128 x 256 (weight x tokens) 1.07, 256 x 128 1.06, 128 x 128
+//           0.70; on the bf16 cores 1.78 (128 x 256) and 1.16 (128 x 128), the
+//           larger tiles not fitting the registers as well (measured on
+//           8192^3: 470, 550, 540, 700 us and 910, 1180 us).  3 us to start and
+//           to write y.
+//   direct  a unit takes in 28 KB of scattered rows a us, and 4 us to start,
+//           to join the sums and to write (64 rows x 4096 x 4096: 13 us with 32 x 32
+//           tiles, 20 with 32 x 64, 20 tiled; 64 x 28672 x 8192: 132, 125,
+//           53; 256 x 4096 x 4096: 41, 35, 20; 32 x 4096 x 4096: 11.5 with
+//           16 x 32, 13 with 32 x 32).
+// A tiled product whose last round is only partly filled may be cut in two along
+// the weight rows, the rest with smaller tiles (2048 x 28672 x 8192: 3.5 rounds
+// of 256 x 256, 480 us; 3 rounds and one of 256 x 128, 430 us).
+// Grouped: an expert's last tile is half empty on average.
+
+constexpr int kUnits = 256;
+
+struct Shape {
+  int nf, mf;   // fragments of a wave
+  bool tiled;
+  double step;  // tiled, 8-bit cores
+  double exact; // tiled, bf16 cores; 0: not taken
+  int bn() const { return tiled ? 32 * nf : 16 * nf; }
+  int bm() const { return tiled ? 64 * mf : 16 * mf; }
+};
+constexpr Shape kShapes[] = {
+    {8, 4, true, 1.84, 0.0},  {8, 2, true, 1.06, 0.0},  {4, 4, true, 1.07, 1.78},
+    {4, 2, true, 0.70, 1.16}, {2, 4, false, 0.0, 0.0},  {2, 2, false, 0.0, 0.0},
+    {1, 2, false, 0.0, 0.0},
+};
+constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
+
+// Estimated us of n weight rows against m rows of x (of `experts` experts).
+double cost_of(const Shape& s, int64_t n, int64_t m, int64_t experts, int kb, bool exact) {
+  const int64_t spare = std::min(experts, m) / 2;  // half-empty tiles
+  const double tiles_m = experts ? (double)m / s.bm() + spare + 1 : (double)((m + s.bm() - 1) / s.bm());
+  const double rounds = std::ceil(tiles_m * ((n + s.bn() - 1) / s.bn()) / kUnits);
+  if (!s.tiled) return 4.0 + rounds * (s.bn() + s.bm()) * kb * (QW_BLOCK / 28000.0);
+  const double step = exact ? s.exact : s.step;
+  return step == 0.0 ? 1e30 : rounds * (3.0 + kb * step);
+}
+
+int best_shape(int64_t n, int64_t m, int64_t experts, int kb, bool exact, double* cost) {
+  int best = 0;
+  *cost = 1e30;
+  for (int i = 0; i < kShapeCount; ++i) {
+    const double c = cost_of(kShapes[i], n, m, experts, kb, exact);
+    if (c < *cost) {
+      *cost = c;
+      best = i;
+    }
+  }
+  return best;
+}
+
+template <bool GROUPED>
+hipError_t run_shape(int shape, const GemmArgs& a, const BlockGemm& g, hipStream_t stream) {
+  // no k, or more tiles than a launch holds: the direct kernel loops over them
+  const int64_t most = (a.m / 128 + a.experts + 1) * (a.n / 128 + 1);
+  if (a.kb == 0 || most > 1 << 22) shape = 4;
+  switch (shape) {
+    case 0: return run_tiled<8, 4, 2, false, GROUPED>(a, g, stream);
+    case 1: return run_tiled<8, 2, 3, false, GROUPED>(a, g, stream);
+    case 2: return run_tiled<4, 4, 3, true, GROUPED>(a, g, stream);
+    case 3: return run_tiled<4, 2, 4, true, GROUPED>(a, g, stream);
+    case 4: return run_direct<2, 4, 8, 1, GROUPED>(a, g, stream);
+    case 5: return run_direct<2, 2, 8, 1, GROUPED>(a, g, stream);
+    default: return run_direct<1, 2, 8, 2, GROUPED>(a, g, stream);
+  }
+}
+
+// Weight rows [from, from + count) of a product.
+GemmArgs part_of(GemmArgs a, const BlockGemm& g, int64_t from, int64_t count) {
+  a.codes += from * a.kp;
+  a.scales += from / g.brows * a.kb;
+  a.y = (char*)a.y + from * (g.y_type == QW_BF16 ? 2 : 4);
+  a.n = count;
+  a.nb = (count + g.brows - 1) / g.brows;
+  return a;
+}
+
 }  // namespace
 
 bool block_gemm_fuses(int64_t m, int64_t k) {
-  return m <= 16 && pitch(k) <= kStreamMaxKb * QW_BLOCK;
+  return m <= kFusedMaxM && pitch(k) <= kStreamMaxKb * QW_BLOCK;
 }
 
 hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t stream) {
@@ -737,10 +873,28 @@ hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t stream) {
     return vec ? run_stream<false, true, uint16_t>(a, g, stream)
                : run_stream<false, false, uint16_t>(a, g, stream);
   }
-  if (block_gemm_fuses(g.m, g.k) && a.kb > 0) return run_stream<false, true, uint8_t>(a, g, stream);
-  if (g.m > 128) return run_tiled<8, 4, 2, false>(a, g, stream);
-  if (g.m <= 16) return run_direct<1, 1, 8, false>(a, g, stream);
-  return run_direct<4, 4, 4, false>(a, g, stream);
+  if (g.m <= 16 && a.kb > 0 && a.kb <= kStreamMaxKb)
+    return run_stream<false, true, uint8_t>(a, g, stream);
+  if (g.m <= 16) return run_direct<1, 1, 8, 4, false>(a, g, stream);
+  double cost;
+  const int shape = best_shape(g.n, g.m, 0, a.kb, g.exact, &cost);
+  if (kShapes[shape].tiled) {
+    // the weight rows of whole rounds, and the rest with another shape
+    const Shape& s = kShapes[shape];
+    const int64_t tiles_m = (g.m + s.bm() - 1) / s.bm(), tiles_n = (g.n + s.bn() - 1) / s.bn();
+    const int64_t whole = tiles_m * tiles_n / kUnits * kUnits / tiles_m;
+    if (whole > 0 && whole < tiles_n) {
+      const int64_t cut = whole * s.bn();  // a multiple of 128
+      double rest;
+      const int other = best_shape(g.n - cut, g.m, 0, a.kb, g.exact, &rest);
+      if (cost_of(s, cut, g.m, 0, a.kb, g.exact) + rest + 2.0 < cost) {
+        const hipError_t e = run_shape<false>(shape, part_of(a, g, 0, cut), g, stream);
+        if (e != hipSuccess) return e;
+        return run_shape<false>(other, part_of(a, g, cut, g.n - cut), g, stream);
+      }
+    }
+  }
+  return run_shape<false>(shape, a, g, stream);
 }
 
 hipError_t launch_block_gemm_grouped(const BlockGemm& g, int64_t experts,
@@ -748,10 +902,11 @@ hipError_t launch_block_gemm_grouped(const BlockGemm& g, int64_t experts,
   GemmArgs a = args_of(g);
   a.experts = (int)experts;
   a.offsets = offsets;
+  // an average of 16 rows an expert: each expert's weight is read about once
   if (g.m <= 16 * experts && a.kb > 0 && a.kb <= kStreamMaxKb)
     return run_stream<true, true, uint8_t>(a, g, stream);
-  if (g.m <= 16 * experts) return run_direct<1, 1, 8, true>(a, g, stream);
-  return run_direct<4, 4, 4, true>(a, g, stream);
+  double cost;
+  return run_shape<true>(best_shape(g.n, g.m, experts, a.kb, g.exact, &cost), a, g, stream);
 }
 
 }  // namespace qw

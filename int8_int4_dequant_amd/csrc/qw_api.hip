@@ -466,6 +466,7 @@ int check_block(int brows, int64_t count, int64_t n, int64_t k) {
 
 // x or y side of a product: m rows of n outputs and of k inputs.
 int check_rows(int64_t m, int64_t n, int64_t k) {
+  if (k > QW_BLOCK_MAX_K) return QW_ESHAPE;
   return within(m, n) && within(m, k) && within(m, qw::pitch(k)) ? QW_OK : QW_EM;
 }
 
@@ -718,6 +719,7 @@ struct MlpWork {
 int check_mlp(int64_t t, int64_t topk, int64_t experts, int64_t d, int64_t f) {
   if (topk < 1 || experts < 1 || experts > QW_MOE_MAX_EXPERTS) return QW_EARG;
   if (!within(t, topk, QW_MOE_MAX_SLOTS) || !within(d, 1) || !within(f, 2)) return QW_ESHAPE;
+  if (d > QW_BLOCK_MAX_K || f > QW_BLOCK_MAX_K) return QW_ESHAPE;
   if (!within(t * topk, qw::pitch(d)) || !within(t * topk, 2 * qw::pitch(f))) return QW_ESHAPE;
   return QW_OK;
 }

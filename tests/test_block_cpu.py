@@ -96,7 +96,7 @@ def test_unpack_and_swiglu_refusals():
     (EARG, (1, 8, 128, P + 4, P, 4, P, P, 0, P)), (EARG, (1, 8, 128, P, P, 4, P + 4, P, 0, P)),
     (ESHAPE, (1, -8, 128, P, P, 4, P, P, 0, P)), (ESHAPE, (1, 8, I64, P, P, 4, P, P, 0, P)),
     (EM, (1, 8, 128, P, P, -4, P, P, 0, P)), (EM, (1, 8, 128, P, P, I64, P, P, 0, P)),
-    (EM, (1, 1 << 20, 0, P, P, 1 << 20, P, P, 0, P)),
+    (EM, (1, 1 << 20, 0, P, P, 1 << 20, P, P, 0, P)), (ESHAPE, (1, 8, (1 << 22) + 1, P, P, 4, P, P, 0, P)),
     (ENULL, (1, 8, 128, None, P, 4, P, P, 0, P)), (ENULL, (1, 8, 128, P, None, 4, P, P, 0, P)),
     (ENULL, (1, 8, 128, P, P, 4, None, P, 0, P)), (ENULL, (1, 8, 128, P, P, 4, P, None, 0, P)),
     (ENULL, (1, 8, 128, P, P, 4, P, P, 0, None)), (ENULL, (1, 8, 0, None, None, 4, None, None, 0, None)),
