@@ -281,12 +281,11 @@ hipError_t run_direct(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
 
 // ------------------------------------------------------------ tiled kernel
 //
-// For many rows.  A block of 8 waves computes 16 NF * 2 weight rows x 16 MF * 4
-// tokens, one block of k at a time through two LDS buffers: while the matrix
+// For many rows.  A block of 8 waves, WM of them along the tokens and the rest
+// along the weight rows, each with 16 NF weight rows x 16 MF tokens, one block of k at a time through two LDS buffers: while the matrix
 // cores work on one, the next is copied to the other straight from memory
-// (buffer loads with an LDS target, 16 bytes a lane).  Waves form a grid of 4 along the tokens
-// and 2 along the weight; each keeps its MF token fragments in registers and
-// walks its NF weight fragments.
+// (buffer loads with an LDS target, 16 bytes a lane).  A wave keeps its MF token
+// fragments in registers and walks its NF weight fragments.
 //
 // LDS rows are the 128 bytes of a block.  A phase of a 16-byte LDS read is 16
 // lanes, here 16 consecutive rows at the same place in the row, and the 64
@@ -348,21 +347,22 @@ __device__ __forceinline__ void tile_place(int64_t block, int64_t tiles, int64_t
   tm = band * 8 + in_band - tn * height;
 }
 
-template <int NF, int MF, int STAGES, bool EXACT, bool BROWS1, bool GROUPED, typename YT>
+template <int NF, int MF, int WM, int STAGES, bool EXACT, bool BROWS1, bool GROUPED, typename YT>
 __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
-  constexpr int BN = 32 * NF, BM = 64 * MF, ROWS = BN + BM;
+  constexpr int BN = 16 * NF * (kTileWaves / WM), BM = 16 * MF * WM, ROWS = BN + BM;
+  constexpr int PAIRS = NF * MF / 2;
   constexpr int SEGS = ROWS / 8 / kTileWaves;  // 8-row pieces of a wave
   static_assert(QW_BLOCK % (16 * NF) == 0, "a wave's weight rows lie in one 128 x 128 block");
   static_assert(ROWS / 8 % kTileWaves == 0 && MF % 2 == 0, "whole pieces and pairs");
   // scales of 4 blocks of k at a time (a scale's line of memory holds its
   // row's next ones), of the tile's tokens and then of its rows of blocks
-  constexpr int SROWS = BM + (BROWS1 ? BN : 64);
+  constexpr int SROWS = BM + (BROWS1 ? BN : 64);  // BM: whole pieces of 64
   static_assert(SROWS / 64 <= kTileWaves, "64 rows of scales a wave");
   __shared__ __align__(1024) uint8_t lds[STAGES][ROWS * 128];
   __shared__ __align__(16) float scales[2][4][SROWS];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int wm = (wave & 3) * 16 * MF, wn = (wave >> 2) * 16 * NF;
+  const int wm = wave % WM * 16 * MF, wn = wave / WM * 16 * NF;
   int64_t tm, tn;
   tile_place(blockIdx.x, a.tiles, a.tiles_m, tm, tn);
   const int64_t n0 = tn * BN;
@@ -438,6 +438,20 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
     // matrix cores: d with the scales ps (and psw) is the last pair
     f32x4 d[2] = {}, psw = {};
     float ps[2] = {};
+    // The copies of block b + STAGES - 1, a few pieces with every pair: all at
+    // once they would hold up the reads behind them.
+    constexpr int PER = (SEGS + PAIRS - 1) / PAIRS;
+    auto fetch_with = [&](int b, int buf2, int pair) {
+#pragma unroll
+      for (int p = 0; p < PER; ++p)
+        if (pair * PER + p < SEGS) fetch(b + STAGES - 1, buf2, pair * PER + p);
+    };
+    // Copies on their way when block b + 1 has to be whole, in the last
+    // fragment of block b: all of the blocks b + 2 .. b + STAGES - 2, and as many
+    // pieces of block b + STAGES - 1 as went out with the pairs up to there.
+    constexpr int SENT = ((NF - 1) * (MF / 2) + 1) * PER < SEGS ? ((NF - 1) * (MF / 2) + 1) * PER : SEGS;
+    constexpr int LEFT = (STAGES - 3) * SEGS + SENT;
+    static_assert(LEFT >= 0, "with two buffers the next block's copies all go out before");
     int buf = 0;  // b % STAGES
     for (int b = 0; b < a.kb; ++b) {
       const uint8_t* wl = lds[buf] + wn * 128;
@@ -447,6 +461,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
       f32x4 sw4 = {};
 #pragma unroll
       for (int i = 0; i < NF; ++i) {
+        fetch_with(b, buf2, i * (MF / 2));
         if constexpr (BROWS1) sw4 = *(const f32x4*)&scales[(b >> 2) & 1][b & 3][BM + wn + 16 * i + 4 * q];
         if (i + 1 < NF) {
           wr = lds_fragment(wl, 16 * (i + 1) + r, q);
@@ -455,12 +470,13 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
           // does, the next step fills it again; and the next buffer is whole.
           // Scales of other blocks that are on their way only make the wait
           // longer: they are older than the copies it leaves.
-          landed<(STAGES - 2) * SEGS>();
+          landed<LEFT>();
           wr = lds_fragment(lds[buf1] + wn * 128, r, q);
         }
 #pragma unroll
         for (int j = 0; j < MF; j += 2) {
           f32x4 e[2];
+          if (j > 0) fetch_with(b, buf2, i * (MF / 2) + j / 2);
           dot128x2(wf, &xf[j], e);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -493,10 +509,6 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
             __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x2, EXACT ? 5 : BROWS1 ? 8 : 4, 0);
           }
-          // the next block's copies, a piece with every pair: all at once they
-          // would hold up the reads behind them
-          if (i * (MF / 2) + j / 2 < SEGS)
-            fetch(b + STAGES - 1, buf2, i * (MF / 2) + j / 2);
           __builtin_amdgcn_sched_barrier(0);
           if (i == 0 && j == 0) {
 #pragma unroll
@@ -540,15 +552,15 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
 }
 
 // EXACT: the bf16 cores' instances too.
-template <int NF, int MF, int STAGES, bool EXACT, bool GROUPED>
+template <int NF, int MF, int WM, int STAGES, bool EXACT, bool GROUPED>
 hipError_t run_tiled(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
-  constexpr int BN = 32 * NF, BM = 64 * MF;
+  constexpr int BN = 16 * NF * (kTileWaves / WM), BM = 16 * MF * WM;
   a.tiles_m = GROUPED ? std::min(a.m, (a.m + a.experts * (int64_t)(BM - 1)) / BM)
                       : (a.m + BM - 1) / BM;
   a.tiles = a.tiles_m * ((a.n + BN - 1) / BN);
   a.y_vec = g.n % 4 == 0 && aligned(g.y, g.y_type == QW_BF16 ? 8 : 16);
   auto go = [&](auto exact, auto brows1, auto y) {
-    gemm_tiled<NF, MF, STAGES, decltype(exact)::value, decltype(brows1)::value, GROUPED, decltype(y)>
+    gemm_tiled<NF, MF, WM, STAGES, decltype(exact)::value, decltype(brows1)::value, GROUPED, decltype(y)>
         <<<(unsigned)a.tiles, kTileWaves * 64, 0, stream>>>(a);
   };
   using std::true_type;
@@ -775,17 +787,17 @@ GemmArgs args_of(const BlockGemm& g) {
 //
 // Which kernel and tile: the one with the least estimated time, from what each
 // takes for a round of the 256 compute units.
-//   tiled   a block of k takes `step` us with all units at work: 256 x 256
-//           1.84, 128 x 256 (weight x tokens) 1.07, 256 x 128 1.06, 128 x 128
-//           0.70; on the bf16 cores 1.78 (128 x 256) and 1.16 (128 x 128), the
-//           larger tiles not fitting the registers as well (measured on
-//           8192^3: 470, 550, 540, 700 us and 910, 1180 us).  3 us to start and
-//           to write y.
+//   tiled   a block of k takes `step` us with all units at work (weight rows x
+//           tokens): 256 x 256 1.84, 256 x 128 1.06, 128 x 256 1.07, 128 x 128
+//           0.70, 128 x 64 0.55, 64 x 64 0.40; on the bf16 cores 1.78 (128 x
+//           256), 1.16, 0.84 and 0.62, the larger tiles not fitting the
+//           registers (from 8192^3: 470, 540, 550, 700 us and 910, 1180; 512 x
+//           4096 x 4096: 24.7, 19.7, 23.3 us for the last three; 37, 29, 33).
+//           3 us to start and to write y.
 //   direct  a unit takes in 28 KB of scattered rows a us, and 4 us to start,
-//           to join the sums and to write (64 rows x 4096 x 4096: 13 us with 32 x 32
-//           tiles, 20 with 32 x 64, 20 tiled; 64 x 28672 x 8192: 132, 125,
-//           53; 256 x 4096 x 4096: 41, 35, 20; 32 x 4096 x 4096: 11.5 with
-//           16 x 32, 13 with 32 x 32).
+//           to join the sums and to write (64 x 4096 x 4096: 13 us with 32 x 32
+//           tiles, 16 tiled; 32 x 4096 x 4096: 11.5 with 16 x 32, 13 with 32 x
+//           32; 256 x 4096 x 4096: 41, tiled 16).
 // A tiled product whose last round is only partly filled may be cut in two along
 // the weight rows, the rest with smaller tiles (2048 x 28672 x 8192: 3.5 rounds
 // of 256 x 256, 480 us; 3 rounds and one of 256 x 128, 430 us).
@@ -794,26 +806,24 @@ GemmArgs args_of(const BlockGemm& g) {
 constexpr int kUnits = 256;
 
 struct Shape {
-  int nf, mf;   // fragments of a wave
+  int bn, bm;   // weight rows x tokens of a tile
   bool tiled;
   double step;  // tiled, 8-bit cores
   double exact; // tiled, bf16 cores; 0: not taken
-  int bn() const { return tiled ? 32 * nf : 16 * nf; }
-  int bm() const { return tiled ? 64 * mf : 16 * mf; }
 };
 constexpr Shape kShapes[] = {
-    {8, 4, true, 1.84, 0.0},  {8, 2, true, 1.06, 0.0},  {4, 4, true, 1.07, 1.78},
-    {4, 2, true, 0.70, 1.16}, {2, 4, false, 0.0, 0.0},  {2, 2, false, 0.0, 0.0},
-    {1, 2, false, 0.0, 0.0},
+    {256, 256, true, 1.84, 0.0}, {256, 128, true, 1.06, 0.0},  {128, 256, true, 1.07, 1.78},
+    {128, 128, true, 0.70, 1.16}, {128, 64, true, 0.55, 0.84}, {64, 64, true, 0.40, 0.62},
+    {32, 32, false, 0.0, 0.0},    {16, 32, false, 0.0, 0.0},
 };
 constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
 
 // Estimated us of n weight rows against m rows of x (of `experts` experts).
 double cost_of(const Shape& s, int64_t n, int64_t m, int64_t experts, int kb, bool exact) {
   const int64_t spare = std::min(experts, m) / 2;  // half-empty tiles
-  const double tiles_m = experts ? (double)m / s.bm() + spare + 1 : (double)((m + s.bm() - 1) / s.bm());
-  const double rounds = std::ceil(tiles_m * ((n + s.bn() - 1) / s.bn()) / kUnits);
-  if (!s.tiled) return 4.0 + rounds * (s.bn() + s.bm()) * kb * (QW_BLOCK / 28000.0);
+  const double tiles_m = experts ? (double)m / s.bm + spare + 1 : (double)((m + s.bm - 1) / s.bm);
+  const double rounds = std::ceil(tiles_m * ((n + s.bn - 1) / s.bn) / kUnits);
+  if (!s.tiled) return 4.0 + rounds * (s.bn + s.bm) * kb * (QW_BLOCK / 28000.0);
   const double step = exact ? s.exact : s.step;
   return step == 0.0 ? 1e30 : rounds * (3.0 + kb * step);
 }
@@ -834,15 +844,16 @@ int best_shape(int64_t n, int64_t m, int64_t experts, int kb, bool exact, double
 template <bool GROUPED>
 hipError_t run_shape(int shape, const GemmArgs& a, const BlockGemm& g, hipStream_t stream) {
   // no k, or more tiles than a launch holds: the direct kernel loops over them
-  const int64_t most = (a.m / 128 + a.experts + 1) * (a.n / 128 + 1);
-  if (a.kb == 0 || most > 1 << 22) shape = 4;
+  const int64_t most = (a.m / 64 + a.experts + 1) * (a.n / 64 + 1);
+  if (a.kb == 0 || most > 1 << 22) shape = 6;
   switch (shape) {
-    case 0: return run_tiled<8, 4, 2, false, GROUPED>(a, g, stream);
-    case 1: return run_tiled<8, 2, 3, false, GROUPED>(a, g, stream);
-    case 2: return run_tiled<4, 4, 3, true, GROUPED>(a, g, stream);
-    case 3: return run_tiled<4, 2, 4, true, GROUPED>(a, g, stream);
-    case 4: return run_direct<2, 4, 8, 1, GROUPED>(a, g, stream);
-    case 5: return run_direct<2, 2, 8, 1, GROUPED>(a, g, stream);
+    case 0: return run_tiled<8, 4, 4, 2, false, GROUPED>(a, g, stream);
+    case 1: return run_tiled<8, 2, 4, 3, false, GROUPED>(a, g, stream);
+    case 2: return run_tiled<4, 4, 4, 3, true, GROUPED>(a, g, stream);
+    case 3: return run_tiled<4, 2, 4, 4, true, GROUPED>(a, g, stream);
+    case 4: return run_tiled<2, 2, 2, 4, true, GROUPED>(a, g, stream);
+    case 5: return run_tiled<1, 2, 2, 4, true, GROUPED>(a, g, stream);
+    case 6: return run_direct<2, 2, 8, 1, GROUPED>(a, g, stream);
     default: return run_direct<1, 2, 8, 2, GROUPED>(a, g, stream);
   }
 }
@@ -881,10 +892,10 @@ hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t stream) {
   if (kShapes[shape].tiled) {
     // the weight rows of whole rounds, and the rest with another shape
     const Shape& s = kShapes[shape];
-    const int64_t tiles_m = (g.m + s.bm() - 1) / s.bm(), tiles_n = (g.n + s.bn() - 1) / s.bn();
+    const int64_t tiles_m = (g.m + s.bm - 1) / s.bm, tiles_n = (g.n + s.bn - 1) / s.bn;
     const int64_t whole = tiles_m * tiles_n / kUnits * kUnits / tiles_m;
     if (whole > 0 && whole < tiles_n) {
-      const int64_t cut = whole * s.bn();  // a multiple of 128
+      const int64_t cut = whole * s.bn;  // a multiple of 128
       double rest;
       const int other = best_shape(g.n - cut, g.m, 0, a.kb, g.exact, &rest);
       if (cost_of(s, cut, g.m, 0, a.kb, g.exact) + rest + 2.0 < cost) {
