@@ -90,7 +90,7 @@ __global__ __launch_bounds__(256) void quantize_swiglu(const T* __restrict__ h,
     load8_of_row<VEC>(h + row * 2 * f, j, f, a);
     load8_of_row<VEC>(h + row * 2 * f + f, j, f, b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
+    for (int i = 0; i < 8; ++i) a[i] = gated(a[i], b[i]);
     const float s = block_scale(max16(amax8(a)));
     *(u32x2*)(codes + row * (kb * QW_BLOCK) + j) = codes8(a, s);
     if ((threadIdx.x & 15) == 0) scales[g] = s;

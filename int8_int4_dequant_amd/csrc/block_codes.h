@@ -163,6 +163,20 @@ __device__ __forceinline__ u32x2 codes8(const float v[8], float s) {
                codes4(v[4] / s, v[5] / s, v[6] / s, v[7] / s)};
 }
 
+// exp(x) to about 2 ulp: 2^h with the part of x log2(e) that h has no bits for
+// added in a second step (x in fp32 alone would cost |x| half ulps).
+__device__ __forceinline__ float exp_of(float x) {
+  const float h = x * 0x1.715476p+0f;  // log2(e) to 24 bits, and the rest of it
+  const float l = __builtin_fmaf(x, 0x1.4ae0cp-26f, __builtin_fmaf(x, 0x1.715476p+0f, -h));
+  const float e = __builtin_amdgcn_exp2f(h);
+  return h > 127.0f ? e : __builtin_fmaf(e, l * 0x1.62e43p-1f, e);
+}
+// silu(gate) * up.  The quotient is a product with the hardware reciprocal (1
+// ulp): the result is within a few ulp and is then rounded to 4 bits.
+__device__ __forceinline__ float gated(float gate, float up) {
+  return gate * __builtin_amdgcn_rcpf(1.0f + exp_of(-gate)) * up;
+}
+
 // Thread blocks for `items` of work, `per` to a block: the kernels' loops take
 // what is beyond 2^22 blocks (a launch holds fewer than 2^32 threads).
 inline unsigned grid_for(int64_t items, int per) {

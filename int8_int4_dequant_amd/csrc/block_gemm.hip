@@ -37,10 +37,12 @@ struct GemmArgs {
   const void* x;      // float rows (row length k) or codes (row pitch kp)
   const float* xs;
   void* y;
+  float* ys;          // gated product: y is codes and these are their scales
   const int32_t* offsets;
   int experts;
   int64_t n, k, m;    // n: weight rows of this launch
   int64_t ldy;        // outputs in a row of y
+  int64_t gated;      // gated product: rows of the gate matrix, a multiple of 128
   int64_t kp;
   int kb;             // blocks along k
   int64_t nb;         // rows of scales of one weight
@@ -347,7 +349,15 @@ __device__ __forceinline__ void tile_place(int64_t block, int64_t tiles, int64_t
   tm = band * 8 + in_band - tn * height;
 }
 
-template <int NF, int MF, int WM, int STAGES, bool EXACT, bool BROWS1, bool GROUPED, typename YT>
+//
+// GATED: the weight is a gate and an up matrix of a.gated rows each, one behind
+// the other; the tile is 128 rows of each, and what is written is the quantized
+// silu(gate) * up: a wave's 128 gate rows are one 1 x 128 block of each of its
+// tokens, so half of the tokens' sums change places with the up waves through
+// LDS and every wave scales and rounds half of its tokens.
+
+template <int NF, int MF, int WM, int STAGES, bool EXACT, bool BROWS1, bool GROUPED, bool GATED,
+          typename YT>
 __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
   constexpr int BN = 16 * NF * (kTileWaves / WM), BM = 16 * MF * WM, ROWS = BN + BM;
   constexpr int PAIRS = NF * MF / 2;
@@ -365,21 +375,31 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
   const int wm = wave % WM * 16 * MF, wn = wave / WM * 16 * NF;
   int64_t tm, tn;
   tile_place(blockIdx.x, a.tiles, a.tiles_m, tm, tn);
-  const int64_t n0 = tn * BN;
+  static_assert(!GATED || (NF == 8 && WM == 4), "128 gate rows and 128 up rows");
+  const int64_t n0 = GATED ? tn * QW_BLOCK : tn * BN;
   int64_t m0 = tm * BM, end = min(m0 + BM, a.m);
   int expert = 0;
   if (GROUPED && !grouped_tile(a, tm, BM, expert, m0, end)) return;
   const int kp = (int)a.kp;
   const i32x4 wbuf = buffer_of(a.codes + (expert * a.n + n0) * a.kp,
-                               (uint32_t)(min(a.n - n0, (int64_t)BN) * a.kp));
+                               (uint32_t)(min(a.n - n0, (int64_t)(GATED ? QW_BLOCK : BN)) * a.kp));
+  // GATED: a buffer that starts 128 rows before the up rows, for the tile's rows from 128 on
+  const i32x4 ubuf = buffer_of(a.codes + (expert * a.n + a.gated + n0 - QW_BLOCK) * a.kp,
+                               (uint32_t)(2 * QW_BLOCK * a.kp));
   const i32x4 xbuf = buffer_of((const uint8_t*)a.x + m0 * a.kp, (uint32_t)((end - m0) * a.kp));
   const float* ws = a.scales + expert * a.nb * a.kb;
   const int64_t srow = BROWS1 ? n0 : n0 / QW_BLOCK;
+  const int64_t urows = !GATED ? 0 : BROWS1 ? a.gated : a.gated / QW_BLOCK;  // gate to up
   const i32x4 sbuf = wave * 64 < BM
       ? buffer_of(a.xs + m0 * a.kb, (uint32_t)((end - m0) * a.kb * 4))
       : buffer_of(ws + srow * a.kb,
-                  (uint32_t)(min(a.nb - srow, (int64_t)(BROWS1 ? BN : 2)) * a.kb * 4));
-  const uint32_t soff = (uint32_t)(wave * 64 + lane - (wave * 64 < BM ? 0 : BM)) * a.kb * 4;
+                  (uint32_t)(min(a.nb - srow, urows + (BROWS1 ? BN : 2)) * a.kb * 4));
+  // of the rows of scales behind x's, those from half on are the up matrix's
+  const int srel = wave * 64 + lane - (wave * 64 < BM ? 0 : BM);
+  const int half_rows = BROWS1 ? QW_BLOCK : 1;
+  const uint32_t soff =
+      (uint32_t)(srel + (GATED && wave * 64 >= BM && srel >= half_rows ? urows - half_rows : 0)) *
+      a.kb * 4;
   uint32_t voff[SEGS];
 #pragma unroll
   for (int s = 0; s < SEGS; ++s) {
@@ -394,7 +414,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
   // copy is issued all the same (as zeros, from an empty buffer): a branch
   // would part the products from the scaling that runs beside them.
   auto fetch = [&](int b, int buf, int s) {
-    i32x4 from = s < BN / 64 ? wbuf : xbuf;
+    i32x4 from = s >= BN / 64 ? xbuf : GATED && s >= BN / 128 ? ubuf : wbuf;
     from.z = b < a.kb ? from.z : 0;
     const int seg = wave + kTileWaves * s;
     copy_to_lds(from, voff[s], (uint32_t)b * 128, lds0 + buf * (ROWS * 128) + seg * 1024);
@@ -414,7 +434,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
     float s[MF], sx[MF], sw = 1.0f;
     auto take_scales = [&](int b) {
       const float* sc = scales[(b >> 2) & 1][b & 3];
-      if (!BROWS1) sw = sc[BM + (int)((n0 + wn) / QW_BLOCK - n0 / QW_BLOCK)];
+      if (!BROWS1) sw = sc[BM + (GATED ? wave / WM : (int)((n0 + wn) / QW_BLOCK - n0 / QW_BLOCK))];
 #pragma unroll
       for (int j = 0; j < MF; ++j) sx[j] = sc[wm + 16 * j + r];
     };
@@ -532,6 +552,58 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
         acc[NF - 1][MF - 2 + u][c] = __builtin_fmaf(
             d[u][c], BROWS1 ? ps[u] * psw[c] : ps[u], acc[NF - 1][MF - 2 + u][c]);
   }
+  if constexpr (GATED) {
+    // The LDS ring is free once every copy (the empty ones too) has landed.
+    landed<0>();
+    constexpr int HALF = MF / 2;
+    f32x4* const mine = (f32x4*)&lds[0][0] + ((wave % WM) * 2 + wave / WM) * (NF * HALF * 64) + lane;
+    const f32x4* const other =
+        (const f32x4*)&lds[0][0] + ((wave % WM) * 2 + 1 - wave / WM) * (NF * HALF * 64) + lane;
+    auto exchange = [&](auto up) {
+      constexpr int UP = decltype(up)::value;  // gate waves keep the first tokens, up waves the others
+      static_assert(4 * 2 * NF * HALF * 64 * 16 <= sizeof(lds), "the sums fit the ring");
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < HALF; ++j) mine[(i * HALF + j) * 64] = acc[i][(1 - UP) * HALF + j];
+      landed<0>();
+#pragma unroll
+      for (int j = 0; j < HALF; ++j) {
+        const int64_t row = m0 + wm + 16 * (UP * HALF + j) + r;
+        float v[NF][4], top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+          const f32x4 o = other[(i * HALF + j) * 64];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float m = acc[i][UP * HALF + j][c];
+            v[i][c] = UP ? gated(o[c], m) : gated(m, o[c]);
+            top = fmaxf(top, fabsf(v[i][c]));
+          }
+        }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float scale = block_scale(top);
+        if (row < end) {
+          uint8_t* const to = (uint8_t*)a.y + row * a.gated + n0 + 4 * q;
+#pragma unroll
+          for (int i = 0; i < NF; i += 2) {
+            const float w[8] = {v[i][0], v[i][1], v[i][2], v[i][3],
+                                v[i + 1][0], v[i + 1][1], v[i + 1][2], v[i + 1][3]};
+            const u32x2 c8 = codes8(w, scale);
+            *(uint32_t*)(to + 16 * i) = c8.x;
+            *(uint32_t*)(to + 16 * i + 16) = c8.y;
+          }
+          if (q == 0) a.ys[row * (a.gated / QW_BLOCK) + n0 / QW_BLOCK] = scale;
+        }
+      }
+    };
+    if (wave / WM == 0)
+      exchange(std::integral_constant<int, 0>{});
+    else
+      exchange(std::integral_constant<int, 1>{});
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < MF; ++j) {
     const int64_t row = m0 + wm + 16 * j + r;
@@ -560,8 +632,8 @@ hipError_t run_tiled(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   a.tiles = a.tiles_m * ((a.n + BN - 1) / BN);
   a.y_vec = g.n % 4 == 0 && aligned(g.y, g.y_type == QW_BF16 ? 8 : 16);
   auto go = [&](auto exact, auto brows1, auto y) {
-    gemm_tiled<NF, MF, WM, STAGES, decltype(exact)::value, decltype(brows1)::value, GROUPED, decltype(y)>
-        <<<(unsigned)a.tiles, kTileWaves * 64, 0, stream>>>(a);
+    gemm_tiled<NF, MF, WM, STAGES, decltype(exact)::value, decltype(brows1)::value, GROUPED, false,
+               decltype(y)><<<(unsigned)a.tiles, kTileWaves * 64, 0, stream>>>(a);
   };
   using std::true_type;
   using std::false_type;
@@ -858,6 +930,21 @@ hipError_t run_shape(int shape, const GemmArgs& a, const BlockGemm& g, hipStream
   }
 }
 
+template <int MF, int STAGES>
+hipError_t run_gated(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
+  constexpr int BM = 64 * MF;
+  a.tiles_m = std::min(a.m, (a.m + a.experts * (int64_t)(BM - 1)) / BM);
+  a.tiles = a.tiles_m * (a.gated / QW_BLOCK);
+  const unsigned grid = (unsigned)a.tiles;
+  if (g.brows == 1)
+    gemm_tiled<8, MF, 4, STAGES, false, true, true, true, float>
+        <<<grid, kTileWaves * 64, 0, stream>>>(a);
+  else
+    gemm_tiled<8, MF, 4, STAGES, false, false, true, true, float>
+        <<<grid, kTileWaves * 64, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 // Weight rows [from, from + count) of a product.
 GemmArgs part_of(GemmArgs a, const BlockGemm& g, int64_t from, int64_t count) {
   a.codes += from * a.kp;
@@ -918,6 +1005,25 @@ hipError_t launch_block_gemm_grouped(const BlockGemm& g, int64_t experts,
     return run_stream<true, true, uint8_t>(a, g, stream);
   double cost;
   return run_shape<true>(best_shape(g.n, g.m, experts, a.kb, g.exact, &cost), a, g, stream);
+}
+
+// From 64 rows an expert on the tiles are filled well enough; the blocks of the
+// result have to be blocks of the weight's rows.
+bool block_gemm_gates(int64_t rows, int64_t experts, int64_t f, int64_t k) {
+  return rows > 64 * experts && f % QW_BLOCK == 0 && k > 0 &&
+         (rows / 128 + experts + 1) * (f / QW_BLOCK) <= 1 << 22;
+}
+
+hipError_t launch_block_gemm_gated(const BlockGemm& g, int64_t experts, const int32_t* offsets,
+                                   float* ys, hipStream_t stream) {
+  GemmArgs a = args_of(g);
+  a.experts = (int)experts;
+  a.offsets = offsets;
+  a.gated = g.n / 2;
+  a.ys = ys;
+  const double big = cost_of(kShapes[0], g.n, g.m, experts, a.kb, false);
+  const double small = cost_of(kShapes[1], g.n, g.m, experts, a.kb, false);
+  return big <= small ? run_gated<4, 2>(a, g, stream) : run_gated<2, 3>(a, g, stream);
 }
 
 }  // namespace qw

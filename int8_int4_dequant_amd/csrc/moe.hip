@@ -21,15 +21,14 @@ namespace {
 // bit of the expert number), so equal experts keep the order of their slots.
 
 constexpr int kSortWaves = 16;
-constexpr int kSortOne = 8192;     // slots that one block sorts alone
+constexpr int kSortOne = 4096;     // slots that one block sorts alone
 constexpr int kSortBlocks = 256;   // blocks at most for more of them
 
 // Slots of one block, a multiple of 64 * kSortWaves.
 int64_t sort_run(int64_t slots) {
   const int64_t unit = 64 * kSortWaves;
   if (slots <= kSortOne) return kSortOne;
-  return std::max<int64_t>((slots + kSortBlocks - 1) / kSortBlocks + unit - 1, 4 * unit) / unit *
-         unit;
+  return ((slots + kSortBlocks - 1) / kSortBlocks + unit - 1) / unit * unit;
 }
 
 // The lanes that hold the same id as this one; valid for lanes with `in`.
@@ -91,16 +90,32 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_place(
       atomicAdd(&hist[wave * experts + id], __popcll(same));
   }
   __syncthreads();
-  // thread e: expert e's rows in earlier blocks and in all, then its waves'
+  // Expert e's rows in earlier blocks and in all: 1024 / `span` threads share
+  // the blocks' counts, so that few loads follow each other.
+  __shared__ int rows_before[QW_MOE_MAX_EXPERTS], rows_all[QW_MOE_MAX_EXPERTS];
   const int e = threadIdx.x;
+  if (counts) {
+    for (int i = threadIdx.x; i < experts; i += blockDim.x) rows_before[i] = rows_all[i] = 0;
+    __syncthreads();
+    const int span = 1 << bits, mine_e = threadIdx.x & (span - 1);
+    if (mine_e < experts) {
+      int some = 0, sum = 0;
+#pragma unroll 4
+      for (int b = threadIdx.x >> bits; b < (int)gridDim.x; b += blockDim.x >> bits) {
+        const int c = counts[(int64_t)b * experts + mine_e];
+        some += b < (int)blockIdx.x ? c : 0;
+        sum += c;
+      }
+      atomicAdd(&rows_before[mine_e], some);
+      atomicAdd(&rows_all[mine_e], sum);
+    }
+    __syncthreads();
+  }
   int before = 0, total = 0;
   if (e < experts) {
     if (counts) {
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        const int c = counts[(int64_t)b * experts + e];
-        if (b < (int)blockIdx.x) before += c;
-        total += c;
-      }
+      before = rows_before[e];
+      total = rows_all[e];
     } else {
       for (int w = 0; w < kSortWaves; ++w) total += hist[w * experts + e];
     }

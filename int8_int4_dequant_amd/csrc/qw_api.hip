@@ -708,7 +708,7 @@ struct MlpWork {
     sort = c.take(qw::moe_sort_work_bytes(rows, experts));
     xc = c.take(rows * qw::pitch(d));
     xs = c.take(qw::block_scales(1, rows, d) * 4);
-    h = c.take(rows * 2 * f * 4);
+    h = c.take(qw::block_gemm_gates(rows, experts, f, d) ? 0 : rows * 2 * f * 4);
     hc = c.take(rows * qw::pitch(f));
     hs = c.take(qw::block_scales(1, rows, f) * 4);
     ys = c.take(rows * d * 4);
@@ -761,12 +761,20 @@ int qw_moe_mlp(int block_rows, int64_t experts, int64_t d, int64_t f, const uint
   st = qw_moe_gather_block(t, topk, d, rows, x_type, x, pos, b + at.xc, (float*)(b + at.xs),
                            stream);
   if (st != QW_OK) return st;
-  st = grouped(block_rows, experts, 2 * f, d, gate_up, gate_up_scales, rows, b + at.xc,
-               (const float*)(b + at.xs), offsets, QW_F32, b + at.h, false, stream);
-  if (st != QW_OK) return st;
-  st = qw_block_quantize_swiglu(rows, f, QW_F32, b + at.h, offsets + experts, b + at.hc,
-                                (float*)(b + at.hs), stream);
-  if (st != QW_OK) return st;
+  if (qw::block_gemm_gates(rows, experts, f, d)) {
+    const qw::BlockGemm g = {block_rows, 2 * f, d, rows, gate_up, gate_up_scales, -1, nullptr,
+                             b + at.xc, (const float*)(b + at.xs), QW_F32, b + at.hc, false};
+    st = record(qw::launch_block_gemm_gated(g, experts, offsets, (float*)(b + at.hs),
+                                            (hipStream_t)stream));
+    if (st != QW_OK) return st;
+  } else {
+    st = grouped(block_rows, experts, 2 * f, d, gate_up, gate_up_scales, rows, b + at.xc,
+                 (const float*)(b + at.xs), offsets, QW_F32, b + at.h, false, stream);
+    if (st != QW_OK) return st;
+    st = qw_block_quantize_swiglu(rows, f, QW_F32, b + at.h, offsets + experts, b + at.hc,
+                                  (float*)(b + at.hs), stream);
+    if (st != QW_OK) return st;
+  }
   st = grouped(block_rows, experts, d, f, down, down_scales, rows, b + at.hc,
                (const float*)(b + at.hs), offsets, QW_F32, b + at.ys, false, stream);
   if (st != QW_OK) return st;

@@ -93,6 +93,12 @@ struct BlockGemm {
 hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t stream);
 hipError_t launch_block_gemm_grouped(const BlockGemm& g, int64_t experts,
                                      const int32_t* offsets, hipStream_t stream);
+// The grouped product with a weight of gate rows and then as many up rows (g.n
+// in all), as codes of silu(gate) * up in g.y and their 1 x 128 scales in ys:
+// for sizes that block_gemm_gates takes.
+bool block_gemm_gates(int64_t rows, int64_t experts, int64_t f, int64_t k);
+hipError_t launch_block_gemm_gated(const BlockGemm& g, int64_t experts, const int32_t* offsets,
+                                   float* ys, hipStream_t stream);
 
 // Tokens sorted by expert and back (moe.hip).
 int64_t moe_sort_work_bytes(int64_t slots, int64_t experts);
