@@ -296,6 +296,7 @@ hipError_t run_direct(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
 // the lanes fetch the pieces in that order from memory.
 
 constexpr int kTileWaves = 8;
+constexpr int kUnits = 256;  // compute units
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -326,6 +327,12 @@ __device__ __forceinline__ void landed() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "i"(LEFT) : "memory");
 }
 
+// This wave's LDS accesses are done, and so are the block's; copies stay on
+// their way.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 __device__ __forceinline__ i32x8 lds_fragment(const uint8_t* lds, int row, int q) {
   const int sw = (row >> 1) & 7;
   const u32x4 lo = *(const u32x4*)(lds + row * 128 + ((q ^ sw) << 4));
@@ -354,7 +361,10 @@ __device__ __forceinline__ void tile_place(int64_t block, int64_t tiles, int64_t
 // the other; the tile is 128 rows of each, and what is written is the quantized
 // silu(gate) * up: a wave's 128 gate rows are one 1 x 128 block of each of its
 // tokens, so half of the tokens' sums change places with the up waves through
-// LDS and every wave scales and rounds half of its tokens.
+// LDS and every wave scales and rounds half of its tokens.  A block takes tile
+// after tile and has the next one's first copies on their way while it writes its
+// results (24594 rows of 60 experts, 16 blocks of k: 284 -> 267 us; the other
+// products, whose results take less work, lose by it: 4096^3 63 -> 67).
 
 template <int NF, int MF, int WM, int STAGES, bool EXACT, bool BROWS1, bool GROUPED, bool GATED,
           typename YT>
@@ -373,27 +383,39 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wm = wave % WM * 16 * MF, wn = wave / WM * 16 * NF;
-  int64_t tm, tn;
-  tile_place(blockIdx.x, a.tiles, a.tiles_m, tm, tn);
-  static_assert(!GATED || (NF == 8 && WM == 4), "128 gate rows and 128 up rows");
-  const int64_t n0 = GATED ? tn * QW_BLOCK : tn * BN;
-  int64_t m0 = tm * BM, end = min(m0 + BM, a.m);
-  int expert = 0;
-  if (GROUPED && !grouped_tile(a, tm, BM, expert, m0, end)) return;
+  static_assert(!GATED || (NF == 8 && MF == 2 && WM == 4), "128 gate rows and 128 up rows");
   const int kp = (int)a.kp;
-  const i32x4 wbuf = buffer_of(a.codes + (expert * a.n + n0) * a.kp,
-                               (uint32_t)(min(a.n - n0, (int64_t)(GATED ? QW_BLOCK : BN)) * a.kp));
-  // GATED: a buffer that starts 128 rows before the up rows, for the tile's rows from 128 on
-  const i32x4 ubuf = buffer_of(a.codes + (expert * a.n + a.gated + n0 - QW_BLOCK) * a.kp,
-                               (uint32_t)(2 * QW_BLOCK * a.kp));
-  const i32x4 xbuf = buffer_of((const uint8_t*)a.x + m0 * a.kp, (uint32_t)((end - m0) * a.kp));
-  const float* ws = a.scales + expert * a.nb * a.kb;
-  const int64_t srow = BROWS1 ? n0 : n0 / QW_BLOCK;
   const int64_t urows = !GATED ? 0 : BROWS1 ? a.gated : a.gated / QW_BLOCK;  // gate to up
-  const i32x4 sbuf = wave * 64 < BM
-      ? buffer_of(a.xs + m0 * a.kb, (uint32_t)((end - m0) * a.kb * 4))
-      : buffer_of(ws + srow * a.kb,
-                  (uint32_t)(min(a.nb - srow, urows + (BROWS1 ? BN : 2)) * a.kb * 4));
+  // One tile: what it computes, and the buffers it reads.
+  struct Place {
+    int64_t n0, m0, end;
+    i32x4 wbuf, ubuf, xbuf, sbuf;
+  };
+  // The first tile at or behind `at` (in steps of the grid) that has rows.
+  auto place = [&](int64_t& at, Place& p) {
+    for (; at < a.tiles; at += gridDim.x) {
+      int64_t tm, tn;
+      tile_place(at, a.tiles, a.tiles_m, tm, tn);
+      p.n0 = GATED ? tn * QW_BLOCK : tn * BN;
+      p.m0 = tm * BM;
+      p.end = min(p.m0 + BM, a.m);
+      int expert = 0;
+      if (GROUPED && !grouped_tile(a, tm, BM, expert, p.m0, p.end)) continue;
+      p.wbuf = buffer_of(a.codes + (expert * a.n + p.n0) * a.kp,
+                         (uint32_t)(min(a.n - p.n0, (int64_t)(GATED ? QW_BLOCK : BN)) * a.kp));
+      // GATED: from 128 rows before the up rows, for the tile's rows from 128 on
+      p.ubuf = buffer_of(a.codes + (expert * a.n + a.gated + p.n0 - QW_BLOCK) * a.kp,
+                         (uint32_t)(2 * QW_BLOCK * a.kp));
+      p.xbuf = buffer_of((const uint8_t*)a.x + p.m0 * a.kp, (uint32_t)((p.end - p.m0) * a.kp));
+      const int64_t srow = BROWS1 ? p.n0 : p.n0 / QW_BLOCK;
+      p.sbuf = wave * 64 < BM
+          ? buffer_of(a.xs + p.m0 * a.kb, (uint32_t)((p.end - p.m0) * a.kb * 4))
+          : buffer_of(a.scales + (expert * a.nb + srow) * a.kb,
+                      (uint32_t)(min(a.nb - srow, urows + (BROWS1 ? BN : 2)) * a.kb * 4));
+      return true;
+    }
+    return false;
+  };
   // of the rows of scales behind x's, those from half on are the up matrix's
   const int srel = wave * 64 + lane - (wave * 64 < BM ? 0 : BM);
   const int half_rows = BROWS1 ? QW_BLOCK : 1;
@@ -413,38 +435,49 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
   // Piece s of block b.  Behind the last block there is nothing to read, but the
   // copy is issued all the same (as zeros, from an empty buffer): a branch
   // would part the products from the scaling that runs beside them.
-  auto fetch = [&](int b, int buf, int s) {
-    i32x4 from = s >= BN / 64 ? xbuf : GATED && s >= BN / 128 ? ubuf : wbuf;
+  auto fetch = [&](const Place& p, int b, int buf, int s) {
+    i32x4 from = s >= BN / 64 ? p.xbuf : GATED && s >= BN / 128 ? p.ubuf : p.wbuf;
     from.z = b < a.kb ? from.z : 0;
     const int seg = wave + kTileWaves * s;
     copy_to_lds(from, voff[s], (uint32_t)b * 128, lds0 + buf * (ROWS * 128) + seg * 1024);
   };
-  f32x4 acc[NF][MF] = {};
-  if (a.kb > 0) {
-    auto fetch_scales = [&](int b) {  // of the 4 blocks from b on
-      if (wave < SROWS / 64) {
+  auto fetch_scales = [&](const Place& p, int b) {  // of the 4 blocks from b on
+    if (wave < SROWS / 64) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          copy4_to_lds(sbuf, soff, (uint32_t)(b + c) * 4,
-                       lds1 + (((b >> 2) & 1) * 4 + c) * (SROWS * 4) + wave * 256);
-      }
-    };
+      for (int c = 0; c < 4; ++c)
+        copy4_to_lds(p.sbuf, soff, (uint32_t)(b + c) * 4,
+                     lds1 + (((b >> 2) & 1) * 4 + c) * (SROWS * 4) + wave * 256);
+    }
+  };
+  auto fetch_first = [&](const Place& p) {  // what a tile's first step takes, and more
+    fetch_scales(p, 0);
+#pragma unroll
+    for (int c = 0; c < STAGES - 1; ++c)
+#pragma unroll
+      for (int s = 0; s < SEGS; ++s) fetch(p, c, c, s);
+  };
+
+  // GATED: tile after tile, the next one's first copies on their way while this
+  // one's results are written.
+  int64_t at = blockIdx.x;
+  Place p;
+  if (!place(at, p)) return;
+  fetch_first(p);
+  for (;;) {
+    int64_t at2 = at + gridDim.x;
+    Place p2;
+    const bool more = GATED && place(at2, p2);
+    landed<0>();
+    f32x4 acc[NF][MF] = {};
     // The scales that block b's products are multiplied with: read from LDS
     // with the first fragments, joined behind the first products.
     float s[MF], sx[MF], sw = 1.0f;
     auto take_scales = [&](int b) {
       const float* sc = scales[(b >> 2) & 1][b & 3];
-      if (!BROWS1) sw = sc[BM + (GATED ? wave / WM : (int)((n0 + wn) / QW_BLOCK - n0 / QW_BLOCK))];
+      if (!BROWS1) sw = sc[BM + (GATED ? wave / WM : (int)((p.n0 + wn) / QW_BLOCK - p.n0 / QW_BLOCK))];
 #pragma unroll
       for (int j = 0; j < MF; ++j) sx[j] = sc[wm + 16 * j + r];
     };
-    fetch_scales(0);
-#pragma unroll
-    for (int c = 0; c < STAGES - 1; ++c)
-#pragma unroll
-      for (int p = 0; p < SEGS; ++p)
-        fetch(c, c, p);
-    landed<0>();
     take_scales(0);
     i32x8 xr[MF];    // token fragments as they are read, and as the products take them
     Frag<EXACT> xf[MF];
@@ -463,8 +496,8 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
     constexpr int PER = (SEGS + PAIRS - 1) / PAIRS;
     auto fetch_with = [&](int b, int buf2, int pair) {
 #pragma unroll
-      for (int p = 0; p < PER; ++p)
-        if (pair * PER + p < SEGS) fetch(b + STAGES - 1, buf2, pair * PER + p);
+      for (int c = 0; c < PER; ++c)
+        if (pair * PER + c < SEGS) fetch(p, b + STAGES - 1, buf2, pair * PER + c);
     };
     // Copies on their way when block b + 1 has to be whole, in the last
     // fragment of block b: all of the blocks b + 2 .. b + STAGES - 2, and as many
@@ -477,7 +510,7 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
       const uint8_t* wl = lds[buf] + wn * 128;
       const int buf1 = buf + 1 < STAGES ? buf + 1 : 0;    // of block b + 1
       const int buf2 = buf > 0 ? buf - 1 : STAGES - 1;    // of block b + STAGES - 1
-      if ((b & 3) == 0 && b + 4 < a.kb) fetch_scales(b + 4);
+      if ((b & 3) == 0 && b + 4 < a.kb) fetch_scales(p, b + 4);
       f32x4 sw4 = {};
 #pragma unroll
       for (int i = 0; i < NF; ++i) {
@@ -551,41 +584,43 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
       for (int c = 0; c < 4; ++c)
         acc[NF - 1][MF - 2 + u][c] = __builtin_fmaf(
             d[u][c], BROWS1 ? ps[u] * psw[c] : ps[u], acc[NF - 1][MF - 2 + u][c]);
-  }
-  if constexpr (GATED) {
-    // The LDS ring is free once every copy (the empty ones too) has landed.
+    // All is read, and every copy has landed, the empty ones too: the ring is free.
     landed<0>();
-    constexpr int HALF = MF / 2;
-    f32x4* const mine = (f32x4*)&lds[0][0] + ((wave % WM) * 2 + wave / WM) * (NF * HALF * 64) + lane;
-    const f32x4* const other =
-        (const f32x4*)&lds[0][0] + ((wave % WM) * 2 + 1 - wave / WM) * (NF * HALF * 64) + lane;
-    auto exchange = [&](auto up) {
-      constexpr int UP = decltype(up)::value;  // gate waves keep the first tokens, up waves the others
-      static_assert(4 * 2 * NF * HALF * 64 * 16 <= sizeof(lds), "the sums fit the ring");
-#pragma unroll
-      for (int i = 0; i < NF; ++i)
-#pragma unroll
-        for (int j = 0; j < HALF; ++j) mine[(i * HALF + j) * 64] = acc[i][(1 - UP) * HALF + j];
-      landed<0>();
-#pragma unroll
-      for (int j = 0; j < HALF; ++j) {
-        const int64_t row = m0 + wm + 16 * (UP * HALF + j) + r;
+    if (more) fetch_first(p2);
+    if constexpr (GATED) {
+      // 4 of the 8 fragments at a time change places in the last of the buffers,
+      // which the first copies leave free.
+      f32x4* const mine =
+          (f32x4*)&lds[STAGES - 1][0] + ((wave % WM) * 2 + wave / WM) * (4 * 64) + lane;
+      const f32x4* const other =
+          (const f32x4*)&lds[STAGES - 1][0] + ((wave % WM) * 2 + 1 - wave / WM) * (4 * 64) + lane;
+      static_assert(kTileWaves * 4 * 64 * 16 <= ROWS * 128, "they fit one buffer");
+      auto exchange = [&](auto up) {
+        constexpr int UP = decltype(up)::value;  // gate waves keep the first tokens, up waves the others
+        const int64_t row = p.m0 + wm + 16 * UP + r;
         float v[NF][4], top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NF; ++i) {
-          const f32x4 o = other[(i * HALF + j) * 64];
+        for (int h = 0; h < NF; h += 4) {
+          if (h > 0) lds_barrier();  // the first ones have been read
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float m = acc[i][UP * HALF + j][c];
-            v[i][c] = UP ? gated(o[c], m) : gated(m, o[c]);
-            top = fmaxf(top, fabsf(v[i][c]));
+          for (int i = 0; i < 4; ++i) mine[i * 64] = acc[h + i][1 - UP];
+          lds_barrier();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 o = other[i * 64];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float m = acc[h + i][UP][c];
+              v[h + i][c] = UP ? gated(o[c], m) : gated(m, o[c]);
+              top = fmaxf(top, fabsf(v[h + i][c]));
+            }
           }
         }
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         const float scale = block_scale(top);
-        if (row < end) {
-          uint8_t* const to = (uint8_t*)a.y + row * a.gated + n0 + 4 * q;
+        if (row < p.end) {
+          uint8_t* const to = (uint8_t*)a.y + row * a.gated + p.n0 + 4 * q;
 #pragma unroll
           for (int i = 0; i < NF; i += 2) {
             const float w[8] = {v[i][0], v[i][1], v[i][2], v[i][3],
@@ -594,32 +629,35 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
             *(uint32_t*)(to + 16 * i) = c8.x;
             *(uint32_t*)(to + 16 * i + 16) = c8.y;
           }
-          if (q == 0) a.ys[row * (a.gated / QW_BLOCK) + n0 / QW_BLOCK] = scale;
+          if (q == 0) a.ys[row * (a.gated / QW_BLOCK) + p.n0 / QW_BLOCK] = scale;
+        }
+      };
+      if (wave / WM == 0)
+        exchange(std::integral_constant<int, 0>{});
+      else
+        exchange(std::integral_constant<int, 1>{});
+    } else {
+#pragma unroll
+      for (int j = 0; j < MF; ++j) {
+        const int64_t row = p.m0 + wm + 16 * j + r;
+        if (row >= p.end) continue;
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+          const int64_t col = p.n0 + wn + 16 * i + 4 * q;
+          YT* y = (YT*)a.y + row * a.ldy + col;
+          if (a.y_vec) {
+            if (col < a.n) store4(y, acc[i][j]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (col + c < a.n) store1(y + c, acc[i][j][c]);
+          }
         }
       }
-    };
-    if (wave / WM == 0)
-      exchange(std::integral_constant<int, 0>{});
-    else
-      exchange(std::integral_constant<int, 1>{});
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < MF; ++j) {
-    const int64_t row = m0 + wm + 16 * j + r;
-    if (row >= end) continue;
-#pragma unroll
-    for (int i = 0; i < NF; ++i) {
-      const int64_t col = n0 + wn + 16 * i + 4 * q;
-      YT* y = (YT*)a.y + row * a.ldy + col;
-      if (a.y_vec) {
-        if (col < a.n) store4(y, acc[i][j]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (col + c < a.n) store1(y + c, acc[i][j][c]);
-      }
     }
+    if (!more) return;
+    at = at2;
+    p = p2;
   }
 }
 
@@ -630,10 +668,11 @@ hipError_t run_tiled(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   a.tiles_m = GROUPED ? std::min(a.m, (a.m + a.experts * (int64_t)(BM - 1)) / BM)
                       : (a.m + BM - 1) / BM;
   a.tiles = a.tiles_m * ((a.n + BN - 1) / BN);
+  const unsigned grid = (unsigned)a.tiles;
   a.y_vec = g.n % 4 == 0 && aligned(g.y, g.y_type == QW_BF16 ? 8 : 16);
   auto go = [&](auto exact, auto brows1, auto y) {
     gemm_tiled<NF, MF, WM, STAGES, decltype(exact)::value, decltype(brows1)::value, GROUPED, false,
-               decltype(y)><<<(unsigned)a.tiles, kTileWaves * 64, 0, stream>>>(a);
+               decltype(y)><<<grid, kTileWaves * 64, 0, stream>>>(a);
   };
   using std::true_type;
   using std::false_type;
@@ -783,7 +822,7 @@ __global__ __launch_bounds__(WV * 64) void gemm_stream(GemmArgs a) {
     *(f32x4*)&part[buf][wave][r][4 * q] = acc;
     // The weight's loads stay on their way.  One barrier a tile: the other
     // buffer is written next, and read no later than the next barrier.
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    lds_barrier();
     const int t = threadIdx.x >> 4, c = threadIdx.x & 15;
     if (t < 16 && m0 + t < end && tile * 16 + c < a.n) {
       float sum = part[buf][0][t][c];
@@ -875,8 +914,6 @@ GemmArgs args_of(const BlockGemm& g) {
 // of 256 x 256, 480 us; 3 rounds and one of 256 x 128, 430 us).
 // Grouped: an expert's last tile is half empty on average.
 
-constexpr int kUnits = 256;
-
 struct Shape {
   int bn, bm;   // weight rows x tokens of a tile
   bool tiled;
@@ -930,17 +967,16 @@ hipError_t run_shape(int shape, const GemmArgs& a, const BlockGemm& g, hipStream
   }
 }
 
-template <int MF, int STAGES>
 hipError_t run_gated(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
-  constexpr int BM = 64 * MF;
+  constexpr int BM = 128;
   a.tiles_m = std::min(a.m, (a.m + a.experts * (int64_t)(BM - 1)) / BM);
   a.tiles = a.tiles_m * (a.gated / QW_BLOCK);
-  const unsigned grid = (unsigned)a.tiles;
+  const unsigned grid = (unsigned)std::min<int64_t>(a.tiles, kUnits);
   if (g.brows == 1)
-    gemm_tiled<8, MF, 4, STAGES, false, true, true, true, float>
+    gemm_tiled<8, 2, 4, 3, false, true, true, true, float>
         <<<grid, kTileWaves * 64, 0, stream>>>(a);
   else
-    gemm_tiled<8, MF, 4, STAGES, false, false, true, true, float>
+    gemm_tiled<8, 2, 4, 3, false, false, true, true, float>
         <<<grid, kTileWaves * 64, 0, stream>>>(a);
   return hipGetLastError();
 }
@@ -1021,9 +1057,7 @@ hipError_t launch_block_gemm_gated(const BlockGemm& g, int64_t experts, const in
   a.offsets = offsets;
   a.gated = g.n / 2;
   a.ys = ys;
-  const double big = cost_of(kShapes[0], g.n, g.m, experts, a.kb, false);
-  const double small = cost_of(kShapes[1], g.n, g.m, experts, a.kb, false);
-  return big <= small ? run_gated<4, 2>(a, g, stream) : run_gated<2, 3>(a, g, stream);
+  return run_gated(a, g, stream);
 }
 
 }  // namespace qw
