@@ -11,7 +11,9 @@
 namespace qw {
 namespace {
 
-// 1 x 128 blocks: 16 blocks to a thread block, numbered along the rows.
+// 1 x 128 blocks: 16 blocks to a thread block, numbered along the rows.  (4 times
+// as many with their loads on the way together: 17 us for 2048 x 8192 bf16
+// instead of 14.)
 template <bool VEC, typename T>
 __global__ __launch_bounds__(256) void quantize_rows(const T* __restrict__ w,
                                                      uint8_t* __restrict__ codes,

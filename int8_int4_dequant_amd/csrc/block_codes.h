@@ -57,17 +57,31 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
   *(u32x2*)p = u32x2{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3])};
 }
 
-// 8 consecutive elements at a 16-byte aligned address.
+template <bool NT, typename V>
+__device__ __forceinline__ V load_as(const void* p) {
+  return NT ? __builtin_nontemporal_load((const V*)p) : *(const V*)p;
+}
+template <bool NT, typename V>
+__device__ __forceinline__ void store_as(void* p, V v) {
+  if (NT)
+    __builtin_nontemporal_store(v, (V*)p);
+  else
+    *(V*)p = v;
+}
+
+// 8 consecutive elements at a 16-byte aligned address; NT: past the caches.
+template <bool NT = false>
 __device__ __forceinline__ void load8(const float* p, float v[8]) {
-  const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
+  const f32x4 a = load_as<NT, f32x4>(p), b = load_as<NT, f32x4>(p + 4);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[i] = a[i];
     v[4 + i] = b[i];
   }
 }
+template <bool NT = false>
 __device__ __forceinline__ void load8(const uint16_t* p, float v[8]) {
-  const u32x4 a = *(const u32x4*)p;
+  const u32x4 a = load_as<NT, u32x4>(p);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = bf16_lo(a[i]);
@@ -77,11 +91,11 @@ __device__ __forceinline__ void load8(const uint16_t* p, float v[8]) {
 
 // Elements [j, j + 8) of a row of k, zero from k on; VEC: the row is 16-byte
 // aligned and k % 8 == 0, so the 8 are all there or none is.
-template <bool VEC, typename T>
+template <bool VEC, bool NT = false, typename T>
 __device__ __forceinline__ void load8_of_row(const T* row, int64_t j, int64_t k, float v[8]) {
   if constexpr (VEC) {
     if (j < k) {
-      load8(row + j, v);
+      load8<NT>(row + j, v);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = 0.0f;
@@ -93,18 +107,20 @@ __device__ __forceinline__ void load8_of_row(const T* row, int64_t j, int64_t k,
 }
 
 // The same for a store.
+template <bool NT = false>
 __device__ __forceinline__ void store8(float* p, const float v[8]) {
-  *(f32x4*)p = f32x4{v[0], v[1], v[2], v[3]};
-  *(f32x4*)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  store_as<NT>(p, f32x4{v[0], v[1], v[2], v[3]});
+  store_as<NT>(p + 4, f32x4{v[4], v[5], v[6], v[7]});
 }
+template <bool NT = false>
 __device__ __forceinline__ void store8(uint16_t* p, const float v[8]) {
-  *(u32x4*)p = u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
-                     to_bf16x2(v[6], v[7])};
+  store_as<NT>(p, u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
+                        to_bf16x2(v[6], v[7])});
 }
-template <bool VEC, typename T>
+template <bool VEC, bool NT = false, typename T>
 __device__ __forceinline__ void store8_of_row(T* row, int64_t j, int64_t k, const float v[8]) {
   if constexpr (VEC) {
-    if (j < k) store8(row + j, v);
+    if (j < k) store8<NT>(row + j, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)

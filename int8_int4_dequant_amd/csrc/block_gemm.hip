@@ -37,6 +37,8 @@ struct GemmArgs {
   const void* x;      // float rows (row length k) or codes (row pitch kp)
   const float* xs;
   void* y;
+  const int32_t* order;  // Source TOKENS: slot of a row, and slots of a token
+  int topk;
   float* ys;          // gated product: y is codes and these are their scales
   const int32_t* offsets;
   int experts;
@@ -700,10 +702,17 @@ hipError_t run_tiled(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
 // LDS, once per 16 rows.  Float x costs each block one pass over its own rows
 // of x instead of a launch.
 
+// Where the float values of a row of x come from.
+enum Source {
+  ROWS,    // x [rows][k]
+  TOKENS,  // x [tokens][k], a row is that of its slot's token (order, topk)
+  GATES,   // x [rows][2 k], a row is silu of its first half times its second
+};
+
 // This wave's part of float x as fragments: 16 lanes quantize a block of k of a
-// token, as quantize_rows does, 4 tokens and 2 blocks at a time; the codes
-// change lanes through 4 KiB of LDS of the wave's own.
-template <int KPW, bool VEC, typename T>
+// row, as quantize_rows does, 4 rows and 2 blocks at a time; the codes change
+// lanes through 4 KiB of LDS of the wave's own.
+template <int KPW, Source SRC, bool VEC, typename T>
 __device__ __forceinline__ void quantize_part(const GemmArgs& a, int64_t m0, int64_t end, int k0,
                                               uint8_t (*lds)[16][128], float (*scale)[16],
                                               int lane, i32x8* xf, float* sx) {
@@ -712,11 +721,20 @@ __device__ __forceinline__ void quantize_part(const GemmArgs& a, int64_t m0, int
   for (int g = 0; g < KPW; g += 2) {
     constexpr int W = 2;
     for (int64_t row = m0 + q; row - q < end; row += 4) {
+      int64_t from = min(row, end - 1);
+      if (SRC == TOKENS) from = max(a.order[from], 0) / a.topk;
+      const T* x = (const T*)a.x + from * (SRC == GATES ? 2 * a.k : a.k);
       float v[W][8];
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         const int64_t j = (int64_t)(k0 + g + i) * QW_BLOCK + r * 8;
-        load8_of_row<VEC>((const T*)a.x + min(row, end - 1) * a.k, j, a.k, v[i]);
+        load8_of_row<VEC>(x, j, a.k, v[i]);
+        if constexpr (SRC == GATES) {
+          float up[8];
+          load8_of_row<VEC>(x + a.k, j, a.k, up);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[i][c] = gated(v[i][c], up[c]);
+        }
       }
 #pragma unroll
       for (int i = 0; i < W; ++i) {
@@ -733,8 +751,8 @@ __device__ __forceinline__ void quantize_part(const GemmArgs& a, int64_t m0, int
   }
 }
 
-template <int KPW, int WV, bool EXACT, bool BROWS1, bool GROUPED, bool VEC, typename XT,
-          typename YT>
+template <int KPW, int WV, bool EXACT, bool BROWS1, bool GROUPED, Source SRC, bool VEC,
+          typename XT, typename YT>
 __global__ __launch_bounds__(WV * 64) void gemm_stream(GemmArgs a) {
   __shared__ __align__(16) float part[2][WV][16][20];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -786,7 +804,7 @@ __global__ __launch_bounds__(WV * 64) void gemm_stream(GemmArgs a) {
     constexpr int W = 2;
     __shared__ __align__(16) uint8_t codes[WV][W][16][128];
     __shared__ float scale[WV][W][16];
-    quantize_part<KPW, VEC, XT>(a, m0, end, k0, codes[wave], scale[wave], lane, xf, sx);
+    quantize_part<KPW, SRC, VEC, XT>(a, m0, end, k0, codes[wave], scale[wave], lane, xf, sx);
   }
   const bool have = m0 + r < end;
 #pragma unroll
@@ -838,7 +856,7 @@ __global__ __launch_bounds__(WV * 64) void gemm_stream(GemmArgs a) {
 
 constexpr int kStreamWaves = 8;
 
-template <int KPW, bool GROUPED, bool VEC, typename XT>
+template <int KPW, bool GROUPED, Source SRC, bool VEC, typename XT>
 hipError_t run_stream(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   a.tiles_m = GROUPED ? std::min(a.m, (a.m + a.experts * (int64_t)15) / 16) : (a.m + 15) / 16;
   const int64_t tiles_n = (a.n + 15) / 16;
@@ -847,18 +865,22 @@ hipError_t run_stream(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   a.chunks = std::min(tiles_n, std::max<int64_t>(1, (want + a.tiles_m - 1) / a.tiles_m));
   const unsigned grid = (unsigned)(a.chunks * a.tiles_m);
   auto go = [&](auto exact, auto brows1, auto y) {
-    gemm_stream<KPW, kStreamWaves, decltype(exact)::value, decltype(brows1)::value, GROUPED, VEC,
-                XT, decltype(y)><<<grid, kStreamWaves * 64, 0, stream>>>(a);
+    gemm_stream<KPW, kStreamWaves, decltype(exact)::value, decltype(brows1)::value, GROUPED, SRC,
+                VEC, XT, decltype(y)><<<grid, kStreamWaves * 64, 0, stream>>>(a);
   };
   using std::true_type;
   using std::false_type;
   const bool one = g.brows == 1;
-  if (g.y_type == QW_BF16)
-    one ? go(false_type{}, true_type{}, uint16_t{}) : go(false_type{}, false_type{}, uint16_t{});
-  else if (g.exact)
-    one ? go(true_type{}, true_type{}, 0.0f) : go(true_type{}, false_type{}, 0.0f);
-  else if constexpr (GROUPED)
-    one ? go(false_type{}, true_type{}, 0.0f) : go(false_type{}, false_type{}, 0.0f);
+  if constexpr (!GROUPED || is_codes<XT>::value) {
+    if (g.y_type == QW_BF16)
+      one ? go(false_type{}, true_type{}, uint16_t{}) : go(false_type{}, false_type{}, uint16_t{});
+    else if (g.exact)
+      one ? go(true_type{}, true_type{}, 0.0f) : go(true_type{}, false_type{}, 0.0f);
+  }
+  if constexpr (GROUPED) {
+    if (g.y_type == QW_F32 && !g.exact)
+      one ? go(false_type{}, true_type{}, 0.0f) : go(false_type{}, false_type{}, 0.0f);
+  }
   return hipGetLastError();
 }
 
@@ -869,13 +891,13 @@ constexpr int kFusedMaxM = 8;
 // Most blocks of k that the stream kernel's waves hold.
 constexpr int kStreamMaxKb = 12 * kStreamWaves;
 
-template <bool GROUPED, bool VEC, typename XT>
+template <bool GROUPED, Source SRC, bool VEC, typename XT>
 hipError_t run_stream(const GemmArgs& a, const BlockGemm& g, hipStream_t stream) {
   const int each = (a.kb + kStreamWaves - 1) / kStreamWaves;
-  if (each <= 2) return run_stream<2, GROUPED, VEC, XT>(a, g, stream);
-  if (each <= 4) return run_stream<4, GROUPED, VEC, XT>(a, g, stream);
-  if (each <= 8) return run_stream<8, GROUPED, VEC, XT>(a, g, stream);
-  return run_stream<12, GROUPED, VEC, XT>(a, g, stream);
+  if (each <= 2) return run_stream<2, GROUPED, SRC, VEC, XT>(a, g, stream);
+  if (each <= 4) return run_stream<4, GROUPED, SRC, VEC, XT>(a, g, stream);
+  if (each <= 8) return run_stream<8, GROUPED, SRC, VEC, XT>(a, g, stream);
+  return run_stream<12, GROUPED, SRC, VEC, XT>(a, g, stream);
 }
 
 GemmArgs args_of(const BlockGemm& g) {
@@ -1002,13 +1024,13 @@ hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t stream) {
   if (g.x_type >= 0) {
     const bool vec = g.k % 8 == 0 && aligned(g.x, 16);
     if (g.x_type == QW_F32)
-      return vec ? run_stream<false, true, float>(a, g, stream)
-                 : run_stream<false, false, float>(a, g, stream);
-    return vec ? run_stream<false, true, uint16_t>(a, g, stream)
-               : run_stream<false, false, uint16_t>(a, g, stream);
+      return vec ? run_stream<false, ROWS, true, float>(a, g, stream)
+                 : run_stream<false, ROWS, false, float>(a, g, stream);
+    return vec ? run_stream<false, ROWS, true, uint16_t>(a, g, stream)
+               : run_stream<false, ROWS, false, uint16_t>(a, g, stream);
   }
   if (g.m <= 16 && a.kb > 0 && a.kb <= kStreamMaxKb)
-    return run_stream<false, true, uint8_t>(a, g, stream);
+    return run_stream<false, ROWS, true, uint8_t>(a, g, stream);
   if (g.m <= 16) return run_direct<1, 1, 8, 4, false>(a, g, stream);
   double cost;
   const int shape = best_shape(g.n, g.m, 0, a.kb, g.exact, &cost);
@@ -1038,9 +1060,39 @@ hipError_t launch_block_gemm_grouped(const BlockGemm& g, int64_t experts,
   a.offsets = offsets;
   // an average of 16 rows an expert: each expert's weight is read about once
   if (g.m <= 16 * experts && a.kb > 0 && a.kb <= kStreamMaxKb)
-    return run_stream<true, true, uint8_t>(a, g, stream);
+    return run_stream<true, ROWS, true, uint8_t>(a, g, stream);
   double cost;
   return run_shape<true>(best_shape(g.n, g.m, experts, a.kb, g.exact, &cost), a, g, stream);
+}
+
+// Few rows an expert: what a block of the stream kernel spends on quantizing them
+// is less than a kernel of its own.
+bool block_gemm_grouped_fuses(int64_t rows, int64_t experts, int64_t k) {
+  return rows <= 4 * experts && k > 0 && pitch(k) <= kStreamMaxKb * QW_BLOCK;
+}
+
+hipError_t launch_block_gemm_tokens(const BlockGemm& g, int64_t experts, const int32_t* offsets,
+                                    const int32_t* order, int64_t topk, hipStream_t stream) {
+  GemmArgs a = args_of(g);
+  a.experts = (int)experts;
+  a.offsets = offsets;
+  a.order = order;
+  a.topk = (int)topk;
+  const bool vec = g.k % 8 == 0 && aligned(g.x, 16);
+  if (g.x_type == QW_F32)
+    return vec ? run_stream<true, TOKENS, true, float>(a, g, stream)
+               : run_stream<true, TOKENS, false, float>(a, g, stream);
+  return vec ? run_stream<true, TOKENS, true, uint16_t>(a, g, stream)
+             : run_stream<true, TOKENS, false, uint16_t>(a, g, stream);
+}
+
+hipError_t launch_block_gemm_gates(const BlockGemm& g, int64_t experts, const int32_t* offsets,
+                                   hipStream_t stream) {
+  GemmArgs a = args_of(g);
+  a.experts = (int)experts;
+  a.offsets = offsets;
+  return g.k % 8 == 0 ? run_stream<true, GATES, true, float>(a, g, stream)
+                      : run_stream<true, GATES, false, float>(a, g, stream);
 }
 
 // From 64 rows an expert on the tiles are filled well enough; the blocks of the

@@ -186,8 +186,16 @@ hipError_t sort(int64_t slots, int64_t experts, const ID* ids, int32_t* pos, int
 //
 // Rows are cut into pieces of 8 values; thread i takes piece i % pieces of
 // token i / pieces.
+//
+// NT: what goes by once goes past the caches, when the rows are more than the
+// caches keep for whoever comes next (8192 tokens x 8 x 4096 bf16: combine 137
+// -> 110 us with loads and stores of that kind, the gather of twice as many 207
+// -> 181 with stores, the gradients 217 -> 195 with loads but 235 with stores;
+// 201 MB that the kernel before wrote are combined in 36 us, past the caches in 48).
 
-template <bool VEC, typename T>
+constexpr int64_t kCached = 256 << 20;  // bytes
+
+template <bool VEC, bool NT, typename T>
 __global__ __launch_bounds__(256) void gather(const T* __restrict__ x,
                                               const int32_t* __restrict__ pos,
                                               T* __restrict__ xs, int topk, int64_t d,
@@ -199,7 +207,7 @@ __global__ __launch_bounds__(256) void gather(const T* __restrict__ x,
     load8_of_row<VEC>(x + token * d, j, d, v);
     for (int c = 0; c < topk; ++c) {
       const int64_t p = pos[token * topk + c];
-      if (p >= 0 && p < rows) store8_of_row<VEC>(xs + p * d, j, d, v);
+      if (p >= 0 && p < rows) store8_of_row<VEC, NT>(xs + p * d, j, d, v);
     }
   }
 }
@@ -229,7 +237,7 @@ __global__ __launch_bounds__(256) void gather_block(const T* __restrict__ x,
   }
 }
 
-template <bool VEC, typename T, typename YT>
+template <bool VEC, bool NT, typename T, typename YT>
 __global__ __launch_bounds__(256) void combine(const T* __restrict__ ys,
                                                const int32_t* __restrict__ pos,
                                                const float* __restrict__ weights,
@@ -239,22 +247,33 @@ __global__ __launch_bounds__(256) void combine(const T* __restrict__ ys,
        i += (int64_t)gridDim.x * 256) {
     const int64_t token = i / pieces, j = (i - token * pieces) * 8;
     float s[8] = {};
-    for (int c = 0; c < topk; ++c) {
-      const int64_t p = pos[token * topk + c];
-      if (p < 0 || p >= rows) continue;
-      const float w = weights ? weights[token * topk + c] : 1.0f;
-      float v[8];
-      load8_of_row<VEC>(ys + p * d, j, d, v);
+    // 4 choices at a time, their rows on the way together; without a row, row 0
+    // is read and left out
+    for (int c0 = 0; c0 < topk; c0 += 4) {
+      int64_t p[4];
+      float w[4], v[4][8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) s[u] = __builtin_fmaf(w, v[u], s[u]);
+      for (int c = 0; c < 4; ++c) {
+        const int64_t slot = token * topk + min(c0 + c, topk - 1);
+        p[c] = pos[slot];
+        w[c] = weights ? weights[slot] : 1.0f;
+        if (c0 + c >= topk || p[c] >= rows) p[c] = -1;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) load8_of_row<VEC, NT>(ys + max(p[c], (int64_t)0) * d, j, d, v[c]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          s[u] = p[c] >= 0 ? __builtin_fmaf(w[c], v[c][u], s[u]) : s[u];
     }
-    store8_of_row<VEC>(y + token * d, j, d, s);
+    store8_of_row<VEC, NT>(y + token * d, j, d, s);
   }
 }
 
 // One thread block per token; 8 choices at a time share a pass over dy.
 constexpr int kChoices = 8;
-template <bool VEC, typename T>
+template <bool VEC, bool NT, typename T>
 __global__ __launch_bounds__(256) void combine_backward(
     const T* __restrict__ dy, const T* __restrict__ ys, const int32_t* __restrict__ pos,
     const float* __restrict__ weights, T* __restrict__ dys, float* __restrict__ dweights,
@@ -273,13 +292,13 @@ __global__ __launch_bounds__(256) void combine_backward(
       }
       for (int64_t j = threadIdx.x * 8; j < d; j += 256 * 8) {
         float g[8];
-        load8_of_row<VEC>(dy + token * d, j, d, g);
+        load8_of_row<VEC, NT>(dy + token * d, j, d, g);
 #pragma unroll
         for (int c = 0; c < kChoices; ++c) {
           if (p[c] < 0) continue;
           if (dweights) {
             float v[8];
-            load8_of_row<VEC>(ys + p[c] * d, j, d, v);
+            load8_of_row<VEC, NT>(ys + p[c] * d, j, d, v);
 #pragma unroll
             for (int u = 0; u < 8; ++u) dot[c] = __builtin_fmaf(g[u], v[u], dot[c]);
           }
@@ -317,10 +336,13 @@ template <typename T>
 hipError_t run_gather(int64_t t, int topk, int64_t d, int64_t rows, const T* x,
                       const int32_t* pos, T* xs, hipStream_t stream) {
   const int64_t pieces = (d + 7) / 8, items = t * pieces;
-  if (rows_vec(d, x, xs))
-    gather<true><<<grid_for(items, 256), 256, 0, stream>>>(x, pos, xs, topk, d, pieces, rows, items);
+  const unsigned grid = grid_for(items, 256);
+  if (!rows_vec(d, x, xs))
+    gather<false, false><<<grid, 256, 0, stream>>>(x, pos, xs, topk, d, pieces, rows, items);
+  else if (rows * d * (int64_t)sizeof(T) > kCached)
+    gather<true, true><<<grid, 256, 0, stream>>>(x, pos, xs, topk, d, pieces, rows, items);
   else
-    gather<false><<<grid_for(items, 256), 256, 0, stream>>>(x, pos, xs, topk, d, pieces, rows, items);
+    gather<true, false><<<grid, 256, 0, stream>>>(x, pos, xs, topk, d, pieces, rows, items);
   return hipGetLastError();
 }
 
@@ -342,10 +364,13 @@ hipError_t run_combine(int64_t t, int topk, int64_t d, int64_t rows, const T* ys
                        const int32_t* pos, const float* weights, YT* y, hipStream_t stream) {
   const int64_t pieces = (d + 7) / 8, items = t * pieces;
   const unsigned grid = grid_for(items, 256);
-  if (rows_vec(d, ys, y))
-    combine<true><<<grid, 256, 0, stream>>>(ys, pos, weights, y, topk, d, pieces, rows, items);
+  if (rows == 0) topk = 0;  // no row to look at
+  if (!rows_vec(d, ys, y))
+    combine<false, false><<<grid, 256, 0, stream>>>(ys, pos, weights, y, topk, d, pieces, rows, items);
+  else if (rows * d * (int64_t)sizeof(T) > kCached)
+    combine<true, true><<<grid, 256, 0, stream>>>(ys, pos, weights, y, topk, d, pieces, rows, items);
   else
-    combine<false><<<grid, 256, 0, stream>>>(ys, pos, weights, y, topk, d, pieces, rows, items);
+    combine<true, false><<<grid, 256, 0, stream>>>(ys, pos, weights, y, topk, d, pieces, rows, items);
   return hipGetLastError();
 }
 
@@ -355,10 +380,15 @@ hipError_t run_backward(int64_t t, int topk, int64_t d, int64_t rows, const T* d
                         hipStream_t stream) {
   const unsigned grid = grid_for(t, 1);
   // a NULL pointer is aligned
-  if (d % 8 == 0 && aligned(dy, 16) && aligned(ys, 16) && aligned(dys, 16))
-    combine_backward<true><<<grid, 256, 0, stream>>>(dy, ys, pos, weights, dys, dweights, topk, d, rows, t);
+  if (d % 8 != 0 || !aligned(dy, 16) || !aligned(ys, 16) || !aligned(dys, 16))
+    combine_backward<false, false>
+        <<<grid, 256, 0, stream>>>(dy, ys, pos, weights, dys, dweights, topk, d, rows, t);
+  else if (rows * d * (int64_t)sizeof(T) > kCached)
+    combine_backward<true, true>
+        <<<grid, 256, 0, stream>>>(dy, ys, pos, weights, dys, dweights, topk, d, rows, t);
   else
-    combine_backward<false><<<grid, 256, 0, stream>>>(dy, ys, pos, weights, dys, dweights, topk, d, rows, t);
+    combine_backward<true, false>
+        <<<grid, 256, 0, stream>>>(dy, ys, pos, weights, dys, dweights, topk, d, rows, t);
   return hipGetLastError();
 }
 

@@ -489,16 +489,6 @@ struct Carve {
   }
 };
 
-// A grouped product of checked arguments; exact: see BlockGemm.
-int grouped(int brows, int64_t experts, int64_t n, int64_t k, const uint8_t* codes,
-            const float* scales, int64_t rows, const uint8_t* xc, const float* xs,
-            const int32_t* offsets, int y_type, void* y, bool exact, void* stream) {
-  if (rows * n == 0) return QW_OK;
-  const qw::BlockGemm g = {brows, n, k, rows, codes, scales, -1, nullptr, xc, xs,
-                           y_type, y, exact};
-  return record(qw::launch_block_gemm_grouped(g, experts, offsets, (hipStream_t)stream));
-}
-
 }  // namespace
 
 extern "C" {
@@ -619,8 +609,9 @@ int qw_block_gemm_grouped(int block_rows, int64_t experts, int64_t n, int64_t k,
   if (!y || !offsets || (k > 0 && (!codes || !scales || !x_codes || !x_scales)))
     return QW_ENULL;
   if (!qw::aligned(codes, 16) || !qw::aligned(x_codes, 16)) return QW_EARG;
-  return grouped(block_rows, experts, n, k, codes, scales, rows, x_codes, x_scales, offsets,
-                 y_type, y, y_type == QW_F32, stream);
+  const qw::BlockGemm g = {block_rows, n, k, rows, codes, scales, -1, nullptr, x_codes,
+                           x_scales, y_type, y, y_type == QW_F32};
+  return record(qw::launch_block_gemm_grouped(g, experts, offsets, (hipStream_t)stream));
 }
 
 // ------------------------------------------ tokens sorted by expert and back
@@ -697,20 +688,26 @@ int qw_moe_combine_backward(int64_t t, int64_t topk, int64_t d, int64_t rows, in
 
 namespace {
 
-// The buffers of qw_moe_mlp in its work buffer.
+// The buffers of qw_moe_mlp in its work buffer, and the way it takes: few rows
+// are quantized by the products themselves, many gated by the first one.
 struct MlpWork {
-  int64_t pos, offsets, sort, xc, xs, h, hc, hs, ys, bytes;
+  bool few, gates;
+  int64_t pos, order, offsets, sort, xc, xs, h, hc, hs, ys, bytes;
   MlpWork(int64_t t, int64_t topk, int64_t experts, int64_t d, int64_t f) {
     const int64_t rows = t * topk;
+    few = qw::block_gemm_grouped_fuses(rows, experts, d) &&
+          qw::block_gemm_grouped_fuses(rows, experts, f);
+    gates = qw::block_gemm_gates(rows, experts, f, d);
     Carve c;
     pos = c.take(rows * 4);
+    order = c.take(few ? rows * 4 : 0);
     offsets = c.take((experts + 1) * 4);
     sort = c.take(qw::moe_sort_work_bytes(rows, experts));
-    xc = c.take(rows * qw::pitch(d));
-    xs = c.take(qw::block_scales(1, rows, d) * 4);
-    h = c.take(qw::block_gemm_gates(rows, experts, f, d) ? 0 : rows * 2 * f * 4);
-    hc = c.take(rows * qw::pitch(f));
-    hs = c.take(qw::block_scales(1, rows, f) * 4);
+    xc = c.take(few ? 0 : rows * qw::pitch(d));
+    xs = c.take(few ? 0 : qw::block_scales(1, rows, d) * 4);
+    h = c.take(gates ? 0 : rows * 2 * f * 4);
+    hc = c.take(few ? 0 : rows * qw::pitch(f));
+    hs = c.take(few ? 0 : qw::block_scales(1, rows, f) * 4);
     ys = c.take(rows * d * 4);
     bytes = c.at;
   }
@@ -755,28 +752,42 @@ int qw_moe_mlp(int block_rows, int64_t experts, int64_t d, int64_t f, const uint
   const int64_t rows = t * topk;
   int32_t* const pos = (int32_t*)(b + at.pos);
   int32_t* const offsets = (int32_t*)(b + at.offsets);
-  st = qw_moe_sort(t, topk, experts, id_bytes, ids, pos, nullptr, offsets, b + at.sort,
+  int32_t* const order = at.few ? (int32_t*)(b + at.order) : nullptr;
+  const hipStream_t s = (hipStream_t)stream;
+  st = qw_moe_sort(t, topk, experts, id_bytes, ids, pos, order, offsets, b + at.sort,
                    at.xc - at.sort, stream);
   if (st != QW_OK) return st;
-  st = qw_moe_gather_block(t, topk, d, rows, x_type, x, pos, b + at.xc, (float*)(b + at.xs),
-                           stream);
-  if (st != QW_OK) return st;
-  if (qw::block_gemm_gates(rows, experts, f, d)) {
-    const qw::BlockGemm g = {block_rows, 2 * f, d, rows, gate_up, gate_up_scales, -1, nullptr,
-                             b + at.xc, (const float*)(b + at.xs), QW_F32, b + at.hc, false};
-    st = record(qw::launch_block_gemm_gated(g, experts, offsets, (float*)(b + at.hs),
-                                            (hipStream_t)stream));
+  qw::BlockGemm up = {block_rows, 2 * f, d, rows, gate_up, gate_up_scales, x_type, x,
+                      nullptr, nullptr, QW_F32, b + at.h, false};
+  qw::BlockGemm out = {block_rows, d, f, rows, down, down_scales, QW_F32, b + at.h,
+                       nullptr, nullptr, QW_F32, b + at.ys, false};
+  if (at.few) {
+    st = record(qw::launch_block_gemm_tokens(up, experts, offsets, order, topk, s));
     if (st != QW_OK) return st;
+    st = record(qw::launch_block_gemm_gates(out, experts, offsets, s));
   } else {
-    st = grouped(block_rows, experts, 2 * f, d, gate_up, gate_up_scales, rows, b + at.xc,
-                 (const float*)(b + at.xs), offsets, QW_F32, b + at.h, false, stream);
+    float* const xs = (float*)(b + at.xs);
+    float* const hs = (float*)(b + at.hs);
+    st = qw_moe_gather_block(t, topk, d, rows, x_type, x, pos, b + at.xc, xs, stream);
     if (st != QW_OK) return st;
-    st = qw_block_quantize_swiglu(rows, f, QW_F32, b + at.h, offsets + experts, b + at.hc,
-                                  (float*)(b + at.hs), stream);
-    if (st != QW_OK) return st;
+    up.x_type = out.x_type = -1;
+    up.xc = b + at.xc;
+    up.xs = xs;
+    out.xc = b + at.hc;
+    out.xs = hs;
+    if (at.gates) {
+      up.y = b + at.hc;
+      st = record(qw::launch_block_gemm_gated(up, experts, offsets, hs, s));
+      if (st != QW_OK) return st;
+    } else if (f > 0) {
+      st = record(qw::launch_block_gemm_grouped(up, experts, offsets, s));
+      if (st != QW_OK) return st;
+      st = qw_block_quantize_swiglu(rows, f, QW_F32, b + at.h, offsets + experts, b + at.hc, hs,
+                                    stream);
+      if (st != QW_OK) return st;
+    }
+    st = record(qw::launch_block_gemm_grouped(out, experts, offsets, s));
   }
-  st = grouped(block_rows, experts, d, f, down, down_scales, rows, b + at.hc,
-               (const float*)(b + at.hs), offsets, QW_F32, b + at.ys, false, stream);
   if (st != QW_OK) return st;
   return qw_moe_combine(t, topk, d, rows, QW_F32, b + at.ys, pos, weights, y_type, y, stream);
 }

@@ -93,6 +93,15 @@ struct BlockGemm {
 hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t stream);
 hipError_t launch_block_gemm_grouped(const BlockGemm& g, int64_t experts,
                                      const int32_t* offsets, hipStream_t stream);
+// Grouped products with float x (x_type, x; y fp32, not exact) that quantize it
+// themselves, for sizes that block_gemm_grouped_fuses takes: of rows that are
+// still in token order (a row's token is order[row] / topk), and of rows of 2 k
+// fp32 values (g.x 16-byte aligned) whose gated product is the row.
+bool block_gemm_grouped_fuses(int64_t rows, int64_t experts, int64_t k);
+hipError_t launch_block_gemm_tokens(const BlockGemm& g, int64_t experts, const int32_t* offsets,
+                                    const int32_t* order, int64_t topk, hipStream_t stream);
+hipError_t launch_block_gemm_gates(const BlockGemm& g, int64_t experts, const int32_t* offsets,
+                                   hipStream_t stream);
 // The grouped product with a weight of gate rows and then as many up rows (g.n
 // in all), as codes of silu(gate) * up in g.y and their 1 x 128 scales in ys:
 // for sizes that block_gemm_gates takes.

@@ -197,7 +197,7 @@ def mlp_reference(gate_up, down, x, ids, weights, f):
 
 
 MLP = [(1, 1, 1, 128, 128), (1, 4, 8, 512, 384), (3, 2, 5, 200, 70), (7, 2, 4, 130, 257), (40, 2, 8, 256, 128), (130, 4, 6, 300, 200),
-       (300, 2, 3, 264, 136), (600, 1, 2, 128, 300), (200, 2, 4, 260, 128), (333, 3, 5, 128, 384), (900, 2, 6, 700, 256)]
+       (300, 2, 3, 264, 136), (600, 1, 2, 128, 300), (200, 2, 4, 260, 128), (333, 3, 5, 128, 384), (900, 2, 6, 700, 256), (2, 2, 3, 1300, 600), (16, 2, 8, 136, 1100)]
 
 
 @pytest.mark.parametrize("t,topk,experts,d,f", MLP)
@@ -232,12 +232,13 @@ def test_mlp(t, topk, experts, d, f, br, dtype, weighted):
     assert np.linalg.norm(host(yb) - host(y)) <= 2.0 ** -8 * norm + 1e-30
 
 
-def test_mlp_with_no_slot_in():
+@pytest.mark.parametrize("t", [1, 9, 300])
+def test_mlp_with_no_slot_in(t):
     gate_up = qw.block_quantize(torch.randn(4, 256, 128, device="cuda"), 128)
     down = qw.block_quantize(torch.randn(4, 128, 128, device="cuda"), 128)
-    y = torch.full((9, 128), 7.0, device="cuda")
-    qw.moe_mlp(gate_up, down, torch.randn(9, 128, device="cuda"), torch.full((9, 2), -1, device="cuda"),
-               torch.full((9, 2), float("nan"), device="cuda"), out=y)
+    y = torch.full((t, 128), 7.0, device="cuda")
+    qw.moe_mlp(gate_up, down, torch.randn(t, 128, device="cuda"), torch.full((t, 2), -1, device="cuda"),
+               torch.full((t, 2), float("nan"), device="cuda"), out=y)
     assert not bool(y.any())
     assert qw.moe_mlp(gate_up, down, torch.zeros(0, 128, device="cuda"), torch.zeros(0, 2, dtype=torch.int64, device="cuda")).shape == (0, 128)
 
