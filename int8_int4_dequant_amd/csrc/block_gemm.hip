@@ -884,10 +884,12 @@ hipError_t run_stream(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Rows up to which the stream kernel quantizes x itself: each block pays for it
-// (4096 x 4096: 8.5 us at 1 row, 11.3 at 8, 16.8 at 16; with codes 6.4, 7.3
-// and 8.0, and 2.8 for a kernel that makes them).
-constexpr int kFusedMaxM = 8;
+// The stream kernel quantizes x itself up to this many rows, and up to this many
+// of a wave's blocks over all rows: every block of the grid pays for it (4096 x
+// 4096: 8.5 us at 1 row, 11.3 at 8, 16.8 at 16; with codes 6.4, 7.3 and 8.0, and
+// 2.8 and a launch for a kernel that makes them; 28672 x 8192 at 8 rows 51.3
+// against 48.6).
+constexpr int kFusedMaxM = 8, kFusedBlocks = 32;
 // Most blocks of k that the stream kernel's waves hold.
 constexpr int kStreamMaxKb = 12 * kStreamWaves;
 
@@ -1016,7 +1018,8 @@ GemmArgs part_of(GemmArgs a, const BlockGemm& g, int64_t from, int64_t count) {
 }  // namespace
 
 bool block_gemm_fuses(int64_t m, int64_t k) {
-  return m <= kFusedMaxM && pitch(k) <= kStreamMaxKb * QW_BLOCK;
+  const int64_t each = (pitch(k) / QW_BLOCK + kStreamWaves - 1) / kStreamWaves;
+  return m <= kFusedMaxM && pitch(k) <= kStreamMaxKb * QW_BLOCK && m * each <= kFusedBlocks;
 }
 
 hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t stream) {
