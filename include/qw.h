@@ -606,9 +606,9 @@ int qw_moe_combine_backward(int64_t t, int64_t topk, int64_t d, int64_t rows, in
  *   x [t][d], ids [t][topk] as in qw_moe_sort, weights fp32 [t][topk] or NULL
  *   y [t][d]
  *   work: qw_moe_mlp_work_bytes(...) bytes, 16-byte aligned (QW_EWORK)
- * block_rows is that of both weights.  Both products run on the 8-bit cores
- * (see qw_block_gemm) with fp32 results: what they drop is far below the
- * rounding of the hidden values to codes.
+ * block_rows is that of both weights.  Both products have fp32 results, on the
+ * 8-bit cores where there are many rows (see qw_block_gemm): what those drop is
+ * far below the rounding of the hidden values to codes.
  */
 int64_t qw_moe_mlp_work_bytes(int64_t t, int64_t topk, int64_t experts, int64_t d, int64_t f);
 int qw_moe_mlp(int block_rows, int64_t experts, int64_t d, int64_t f,

@@ -373,6 +373,7 @@ template <int NF, int MF, int WM, int STAGES, bool EXACT, bool BROWS1, bool GROU
 __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
   constexpr int BN = 16 * NF * (kTileWaves / WM), BM = 16 * MF * WM, ROWS = BN + BM;
   constexpr int PAIRS = NF * MF / 2;
+  constexpr bool ROTATE = NF * MF == 32 && !GROUPED;
   constexpr int SEGS = ROWS / 8 / kTileWaves;  // 8-row pieces of a wave
   static_assert(QW_BLOCK % (16 * NF) == 0, "a wave's weight rows lie in one 128 x 128 block");
   static_assert(ROWS / 8 % kTileWaves == 0 && MF % 2 == 0, "whole pieces and pairs");
@@ -392,12 +393,14 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
   struct Place {
     int64_t n0, m0, end;
     i32x4 wbuf, ubuf, xbuf, sbuf;
+    int rot;
   };
   // The first tile at or behind `at` (in steps of the grid) that has rows.
   auto place = [&](int64_t& at, Place& p) {
     for (; at < a.tiles; at += gridDim.x) {
       int64_t tm, tn;
       tile_place(at, a.tiles, a.tiles_m, tm, tn);
+      p.rot = ROTATE && a.kb >= 16 ? (int)((tm * 5 + tn) & 7) : 0;
       p.n0 = GATED ? tn * QW_BLOCK : tn * BN;
       p.m0 = tm * BM;
       p.end = min(p.m0 + BM, a.m);
@@ -434,6 +437,14 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0];
   const uint32_t lds1 =
       (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&scales[0][0][0];
+  // Tiles of the largest shape start at different blocks of k, up to 7 apart (and
+  // within what an L2 holds of the rows they share): in step they would all ask
+  // the same channels, with rows often a power of two apart (8192^3 479 -> 464
+  // us; the others, and grouped ones, lose 2 to 5 in a hundred by it).
+  auto rotated = [&](const Place& p, int b) {
+    if (!ROTATE) return b;
+    return b + p.rot < a.kb ? b + p.rot : b + p.rot - a.kb;
+  };
   // Piece s of block b.  Behind the last block there is nothing to read, but the
   // copy is issued all the same (as zeros, from an empty buffer): a branch
   // would part the products from the scaling that runs beside them.
@@ -441,13 +452,14 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
     i32x4 from = s >= BN / 64 ? p.xbuf : GATED && s >= BN / 128 ? p.ubuf : p.wbuf;
     from.z = b < a.kb ? from.z : 0;
     const int seg = wave + kTileWaves * s;
-    copy_to_lds(from, voff[s], (uint32_t)b * 128, lds0 + buf * (ROWS * 128) + seg * 1024);
+    copy_to_lds(from, voff[s], (uint32_t)rotated(p, b) * 128,
+                lds0 + buf * (ROWS * 128) + seg * 1024);
   };
   auto fetch_scales = [&](const Place& p, int b) {  // of the 4 blocks from b on
     if (wave < SROWS / 64) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        copy4_to_lds(p.sbuf, soff, (uint32_t)(b + c) * 4,
+        copy4_to_lds(p.sbuf, soff, (uint32_t)rotated(p, b + c) * 4,
                      lds1 + (((b >> 2) & 1) * 4 + c) * (SROWS * 4) + wave * 256);
     }
   };
@@ -871,15 +883,11 @@ hipError_t run_stream(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
   using std::true_type;
   using std::false_type;
   const bool one = g.brows == 1;
-  if constexpr (!GROUPED || is_codes<XT>::value) {
-    if (g.y_type == QW_BF16)
-      one ? go(false_type{}, true_type{}, uint16_t{}) : go(false_type{}, false_type{}, uint16_t{});
-    else if (g.exact)
-      one ? go(true_type{}, true_type{}, 0.0f) : go(true_type{}, false_type{}, 0.0f);
-  }
-  if constexpr (GROUPED) {
-    if (g.y_type == QW_F32 && !g.exact)
-      one ? go(false_type{}, true_type{}, 0.0f) : go(false_type{}, false_type{}, 0.0f);
+  // fp32 results on the bf16 cores, asked for or not: they wait for memory either way
+  if (g.y_type == QW_F32) {
+    one ? go(true_type{}, true_type{}, 0.0f) : go(true_type{}, false_type{}, 0.0f);
+  } else if constexpr (!GROUPED || is_codes<XT>::value) {
+    one ? go(false_type{}, true_type{}, uint16_t{}) : go(false_type{}, false_type{}, uint16_t{});
   }
   return hipGetLastError();
 }
