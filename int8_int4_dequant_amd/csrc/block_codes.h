@@ -2,6 +2,8 @@
 // kernels that make or read them (block.hip, block_gemm.hip, moe.hip).
 #pragma once
 
+#include <type_traits>
+
 #include "qw_internal.h"
 
 namespace qw {
@@ -57,6 +59,11 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
   *(u32x2*)p = u32x2{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3])};
 }
 
+// 16 bytes at the alignment of an element: rows of any length take the vector
+// accesses too, which the hardware splits where it has to.
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+
 template <bool NT, typename V>
 __device__ __forceinline__ V load_as(const void* p) {
   return NT ? __builtin_nontemporal_load((const V*)p) : *(const V*)p;
@@ -69,19 +76,21 @@ __device__ __forceinline__ void store_as(void* p, V v) {
     *(V*)p = v;
 }
 
-// 8 consecutive elements at a 16-byte aligned address; NT: past the caches.
-template <bool NT = false>
+// 8 consecutive elements, at a 16-byte aligned address (VEC) or any; NT: past the
+// caches.
+template <bool VEC, bool NT = false>
 __device__ __forceinline__ void load8(const float* p, float v[8]) {
-  const f32x4 a = load_as<NT, f32x4>(p), b = load_as<NT, f32x4>(p + 4);
+  typedef std::conditional_t<VEC, f32x4, f32x4_u> V;
+  const f32x4 a = load_as<NT, V>(p), b = load_as<NT, V>(p + 4);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[i] = a[i];
     v[4 + i] = b[i];
   }
 }
-template <bool NT = false>
+template <bool VEC, bool NT = false>
 __device__ __forceinline__ void load8(const uint16_t* p, float v[8]) {
-  const u32x4 a = load_as<NT, u32x4>(p);
+  const u32x4 a = load_as<NT, std::conditional_t<VEC, u32x4, u32x4_u>>(p);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = bf16_lo(a[i]);
@@ -93,35 +102,32 @@ __device__ __forceinline__ void load8(const uint16_t* p, float v[8]) {
 // aligned and k % 8 == 0, so the 8 are all there or none is.
 template <bool VEC, bool NT = false, typename T>
 __device__ __forceinline__ void load8_of_row(const T* row, int64_t j, int64_t k, float v[8]) {
-  if constexpr (VEC) {
-    if (j < k) {
-      load8<NT>(row + j, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    }
+  if (VEC ? j < k : j + 8 <= k) {
+    load8<VEC, NT>(row + j, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = j + i < k ? load1(row + j + i) : 0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = !VEC && j + i < k ? load1(row + j + i) : 0.0f;
   }
 }
 
 // The same for a store.
-template <bool NT = false>
+template <bool VEC, bool NT = false>
 __device__ __forceinline__ void store8(float* p, const float v[8]) {
-  store_as<NT>(p, f32x4{v[0], v[1], v[2], v[3]});
-  store_as<NT>(p + 4, f32x4{v[4], v[5], v[6], v[7]});
+  typedef std::conditional_t<VEC, f32x4, f32x4_u> V;
+  store_as<NT, V>(p, V{v[0], v[1], v[2], v[3]});
+  store_as<NT, V>(p + 4, V{v[4], v[5], v[6], v[7]});
 }
-template <bool NT = false>
+template <bool VEC, bool NT = false>
 __device__ __forceinline__ void store8(uint16_t* p, const float v[8]) {
-  store_as<NT>(p, u32x4{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
-                        to_bf16x2(v[6], v[7])});
+  typedef std::conditional_t<VEC, u32x4, u32x4_u> V;
+  store_as<NT, V>(p, V{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3]), to_bf16x2(v[4], v[5]),
+                       to_bf16x2(v[6], v[7])});
 }
 template <bool VEC, bool NT = false, typename T>
 __device__ __forceinline__ void store8_of_row(T* row, int64_t j, int64_t k, const float v[8]) {
-  if constexpr (VEC) {
-    if (j < k) store8<NT>(row + j, v);
-  } else {
+  if (VEC ? j < k : j + 8 <= k) {
+    store8<VEC, NT>(row + j, v);
+  } else if (!VEC) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (j + i < k) store1(row + j + i, v[i]);

@@ -763,7 +763,7 @@ def _run(what, dev, stream, fn, *args):
         if stream.device.index != dev:
             raise ValueError(f"tensors on device {dev} and a stream of {stream.device}")
         raw = stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -776,7 +776,8 @@ def _on_stream(f):
     """``stream`` (a torch stream or a hipStream_t) as the current stream of
     the whole call, so that what it allocates belongs to that stream too."""
     @functools.wraps(f)
-    def call(*args, stream=None, **kwargs):
+    def call(*args, **kwargs):
+        stream = kwargs.pop("stream", None) if kwargs else None
         if stream is None:
             return f(*args, **kwargs)
         if not isinstance(stream, torch.cuda.Stream):

@@ -160,6 +160,36 @@ SIZES = [(1, 1, 1), (1, 128, 128), (1, 4096, 4096), (2, 17, 129), (3, 1000, 300)
          (257, 511, 384), (300, 2304, 1280), (1000, 130, 100), (513, 4097, 333)]
 
 
+# the larger tiles, a last round that is cut off, waves with many blocks of k, and
+# more of them than a wave holds
+LARGE = [(2, 60, 9000), (8, 60, 9000), (3, 40, 13000), (16, 70, 13000), (600, 3000, 260), (1000, 5000, 500), (4096, 4096, 256),
+         (2100, 4000, 200), (2048, 8300, 1000), (40, 4096, 1000), (60, 2048, 4000)]
+
+
+def on_gpu(xrec, rec, k, y):
+    """check_product for large sizes, in float64 on the GPU, piece by piece."""
+    val = lambda r, br: qw.block_unpack(r).double()  # noqa: E731  (fl32(code * S): 2^-24 of each value)
+    xv, wv = val(xrec, 1), val(rec, rec["block_rows"])
+    ref, base = xv @ wv.T, xv.abs() @ wv.abs().T
+    bar = (BAR[y.dtype] + 2.0 ** -23) * base
+    assert bool(((y.double() - ref).abs() <= bar + HALF[y.dtype] * (ref.abs() + bar)).all())
+
+
+@pytest.mark.parametrize("m,n,k", LARGE)
+@pytest.mark.parametrize("br,dtype", [(128, torch.float32), (1, torch.float32), (128, torch.bfloat16), (1, torch.bfloat16)])
+def test_gemm_large(m, n, k, br, dtype):
+    print("gemm", m, n, k, br, dtype, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(m + n + k)
+    make = lambda r, c: torch.randn(r, c, generator=g, device="cuda") * torch.rand(c, generator=g, device="cuda").exp()  # noqa: E731
+    rec, x = qw.block_quantize(make(n, k), br), make(m, k)
+    xrec = qw.block_quantize(x, 1)
+    y = torch.full((m + 1, n), 7.0, dtype=dtype, device="cuda")
+    qw.block_gemm(rec, xrec, out=y[:m], out_dtype=dtype)
+    on_gpu(xrec, rec, k, y[:m])
+    assert bool((y[m] == 7).all())
+    on_gpu(xrec, rec, k, qw.block_matmul(rec, x, out_dtype=dtype))
+
+
 @pytest.mark.parametrize("m,n,k", SIZES)
 @pytest.mark.parametrize("br,dtype", [(128, torch.float32), (1, torch.float32), (128, torch.bfloat16), (1, torch.bfloat16)])
 def test_gemm(m, n, k, br, dtype):
@@ -255,7 +285,7 @@ def test_gradients_of_a_product():
 
 
 GROUPS = [([0], 5, 130), ([3], 100, 200), ([0, 0, 1, 0], 64, 128), ([1, 2, 3, 4, 5], 260, 300), ([17, 0, 64, 1, 65, 0, 130], 200, 257),
-          ([300, 1, 0, 257, 128], 513, 384), ([40] * 70, 96, 256), ([1] * 130, 130, 129), ([0] * 99 + [700], 300, 200)]
+          ([300, 1, 0, 257, 128], 513, 384), ([40] * 70, 96, 256), ([1] * 130, 130, 129), ([0] * 99 + [700], 300, 200), ([2, 1], 40, 9000), ([5] * 8, 100, 5000), ([1, 3], 40, 13000), ([20] * 4, 64, 13000)]
 
 
 @pytest.mark.parametrize("counts,n,k", GROUPS)
@@ -280,6 +310,26 @@ def test_grouped(counts, n, k, br, dtype):
         if counts[i]:
             wv = ob.values(codes_of(rec)[i], rec["scales"].cpu().numpy()[i], br, k)
             check_product(y[off[i]:off[i + 1]], xv[off[i]:off[i + 1]], wv)
+
+
+@pytest.mark.parametrize("counts,n,k", [([900, 0, 1500], 4000, 300), ([300] * 8, 2000, 256), ([150] * 30, 1000, 128), ([700] * 12, 2000, 128),
+                                        ([20] * 8, 600, 2000), ([257, 1, 511, 256, 128, 0, 640], 2050, 640)])
+@pytest.mark.parametrize("br,dtype", [(128, torch.float32), (1, torch.float32), (128, torch.bfloat16), (1, torch.bfloat16)])
+def test_grouped_large(counts, n, k, br, dtype):
+    print("grouped", len(counts), sum(counts), n, k, br, dtype, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(n + k)
+    rows = sum(counts) + 37
+    rec = qw.block_quantize(torch.randn(len(counts), n, k, generator=g, device="cuda"), br)
+    xrec = qw.block_quantize(torch.randn(rows, k, generator=g, device="cuda"), 1)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    y = torch.full((rows, n), 7.0, dtype=dtype, device="cuda")
+    qw.block_gemm_grouped(rec, xrec, torch.from_numpy(off).cuda(), out=y, out_dtype=dtype)
+    assert bool((y[off[-1]:] == 7).all())
+    part = lambda r, at, shape: dict(r, shape=shape, codes=r["codes"][at].contiguous(), scales=r["scales"][at].contiguous())  # noqa: E731
+    for e, c in enumerate(counts):
+        if c:
+            at = slice(int(off[e]), int(off[e + 1]))
+            on_gpu(part(xrec, at, [c, k]), part(rec, e, [n, k]), k, y[at])
 
 
 def test_grouped_clamps_offsets():

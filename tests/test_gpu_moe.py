@@ -197,7 +197,8 @@ def mlp_reference(gate_up, down, x, ids, weights, f):
 
 
 MLP = [(1, 1, 1, 128, 128), (1, 4, 8, 512, 384), (3, 2, 5, 200, 70), (7, 2, 4, 130, 257), (40, 2, 8, 256, 128), (130, 4, 6, 300, 200),
-       (300, 2, 3, 264, 136), (600, 1, 2, 128, 300), (200, 2, 4, 260, 128), (333, 3, 5, 128, 384), (900, 2, 6, 700, 256), (2, 2, 3, 1300, 600), (16, 2, 8, 136, 1100)]
+       (300, 2, 3, 264, 136), (600, 1, 2, 128, 300), (200, 2, 4, 260, 128), (333, 3, 5, 128, 384), (900, 2, 6, 700, 256), (2, 2, 3, 1300, 600), (16, 2, 8, 136, 1100),
+       (2, 1, 2, 4200, 300), (1, 1, 1, 9000, 128), (1, 1, 1, 128, 4200), (3, 1, 1, 200, 9100)]
 
 
 @pytest.mark.parametrize("t,topk,experts,d,f", MLP)
