@@ -365,7 +365,7 @@ __device__ __forceinline__ void tile_place(int64_t block, int64_t tiles, int64_t
 // tokens, so half of the tokens' sums change places with the up waves through
 // LDS and every wave scales and rounds half of its tokens.  A block takes tile
 // after tile and has the next one's first copies on their way while it writes its
-// results (24594 rows of 60 experts, 16 blocks of k: 284 -> 267 us; the other
+// results (24594 rows of 64 experts, 16 blocks of k: 284 -> 267 us; the other
 // products, whose results take less work, lose by it: 4096^3 63 -> 67).
 
 template <int NF, int MF, int WM, int STAGES, bool EXACT, bool BROWS1, bool GROUPED, bool GATED,
@@ -895,8 +895,8 @@ hipError_t run_stream(GemmArgs a, const BlockGemm& g, hipStream_t stream) {
 // The stream kernel quantizes x itself up to this many rows, and up to this many
 // of a wave's blocks over all rows: every block of the grid pays for it (4096 x
 // 4096: 8.5 us at 1 row, 11.3 at 8, 16.8 at 16; with codes 6.4, 7.3 and 8.0, and
-// 2.8 and a launch for a kernel that makes them; 28672 x 8192 at 8 rows 51.3
-// against 48.6).
+// 2.8 and a launch for a kernel that makes them; 28672 x 8192 at 8 rows 51.9
+// against 45.6 with that kernel).
 constexpr int kFusedMaxM = 8, kFusedBlocks = 32;
 // Most blocks of k that the stream kernel's waves hold.
 constexpr int kStreamMaxKb = 12 * kStreamWaves;
@@ -943,7 +943,7 @@ GemmArgs args_of(const BlockGemm& g) {
 //           32; 256 x 4096 x 4096: 41, tiled 16).
 // A tiled product whose last round is only partly filled may be cut in two along
 // the weight rows, the rest with smaller tiles (2048 x 28672 x 8192: 3.5 rounds
-// of 256 x 256, 480 us; 3 rounds and one of 256 x 128, 430 us).
+// of 256 x 256, 480 us; 3 rounds and one of 256 x 128, 440 us).
 // Grouped: an expert's last tile is half empty on average.
 
 struct Shape {
