@@ -244,6 +244,16 @@ def test_mlp_with_no_slot_in(t):
     assert qw.moe_mlp(gate_up, down, torch.zeros(0, 128, device="cuda"), torch.zeros(0, 2, dtype=torch.int64, device="cuda")).shape == (0, 128)
 
 
+@pytest.mark.parametrize("t", [1, 9, 400])
+def test_mlp_without_hidden_values(t):
+    """f = 0 is an empty sum: zeros, for few and for many rows an expert."""
+    gate_up = qw.block_quantize(torch.zeros(2, 0, 128, device="cuda"), 128)
+    down = qw.block_quantize(torch.zeros(2, 128, 0, device="cuda"), 128)
+    y = torch.full((t, 128), 7.0, device="cuda")
+    qw.moe_mlp(gate_up, down, torch.randn(t, 128, device="cuda"), torch.zeros(t, 2, dtype=torch.int64, device="cuda"), out=y)
+    assert not bool(y.any())
+
+
 @pytest.mark.parametrize("t", [3, 400])
 def test_mlp_graph_replays(t):
     d, f, e, topk = 256, 192, 8, 2
