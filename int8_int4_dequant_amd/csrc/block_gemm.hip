@@ -1046,12 +1046,13 @@ hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t stream) {
   double cost;
   const int shape = best_shape(g.n, g.m, 0, a.kb, g.exact, &cost);
   if (kShapes[shape].tiled) {
-    // the weight rows of whole rounds, and the rest with another shape
+    // the weight rows of whole rounds, and the rest with another shape; the cut lies
+    // between blocks of 128 rows, which share a scale (a tile of 64 is half of one)
     const Shape& s = kShapes[shape];
     const int64_t tiles_m = (g.m + s.bm - 1) / s.bm, tiles_n = (g.n + s.bn - 1) / s.bn;
     const int64_t whole = tiles_m * tiles_n / kUnits * kUnits / tiles_m;
-    if (whole > 0 && whole < tiles_n) {
-      const int64_t cut = whole * s.bn;  // a multiple of 128
+    const int64_t cut = whole * s.bn / QW_BLOCK * QW_BLOCK;
+    if (cut > 0 && cut < g.n) {
       double rest;
       const int other = best_shape(g.n - cut, g.m, 0, a.kb, g.exact, &rest);
       if (cost_of(s, cut, g.m, 0, a.kb, g.exact) + rest + 2.0 < cost) {
