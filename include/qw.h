@@ -468,7 +468,8 @@ int qw_block_quantize(int block_rows, int64_t count, int64_t n, int64_t k, int t
 /*
  * Quantize the gated product of an MLP's two halves with 1 x 128 blocks:
  *   h       fp32 or bf16 [rows][2 f]: gate | up         (read)
- *   v       = gate / (1 + exp(-gate)) * up, in fp32
+ *   v       = gate / (1 + exp(-gate)) * up, in fp32 (within 4 ulp for every
+ *           finite gate, exp beyond fp32's range included)
  *   codes   [rows][qw_block_pitch(f)], scales [rows][...] of v  (written)
  * `used` (DEVICE int32, may be NULL): how many of the rows there are; the
  * others are neither read nor written.

@@ -91,8 +91,7 @@ __global__ __launch_bounds__(256) void quantize_swiglu(const T* __restrict__ h,
     float a[8], b[8];
     load8_of_row<VEC>(h + row * 2 * f, j, f, a);
     load8_of_row<VEC>(h + row * 2 * f + f, j, f, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = gated(a[i], b[i]);
+    gated<8>(a, b, a);
     const float s = block_scale(max16(amax8(a)));
     *(u32x2*)(codes + row * (kb * QW_BLOCK) + j) = codes8(a, s);
     if ((threadIdx.x & 15) == 0) scales[g] = s;

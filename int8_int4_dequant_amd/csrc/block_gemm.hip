@@ -621,13 +621,13 @@ __global__ __launch_bounds__(kTileWaves * 64, 2) void gemm_tiled(GemmArgs a) {
           lds_barrier();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const f32x4 o = other[i * 64];
+            const f32x4 o = other[i * 64], m = acc[h + i][UP];
+            const f32x4 gate = UP ? o : m, up = UP ? m : o;
+            const float gates[4] = {gate[0], gate[1], gate[2], gate[3]};
+            const float ups[4] = {up[0], up[1], up[2], up[3]};
+            gated<4>(gates, ups, v[h + i]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float m = acc[h + i][UP][c];
-              v[h + i][c] = UP ? gated(o[c], m) : gated(m, o[c]);
-              top = fmaxf(top, fabsf(v[h + i][c]));
-            }
+            for (int c = 0; c < 4; ++c) top = fmaxf(top, fabsf(v[h + i][c]));
           }
         }
         top = fmaxf(top, __shfl_xor(top, 16));
@@ -744,8 +744,7 @@ __device__ __forceinline__ void quantize_part(const GemmArgs& a, int64_t m0, int
         if constexpr (SRC == GATES) {
           float up[8];
           load8_of_row<VEC>(x + a.k, j, a.k, up);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) v[i][c] = gated(v[i][c], up[c]);
+          gated<8>(v[i], up, v[i]);
         }
       }
 #pragma unroll
