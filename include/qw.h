@@ -429,6 +429,10 @@ int qw_gptq_quantize_pack(int bits, int64_t group, int64_t n, int64_t k,
  *             where that is zero.
  *   value     code = e4m3(clip(fl32(w / S), -448, 448)), rounded to nearest
  *             even; the value it stands for is code * S.
+ *   NaN       has no part in its block's maximum and a NaN code (127 or 255),
+ *             and so every sum that it enters is NaN.  An infinity makes its
+ *             block's S infinite, its own code NaN and the others 0, so that
+ *             all values of the block are NaN.
  *   layout    codes [n][kp] with kp = qw_block_pitch(k), k rounded up to
  *             whole blocks; the bytes behind k are zero.  scales
  *             [ceil(n / block_rows)][kp / 128].  Every row starts a 128-byte

@@ -24,11 +24,14 @@ __device__ __forceinline__ float block_scale(float amax) {
   return s == 0.0f ? 1.0f : s;
 }
 
-__device__ __forceinline__ float clip_top(float v) { return fminf(fmaxf(v, -kTop), kTop); }
+// NaN stays NaN (fminf and fmaxf alone would make it a number).
+__device__ __forceinline__ float clip_top(float v) {
+  return v != v ? v : fminf(fmaxf(v, -kTop), kTop);
+}
 
 // Codes of 4 values already divided by their scale, first value in the low
-// byte.  The conversion rounds to nearest even; values are within +-448, so
-// it never saturates.
+// byte.  The conversion rounds to nearest even; values are within +-448 or NaN,
+// so it never saturates.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   int r = __builtin_amdgcn_cvt_pk_fp8_f32(clip_top(a), clip_top(b), 0, false);
   r = __builtin_amdgcn_cvt_pk_fp8_f32(clip_top(c), clip_top(d), r, true);

@@ -1,5 +1,5 @@
 """Block-scaled e4m3 on the GPU at the ends of the values' range: gates of any
-size in the gated product."""
+size in the gated product, and blocks with NaN or infinities in them."""
 
 import numpy as np
 import pytest
@@ -62,3 +62,95 @@ def test_expert_mlp_with_far_gates(t, gate, dtype):
     steep = 3 * abs(gate) if -1e3 < gate < 0 else 3
     bar = (steep + 8) * 2.0 ** -23 + (0 if dtype is torch.float32 else 2.0 ** -8)
     assert bool(((y.double() - want).abs() <= bar * abs(want)).all()), (y[0, 0], want)
+
+
+def poisoned(rows, k, size, poison, dtype):
+    """Values up to `size`, the same with one value replaced, and where: row 2, column 130."""
+    rng = np.random.default_rng([rows, k])
+    w = (rng.uniform(-1, 1, (rows, k)) * size).astype(np.float32)
+    w[:, ::128] = size
+    clean = torch.from_numpy(w).to(dtype)
+    clean[2, 130] = 0.0
+    dirty = clean.clone()
+    dirty[2, 130] = poison
+    return clean.cuda(), dirty.cuda()
+
+
+def codes_of(rec):
+    return rec["codes"].view(torch.uint8).cpu().numpy()
+
+
+# scales of 1, below 2^-60, of a subnormal value, and above 2^100
+SCALES = [448.0, 1e-18, 1e-40, 1e35]
+
+
+@pytest.mark.parametrize("size", SCALES)
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("dtype,k", [(torch.float32, 384), (torch.float32, 301), (torch.bfloat16, 384)])
+def test_a_block_with_a_value_that_is_no_number(size, poison, block_rows, dtype, k):
+    clean, dirty = poisoned(5, k, size, poison, dtype)
+    a, b = qw.block_quantize(clean, block_rows), qw.block_quantize(dirty, block_rows)
+    ca, cb = codes_of(a), codes_of(b)
+    sa, sb = a["scales"].cpu().numpy(), b["scales"].cpu().numpy()
+    assert cb[2, 130] & 127 == 127
+    rows = slice(2, 3) if block_rows == 1 else slice(0, 5)
+    hit = (2 if block_rows == 1 else 0, 1)
+    if np.isnan(poison):      # its own code, and nothing else
+        ca[2, 130] = cb[2, 130]
+        assert np.array_equal(ca, cb) and np.array_equal(sa.view(np.uint32), sb.view(np.uint32))
+    else:                     # the block's scale is infinite
+        assert np.isposinf(sb[hit])
+        sb[hit] = sa[hit]
+        assert np.array_equal(sa, sb)
+        block = cb[rows, 128:256].copy()
+        block[2 - rows.start, 2] &= 0
+        assert not (block & 127).any()
+        cb[rows, 128:256] = ca[rows, 128:256]
+        assert np.array_equal(ca, cb)
+        assert bool(torch.isnan(qw.block_unpack(b)[rows, 128:256]).all())
+
+
+@pytest.mark.parametrize("size", SCALES)
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("m", [4, 12, 40, 300])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_products_of_what_is_no_number(size, poison, m, dtype):
+    """The poisoned row's outputs are NaN, for every way that x is quantized, and the others as they were."""
+    clean, dirty = poisoned(m, 384, size, poison, dtype)
+    rec = qw.block_quantize(torch.rand(70, 384, device="cuda") + 0.5, 128)
+    a, b = qw.block_matmul(rec, clean), qw.block_matmul(rec, dirty)
+    keep = torch.arange(m, device="cuda") != 2
+    assert bool(torch.isnan(b[2]).all()) and torch.equal(a[keep], b[keep])
+    # as rows of an expert's tokens: gathered as codes
+    pos = torch.arange(m, dtype=torch.int32, device="cuda")[:, None]
+    c, d = qw.moe_gather_block(dirty, dict(pos=pos)), qw.block_quantize(dirty, 1)
+    assert np.array_equal(codes_of(c), codes_of(d)) and np.array_equal(c["scales"].cpu().numpy(), d["scales"].cpu().numpy())
+
+
+@pytest.mark.parametrize("t", [2, 40, 700])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_expert_mlp_of_a_token_that_is_no_number(t, dtype):
+    """Tiny tokens, one of them with a NaN: its output is NaN (quantized in the product, gathered, gated)."""
+    gate_up = qw.block_quantize(torch.rand(2, 256, 256, device="cuda") + 0.5, 128)
+    down = qw.block_quantize(torch.rand(2, 256, 128, device="cuda") + 0.5, 128)
+    x = (torch.rand(t, 256, device="cuda") * 1e-18).to(dtype)
+    ids = torch.arange(t, device="cuda")[:, None] % 2
+    clean = qw.moe_mlp(gate_up, down, x, ids)
+    x[1, 130] = float("nan")
+    y = qw.moe_mlp(gate_up, down, x, ids)
+    keep = torch.arange(t, device="cuda") != 1
+    assert bool(torch.isnan(y[1]).all()) and torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("m", [4, 40, 300])
+def test_weights_that_are_no_number(block_rows, m):
+    """A NaN in a tiny weight reaches its own column of y, and only that."""
+    clean, dirty = poisoned(140, 384, 1e-18, float("nan"), torch.float32)
+    x = torch.rand(m, 384, device="cuda") + 0.5
+    for dtype in (torch.float32, torch.bfloat16):
+        a = qw.block_matmul(qw.block_quantize(clean, block_rows), x, out_dtype=dtype)
+        b = qw.block_matmul(qw.block_quantize(dirty, block_rows), x, out_dtype=dtype)
+        keep = torch.arange(140, device="cuda") != 2
+        assert bool(torch.isnan(b[:, 2]).all()) and torch.equal(a[:, keep], b[:, keep])
