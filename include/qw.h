@@ -636,6 +636,21 @@ int qw_moe_mlp(int block_rows, int64_t experts, int64_t d, int64_t f,
 int qw_debug_path(int op, int bits, int64_t group, int64_t n, int64_t k,
                   const void* a, const void* b);
 
+/*
+ * The same for block-scaled products and the expert MLP; `op`:
+ *   0 qw_block_gemm of m rows, and qw_block_matmul where it quantizes x first:
+ *     1 = stream kernel, otherwise 1000 * weight rows + tokens of a tile (16 or 32
+ *     weight rows: direct kernel, more: tiled)
+ *   1 the tile of what op 0 cuts off (the weight rows behind the last whole
+ *     round of tiles), 0 = it cuts nothing off
+ *   2 qw_block_gemm_grouped of m rows, as op 0
+ *   3 qw_moe_mlp of m slots, f = n and d = k: 1 = the products quantize
+ *     tokens and gate, 2 = one call after another, 3 = the first product
+ *     gates
+ *   4 a product within qw_moe_mlp, as op 2
+ */
+int qw_block_debug_path(int op, int64_t experts, int64_t m, int64_t n, int64_t k, int y_type);
+
 #ifdef __cplusplus
 }
 #endif

@@ -958,12 +958,19 @@ constexpr Shape kShapes[] = {
 };
 constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
 
-// Estimated us of n weight rows against m rows of x (of `experts` experts).
+// The kernels beside kShapes: the stream kernel, and the direct one's 16 x 16 tiles.
+enum { kStream = -1, kDirect16 = -2 };
+
+// Estimated us of n weight rows against m rows of x (of `experts` experts); the
+// tiled kernel takes a block of k at least, and a tile with each thread block.
 double cost_of(const Shape& s, int64_t n, int64_t m, int64_t experts, int kb, bool exact) {
   const int64_t spare = std::min(experts, m) / 2;  // half-empty tiles
   const double tiles_m = experts ? (double)m / s.bm + spare + 1 : (double)((m + s.bm - 1) / s.bm);
-  const double rounds = std::ceil(tiles_m * ((n + s.bn - 1) / s.bn) / kUnits);
+  const double tiles_n = (double)((n + s.bn - 1) / s.bn);
+  const double rounds = std::ceil(tiles_m * tiles_n / kUnits);
   if (!s.tiled) return 4.0 + rounds * (s.bn + s.bm) * kb * (QW_BLOCK / 28000.0);
+  const int64_t most = experts ? std::min(m, m / s.bm + experts) : (int64_t)tiles_m;
+  if (kb == 0 || most * tiles_n > 1 << 22) return 1e30;
   const double step = exact ? s.exact : s.step;
   return step == 0.0 ? 1e30 : rounds * (3.0 + kb * step);
 }
@@ -981,11 +988,41 @@ int best_shape(int64_t n, int64_t m, int64_t experts, int kb, bool exact, double
   return best;
 }
 
+// How a product is run: with one shape, or (cut > 0) with `shape` up to weight row
+// `cut` and with `rest` from there on.
+struct Plan {
+  int shape, rest;
+  int64_t cut;
+};
+
+Plan plan_of(int64_t n, int64_t m, int kb, bool exact) {
+  if (m <= 16) return {kb > 0 && kb <= kStreamMaxKb ? kStream : kDirect16, 0, 0};
+  double cost;
+  const int shape = best_shape(n, m, 0, kb, exact, &cost);
+  const Shape& s = kShapes[shape];
+  if (!s.tiled) return {shape, 0, 0};
+  // the weight rows of whole rounds, and the rest with another shape; the cut lies
+  // between blocks of 128 rows, which share a scale (a tile of 64 is half of one)
+  const int64_t tiles_m = (m + s.bm - 1) / s.bm, tiles_n = (n + s.bn - 1) / s.bn;
+  const int64_t whole = tiles_m * tiles_n / kUnits * kUnits / tiles_m;
+  const int64_t cut = whole * s.bn / QW_BLOCK * QW_BLOCK;
+  if (cut > 0 && cut < n) {
+    double rest;
+    const int other = best_shape(n - cut, m, 0, kb, exact, &rest);
+    if (cost_of(s, cut, m, 0, kb, exact) + rest + 2.0 < cost) return {shape, other, cut};
+  }
+  return {shape, 0, 0};
+}
+
+int grouped_plan(int64_t n, int64_t m, int64_t experts, int kb, bool exact) {
+  // an average of 16 rows an expert: each expert's weight is read about once
+  if (m <= 16 * experts && kb > 0 && kb <= kStreamMaxKb) return kStream;
+  double cost;
+  return best_shape(n, m, experts, kb, exact, &cost);
+}
+
 template <bool GROUPED>
 hipError_t run_shape(int shape, const GemmArgs& a, const BlockGemm& g, hipStream_t stream) {
-  // no k, or more tiles than a launch holds: the direct kernel loops over them
-  const int64_t most = (a.m / 64 + a.experts + 1) * (a.n / 64 + 1);
-  if (a.kb == 0 || most > 1 << 22) shape = 6;
   switch (shape) {
     case 0: return run_tiled<8, 4, 4, 2, false, GROUPED>(a, g, stream);
     case 1: return run_tiled<8, 2, 4, 3, false, GROUPED>(a, g, stream);
@@ -1039,29 +1076,13 @@ hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t stream) {
     return vec ? run_stream<false, ROWS, true, uint16_t>(a, g, stream)
                : run_stream<false, ROWS, false, uint16_t>(a, g, stream);
   }
-  if (g.m <= 16 && a.kb > 0 && a.kb <= kStreamMaxKb)
-    return run_stream<false, ROWS, true, uint8_t>(a, g, stream);
-  if (g.m <= 16) return run_direct<1, 1, 8, 4, false>(a, g, stream);
-  double cost;
-  const int shape = best_shape(g.n, g.m, 0, a.kb, g.exact, &cost);
-  if (kShapes[shape].tiled) {
-    // the weight rows of whole rounds, and the rest with another shape; the cut lies
-    // between blocks of 128 rows, which share a scale (a tile of 64 is half of one)
-    const Shape& s = kShapes[shape];
-    const int64_t tiles_m = (g.m + s.bm - 1) / s.bm, tiles_n = (g.n + s.bn - 1) / s.bn;
-    const int64_t whole = tiles_m * tiles_n / kUnits * kUnits / tiles_m;
-    const int64_t cut = whole * s.bn / QW_BLOCK * QW_BLOCK;
-    if (cut > 0 && cut < g.n) {
-      double rest;
-      const int other = best_shape(g.n - cut, g.m, 0, a.kb, g.exact, &rest);
-      if (cost_of(s, cut, g.m, 0, a.kb, g.exact) + rest + 2.0 < cost) {
-        const hipError_t e = run_shape<false>(shape, part_of(a, g, 0, cut), g, stream);
-        if (e != hipSuccess) return e;
-        return run_shape<false>(other, part_of(a, g, cut, g.n - cut), g, stream);
-      }
-    }
-  }
-  return run_shape<false>(shape, a, g, stream);
+  const Plan plan = plan_of(g.n, g.m, a.kb, g.exact);
+  if (plan.shape == kStream) return run_stream<false, ROWS, true, uint8_t>(a, g, stream);
+  if (plan.shape == kDirect16) return run_direct<1, 1, 8, 4, false>(a, g, stream);
+  if (plan.cut == 0) return run_shape<false>(plan.shape, a, g, stream);
+  const hipError_t e = run_shape<false>(plan.shape, part_of(a, g, 0, plan.cut), g, stream);
+  if (e != hipSuccess) return e;
+  return run_shape<false>(plan.rest, part_of(a, g, plan.cut, g.n - plan.cut), g, stream);
 }
 
 hipError_t launch_block_gemm_grouped(const BlockGemm& g, int64_t experts,
@@ -1069,11 +1090,25 @@ hipError_t launch_block_gemm_grouped(const BlockGemm& g, int64_t experts,
   GemmArgs a = args_of(g);
   a.experts = (int)experts;
   a.offsets = offsets;
-  // an average of 16 rows an expert: each expert's weight is read about once
-  if (g.m <= 16 * experts && a.kb > 0 && a.kb <= kStreamMaxKb)
-    return run_stream<true, ROWS, true, uint8_t>(a, g, stream);
-  double cost;
-  return run_shape<true>(best_shape(g.n, g.m, experts, a.kb, g.exact, &cost), a, g, stream);
+  const int shape = grouped_plan(g.n, g.m, experts, a.kb, g.exact);
+  if (shape == kStream) return run_stream<true, ROWS, true, uint8_t>(a, g, stream);
+  return run_shape<true>(shape, a, g, stream);
+}
+
+namespace {
+int path_of(int shape) {
+  if (shape == kStream) return 1;
+  return shape == kDirect16 ? 16016 : kShapes[shape].bn * 1000 + kShapes[shape].bm;
+}
+}  // namespace
+
+int block_gemm_path(int64_t n, int64_t m, int64_t k, bool exact, bool rest) {
+  const Plan p = plan_of(n, m, (int)(pitch(k) / QW_BLOCK), exact);
+  return rest ? p.cut > 0 ? path_of(p.rest) : 0 : path_of(p.shape);
+}
+
+int block_gemm_grouped_path(int64_t n, int64_t m, int64_t k, int64_t experts, bool exact) {
+  return path_of(grouped_plan(n, m, experts, (int)(pitch(k) / QW_BLOCK), exact));
 }
 
 // Few rows an expert: what a block of the stream kernel spends on quantizing them

@@ -792,6 +792,24 @@ int qw_moe_mlp(int block_rows, int64_t experts, int64_t d, int64_t f, const uint
   return qw_moe_combine(t, topk, d, rows, QW_F32, b + at.ys, pos, weights, y_type, y, stream);
 }
 
+int qw_block_debug_path(int op, int64_t experts, int64_t m, int64_t n, int64_t k, int y_type) {
+  const bool mlp = op == 3;
+  if (op < 0 || op > 4 || (op > 1 && (experts < 1 || experts > QW_MOE_MAX_EXPERTS)))
+    return QW_EARG;
+  if (!type_ok(y_type)) return QW_EARG;
+  int st = mlp ? check_mlp(m, 1, experts, k, n) : check_block(1, op > 1 ? experts : 1, n, k);
+  if (st != QW_OK) return st;
+  if (op > 1 && m > QW_MOE_MAX_SLOTS) return QW_EM;
+  if (!mlp) st = check_rows(m, n, k);
+  if (st != QW_OK) return st;
+  if (mlp) {
+    const MlpWork at(m, 1, experts, k, n);
+    return at.few ? 1 : at.gates ? 3 : 2;
+  }
+  if (op < 2) return qw::block_gemm_path(n, m, k, y_type == QW_F32, op == 1);
+  return qw::block_gemm_grouped_path(n, m, k, experts, op == 2 && y_type == QW_F32);
+}
+
 // Which kernel family a call with these arguments would take (1 = fast,
 // 2 = block, 3 = generic, 4 = matrix-core GEMV; for op 5, 1 = GEMV and
 // 2 = GEMM; negative = invalid arguments).  Used by the tests to make sure

@@ -109,6 +109,11 @@ bool block_gemm_gates(int64_t rows, int64_t experts, int64_t f, int64_t k);
 hipError_t launch_block_gemm_gated(const BlockGemm& g, int64_t experts, const int32_t* offsets,
                                    float* ys, hipStream_t stream);
 
+// The kernel that launch_block_gemm and launch_block_gemm_grouped take, as
+// qw_block_debug_path reports it.
+int block_gemm_path(int64_t n, int64_t m, int64_t k, bool exact, bool rest);
+int block_gemm_grouped_path(int64_t n, int64_t m, int64_t k, int64_t experts, bool exact);
+
 // Tokens sorted by expert and back (moe.hip).
 int64_t moe_sort_work_bytes(int64_t slots, int64_t experts);
 hipError_t launch_moe_sort(int64_t slots, int64_t experts, int id_bytes, const void* ids,

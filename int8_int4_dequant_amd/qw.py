@@ -42,7 +42,8 @@ EXPORTS = ["qw_payload_bytes", "qw_num_scales", "qw_status_string", "qw_last_err
            "qw_block_quantize_swiglu", "qw_block_unpack", "qw_block_gemm",
            "qw_block_matmul_work_bytes", "qw_block_matmul", "qw_block_gemm_grouped",
            "qw_moe_sort_work_bytes", "qw_moe_sort", "qw_moe_gather", "qw_moe_gather_block",
-           "qw_moe_combine", "qw_moe_combine_backward", "qw_moe_mlp_work_bytes", "qw_moe_mlp"]
+           "qw_moe_combine", "qw_moe_combine_backward", "qw_moe_mlp_work_bytes", "qw_moe_mlp",
+           "qw_block_debug_path"]
 
 
 # Rows up to which qw_matmul runs the codes GEMV (QW_MATMUL_GEMV_MAX_M in qw.h).
@@ -186,6 +187,8 @@ def lib():
     L.qw_moe_mlp.argtypes = [i32, i64, i64, i64, vp, vp, vp, vp, i64, i64, i32, vp, i32, vp, vp,
                              i32, vp, vp, i64, vp]
     L.qw_moe_mlp.restype = i32
+    L.qw_block_debug_path.argtypes = [i32, i64, i64, i64, i64, i32]
+    L.qw_block_debug_path.restype = i32
     _lib = L
     return L
 
@@ -425,6 +428,10 @@ def qw_moe_mlp(block_rows, experts, d, f, gate_up, gate_up_scales, down, down_sc
                             _ptr(down), _ptr(down_scales), t, topk, x_type, _ptr(x), id_bytes,
                             _ptr(ids), _ptr(weights), y_type, _ptr(y), _ptr(work), work_bytes,
                             _stream(stream))
+
+
+def qw_block_debug_path(op, experts, m, n, k, y_type):
+    return lib().qw_block_debug_path(op, experts, m, n, k, y_type)
 
 
 # -------------------------------------------------------- convenience layer

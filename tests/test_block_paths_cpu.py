@@ -1,0 +1,64 @@
+"""Which kernel a block-scaled product takes (host code, nothing is launched)."""
+
+import random
+
+import pytest
+
+from int8_int4_dequant_amd import qw
+
+ESHAPE, EM, EARG = -3, -4, -9
+F32, BF16 = 0, 1
+
+
+def path(op, m, n, k, y_type=BF16, experts=0):
+    return qw.qw_block_debug_path(op, experts, m, n, k, y_type)
+
+
+@pytest.mark.parametrize("m,n,k,y_type,tile", [
+    (131072, 151936, 4096, BF16, 256256),    # logits of a long batch: 0.3 million tiles
+    (131072, 151936, 4096, F32, 128256),
+    (1 << 20, 65536, 1024, BF16, 256256),
+    (1 << 26, 200, 300, BF16, 256256),
+])
+def test_large_products_are_tiled(m, n, k, y_type, tile):
+    assert path(0, m, n, k, y_type) == tile
+
+
+@pytest.mark.parametrize("m,n,k,experts,y_type,tile", [
+    (1 << 20, 16384, 4096, 128, BF16, 256256),
+    (1 << 20, 16384, 4096, 128, F32, 128256),
+    (1 << 21, 28672, 8192, 8, BF16, 256256),
+])
+def test_large_grouped_products_are_tiled(m, n, k, experts, y_type, tile):
+    assert path(2, m, n, k, y_type, experts) == tile
+
+
+def test_small_products():
+    assert path(0, 8, 4096, 4096) == 1 and path(0, 16, 100, 128, F32) == 1
+    assert path(0, 8, 100, 128 * 97) == 16016
+    assert path(0, 300, 100, 0) == 32032         # nothing to sum
+    assert path(2, 64, 100, 300, BF16, 4) == 1
+    assert path(1, 2048, 28672, 8192) == 256128 and path(1, 100, 4096, 512) == 0
+
+
+def test_tiles_fit_a_launch():
+    """A tiled kernel is one launch, of at most 2^22 thread blocks."""
+    rng = random.Random(5)
+    for _ in range(20000):
+        k = rng.choice([1, 100, 128, 300, 4096, 1 << 22])
+        kp = qw.qw_block_pitch(k)
+        m = int(2 ** rng.uniform(4, 36)) // kp + 17
+        n = int(2 ** rng.uniform(0, 36)) // max(m, kp) + 1
+        experts = rng.choice([0, 0, 1, 8, 512])
+        tile = path(2 if experts else 0, m, n, k, rng.choice([F32, BF16]), experts)
+        if tile > 33000:
+            bn, bm = divmod(tile, 1000)
+            assert (min(m, (m + max(experts, 1) * (bm - 1)) // bm)) * -(-n // bn) <= 1 << 22, (m, n, k, experts)
+
+
+def test_refusals():
+    assert path(5, 8, 8, 8) == path(-1, 8, 8, 8) == path(0, 8, 8, 8, 2) == EARG
+    assert path(2, 8, 8, 8, F32, 0) == path(4, 8, 8, 8, F32, 513) == path(3, 8, 8, 8, F32, 0) == EARG
+    assert path(0, 8, -1, 8) == path(0, 8, 8, -1) == path(0, 8, 8, (1 << 22) + 1) == ESHAPE
+    assert path(0, -1, 8, 8) == path(2, (1 << 30) + 1, 8, 8, F32, 2) == EM
+    assert path(3, (1 << 30) + 1, 8, 8, F32, 2) == ESHAPE
