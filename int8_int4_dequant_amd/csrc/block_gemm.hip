@@ -1144,8 +1144,7 @@ hipError_t launch_block_gemm_gates(const BlockGemm& g, int64_t experts, const in
 // From 64 rows an expert on the tiles are filled well enough; the blocks of the
 // result have to be blocks of the weight's rows (f = 0 has no tile to launch).
 bool block_gemm_gates(int64_t rows, int64_t experts, int64_t f, int64_t k) {
-  return rows > 64 * experts && f > 0 && f % QW_BLOCK == 0 && k > 0 &&
-         (rows / 128 + experts + 1) * (f / QW_BLOCK) <= 1 << 22;
+  return rows > 64 * experts && f > 0 && f % QW_BLOCK == 0 && k > 0;
 }
 
 hipError_t launch_block_gemm_gated(const BlockGemm& g, int64_t experts, const int32_t* offsets,

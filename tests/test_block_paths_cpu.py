@@ -33,6 +33,13 @@ def test_large_grouped_products_are_tiled(m, n, k, experts, y_type, tile):
     assert path(2, m, n, k, y_type, experts) == tile
 
 
+def test_expert_mlp_ways():
+    assert path(3, 32, 1408, 4096, BF16, 64) == 1
+    assert path(3, 64 * 64, 1408, 2048, BF16, 64) == 2 and path(3, 64 * 64 + 1, 1408, 2048, BF16, 64) == 3
+    assert path(3, 65536, 1 << 19, 128, BF16, 512) == 3      # its blocks take tile after tile
+    assert path(3, 9000, 1400, 2048, BF16, 64) == 2
+
+
 def test_small_products():
     assert path(0, 8, 4096, 4096) == 1 and path(0, 16, 100, 128, F32) == 1
     assert path(0, 8, 100, 128 * 97) == 16016
