@@ -611,9 +611,11 @@ int qw_moe_combine_backward(int64_t t, int64_t topk, int64_t d, int64_t rows, in
  *   x [t][d], ids [t][topk] as in qw_moe_sort, weights fp32 [t][topk] or NULL
  *   y [t][d]
  *   work: qw_moe_mlp_work_bytes(...) bytes, 16-byte aligned (QW_EWORK)
- * block_rows is that of both weights.  Both products have fp32 results, on the
- * 8-bit cores where there are many rows (see qw_block_gemm): what those drop is
- * far below the rounding of the hidden values to codes.
+ * block_rows is that of both weights.  Both products and the sum over j have
+ * fp32 results, and y_type decides about the products' sums as in
+ * qw_block_gemm: QW_F32 is the calls one by one in fp32; with QW_BF16 the 8-bit
+ * cores take them where there are many rows, and some of the hidden codes are
+ * their neighbours.
  */
 int64_t qw_moe_mlp_work_bytes(int64_t t, int64_t topk, int64_t experts, int64_t d, int64_t f);
 int qw_moe_mlp(int block_rows, int64_t experts, int64_t d, int64_t f,
@@ -643,11 +645,11 @@ int qw_debug_path(int op, int bits, int64_t group, int64_t n, int64_t k,
  *     weight rows: direct kernel, more: tiled)
  *   1 the tile of what op 0 cuts off (the weight rows behind the last whole
  *     round of tiles), 0 = it cuts nothing off
- *   2 qw_block_gemm_grouped of m rows, as op 0
+ *   2 qw_block_gemm_grouped of m rows, and the products within qw_moe_mlp
+ *     with y of that type, as op 0
  *   3 qw_moe_mlp of m slots, f = n and d = k: 1 = the products quantize
  *     tokens and gate, 2 = one call after another, 3 = the first product
  *     gates
- *   4 a product within qw_moe_mlp, as op 2
  */
 int qw_block_debug_path(int op, int64_t experts, int64_t m, int64_t n, int64_t k, int y_type);
 

@@ -689,15 +689,16 @@ int qw_moe_combine_backward(int64_t t, int64_t topk, int64_t d, int64_t rows, in
 namespace {
 
 // The buffers of qw_moe_mlp in its work buffer, and the way it takes: few rows
-// are quantized by the products themselves, many gated by the first one.
+// are quantized by the products themselves, many gated by the first one (on the
+// 8-bit cores: for bf16 y).
 struct MlpWork {
   bool few, gates;
   int64_t pos, order, offsets, sort, xc, xs, h, hc, hs, ys, bytes;
-  MlpWork(int64_t t, int64_t topk, int64_t experts, int64_t d, int64_t f) {
+  MlpWork(int64_t t, int64_t topk, int64_t experts, int64_t d, int64_t f, int y_type) {
     const int64_t rows = t * topk;
     few = qw::block_gemm_grouped_fuses(rows, experts, d) &&
           qw::block_gemm_grouped_fuses(rows, experts, f);
-    gates = qw::block_gemm_gates(rows, experts, f, d);
+    gates = y_type == QW_BF16 && qw::block_gemm_gates(rows, experts, f, d);
     Carve c;
     pos = c.take(rows * 4);
     order = c.take(few ? rows * 4 : 0);
@@ -705,7 +706,7 @@ struct MlpWork {
     sort = c.take(qw::moe_sort_work_bytes(rows, experts));
     xc = c.take(few ? 0 : rows * qw::pitch(d));
     xs = c.take(few ? 0 : qw::block_scales(1, rows, d) * 4);
-    h = c.take(gates ? 0 : rows * 2 * f * 4);
+    h = c.take(rows * 2 * f * 4);  // the size does not depend on y's type
     hc = c.take(few ? 0 : rows * qw::pitch(f));
     hs = c.take(few ? 0 : qw::block_scales(1, rows, f) * 4);
     ys = c.take(rows * d * 4);
@@ -727,7 +728,7 @@ extern "C" {
 
 int64_t qw_moe_mlp_work_bytes(int64_t t, int64_t topk, int64_t experts, int64_t d, int64_t f) {
   if (check_mlp(t, topk, experts, d, f) != QW_OK) return -1;
-  return MlpWork(t, topk, experts, d, f).bytes;
+  return MlpWork(t, topk, experts, d, f, QW_F32).bytes;
 }
 
 int qw_moe_mlp(int block_rows, int64_t experts, int64_t d, int64_t f, const uint8_t* gate_up,
@@ -746,7 +747,7 @@ int qw_moe_mlp(int block_rows, int64_t experts, int64_t d, int64_t f, const uint
   if (!x || !ids || !y || (f > 0 && (!gate_up || !gate_up_scales || !down || !down_scales)))
     return QW_ENULL;
   if (!qw::aligned(gate_up, 16) || !qw::aligned(down, 16)) return QW_EARG;
-  const MlpWork at(t, topk, experts, d, f);
+  const MlpWork at(t, topk, experts, d, f, y_type);
   if (!work || work_bytes < at.bytes || !qw::aligned(work, 16)) return QW_EWORK;
   uint8_t* const b = (uint8_t*)work;
   const int64_t rows = t * topk;
@@ -757,10 +758,12 @@ int qw_moe_mlp(int block_rows, int64_t experts, int64_t d, int64_t f, const uint
   st = qw_moe_sort(t, topk, experts, id_bytes, ids, pos, order, offsets, b + at.sort,
                    at.xc - at.sort, stream);
   if (st != QW_OK) return st;
+  // fp32 results either way; y's type decides how exact their sums are
+  const bool exact = y_type == QW_F32;
   qw::BlockGemm up = {block_rows, 2 * f, d, rows, gate_up, gate_up_scales, x_type, x,
-                      nullptr, nullptr, QW_F32, b + at.h, false};
+                      nullptr, nullptr, QW_F32, b + at.h, exact};
   qw::BlockGemm out = {block_rows, d, f, rows, down, down_scales, QW_F32, b + at.h,
-                       nullptr, nullptr, QW_F32, b + at.ys, false};
+                       nullptr, nullptr, QW_F32, b + at.ys, exact};
   if (at.few) {
     st = record(qw::launch_block_gemm_tokens(up, experts, offsets, order, topk, s));
     if (st != QW_OK) return st;
@@ -794,7 +797,7 @@ int qw_moe_mlp(int block_rows, int64_t experts, int64_t d, int64_t f, const uint
 
 int qw_block_debug_path(int op, int64_t experts, int64_t m, int64_t n, int64_t k, int y_type) {
   const bool mlp = op == 3;
-  if (op < 0 || op > 4 || (op > 1 && (experts < 1 || experts > QW_MOE_MAX_EXPERTS)))
+  if (op < 0 || op > 3 || (op > 1 && (experts < 1 || experts > QW_MOE_MAX_EXPERTS)))
     return QW_EARG;
   if (!type_ok(y_type)) return QW_EARG;
   int st = mlp ? check_mlp(m, 1, experts, k, n) : check_block(1, op > 1 ? experts : 1, n, k);
@@ -803,11 +806,11 @@ int qw_block_debug_path(int op, int64_t experts, int64_t m, int64_t n, int64_t k
   if (!mlp) st = check_rows(m, n, k);
   if (st != QW_OK) return st;
   if (mlp) {
-    const MlpWork at(m, 1, experts, k, n);
+    const MlpWork at(m, 1, experts, k, n, y_type);
     return at.few ? 1 : at.gates ? 3 : 2;
   }
   if (op < 2) return qw::block_gemm_path(n, m, k, y_type == QW_F32, op == 1);
-  return qw::block_gemm_grouped_path(n, m, k, experts, op == 2 && y_type == QW_F32);
+  return qw::block_gemm_grouped_path(n, m, k, experts, y_type == QW_F32);
 }
 
 // Which kernel family a call with these arguments would take (1 = fast,

@@ -88,7 +88,7 @@ struct BlockGemm {
   const float* xs;
   int y_type;
   void* y;
-  bool exact;  // fp32 y: on the bf16 cores (only a grouped product may go without)
+  bool exact;  // fp32 y: on the bf16 cores (within an expert MLP with bf16 y it goes without)
 };
 hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t stream);
 hipError_t launch_block_gemm_grouped(const BlockGemm& g, int64_t experts,

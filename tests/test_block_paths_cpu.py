@@ -38,6 +38,7 @@ def test_expert_mlp_ways():
     assert path(3, 64 * 64, 1408, 2048, BF16, 64) == 2 and path(3, 64 * 64 + 1, 1408, 2048, BF16, 64) == 3
     assert path(3, 65536, 1 << 19, 128, BF16, 512) == 3      # its blocks take tile after tile
     assert path(3, 9000, 1400, 2048, BF16, 64) == 2
+    assert path(3, 9000, 1408, 2048, F32, 64) == 2           # fp32 sums: on the bf16 cores
 
 
 def test_small_products():
@@ -64,8 +65,8 @@ def test_tiles_fit_a_launch():
 
 
 def test_refusals():
-    assert path(5, 8, 8, 8) == path(-1, 8, 8, 8) == path(0, 8, 8, 8, 2) == EARG
-    assert path(2, 8, 8, 8, F32, 0) == path(4, 8, 8, 8, F32, 513) == path(3, 8, 8, 8, F32, 0) == EARG
+    assert path(4, 8, 8, 8) == path(-1, 8, 8, 8) == path(0, 8, 8, 8, 2) == EARG
+    assert path(2, 8, 8, 8, F32, 0) == path(2, 8, 8, 8, F32, 513) == path(3, 8, 8, 8, F32, 0) == EARG
     assert path(0, 8, -1, 8) == path(0, 8, 8, -1) == path(0, 8, 8, (1 << 22) + 1) == ESHAPE
     assert path(0, -1, 8, 8) == path(2, (1 << 30) + 1, 8, 8, F32, 2) == EM
     assert path(3, (1 << 30) + 1, 8, 8, F32, 2) == ESHAPE
