@@ -544,7 +544,9 @@ int qw_block_gemm_grouped(int block_rows, int64_t experts, int64_t n, int64_t k,
 #define QW_MOE_MAX_EXPERTS 512
 #define QW_MOE_MAX_SLOTS (1ll << 30)
 
-/* Work bytes for qw_moe_sort (-1 if invalid). */
+/* Work bytes for qw_moe_sort (-1 if invalid).  They and qw_moe_mlp_work_bytes
+ * grow with every argument: a buffer for the largest call is enough for all
+ * smaller ones. */
 int64_t qw_moe_sort_work_bytes(int64_t t, int64_t topk, int64_t experts);
 
 /*

@@ -395,8 +395,11 @@ hipError_t run_backward(int64_t t, int topk, int64_t d, int64_t rows, const T* d
 }  // namespace
 
 int64_t moe_sort_work_bytes(int64_t slots, int64_t experts) {
-  const int64_t run = sort_run(slots), blocks = (slots + run - 1) / run;
-  return blocks > 1 ? (blocks * experts * 4 + 255) / 256 * 256 : 0;
+  if (slots <= kSortOne) return 0;
+  // at least sort()'s blocks, without their number's falls where the run grows:
+  // what is enough for more slots is enough for fewer
+  const int64_t blocks = std::min<int64_t>((slots + 64 * kSortWaves - 1) / (64 * kSortWaves), kSortBlocks);
+  return (blocks * experts * 4 + 255) / 256 * 256;
 }
 
 hipError_t launch_moe_sort(int64_t slots, int64_t experts, int id_bytes, const void* ids,

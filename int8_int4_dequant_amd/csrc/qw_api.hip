@@ -699,16 +699,18 @@ struct MlpWork {
     few = qw::block_gemm_grouped_fuses(rows, experts, d) &&
           qw::block_gemm_grouped_fuses(rows, experts, f);
     gates = y_type == QW_BF16 && qw::block_gemm_gates(rows, experts, f, d);
+    // every buffer, whichever way: a size that grows with every argument, so that
+    // what is enough for the largest call is enough for all smaller ones
     Carve c;
     pos = c.take(rows * 4);
-    order = c.take(few ? rows * 4 : 0);
+    order = c.take(rows * 4);
     offsets = c.take((experts + 1) * 4);
     sort = c.take(qw::moe_sort_work_bytes(rows, experts));
-    xc = c.take(few ? 0 : rows * qw::pitch(d));
-    xs = c.take(few ? 0 : qw::block_scales(1, rows, d) * 4);
-    h = c.take(rows * 2 * f * 4);  // the size does not depend on y's type
-    hc = c.take(few ? 0 : rows * qw::pitch(f));
-    hs = c.take(few ? 0 : qw::block_scales(1, rows, f) * 4);
+    xc = c.take(rows * qw::pitch(d));
+    xs = c.take(qw::block_scales(1, rows, d) * 4);
+    h = c.take(rows * 2 * f * 4);
+    hc = c.take(rows * qw::pitch(f));
+    hs = c.take(qw::block_scales(1, rows, f) * 4);
     ys = c.take(rows * d * 4);
     bytes = c.at;
   }

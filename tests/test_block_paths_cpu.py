@@ -70,3 +70,18 @@ def test_refusals():
     assert path(0, 8, -1, 8) == path(0, 8, 8, -1) == path(0, 8, 8, (1 << 22) + 1) == ESHAPE
     assert path(0, -1, 8, 8) == path(2, (1 << 30) + 1, 8, 8, F32, 2) == EM
     assert path(3, (1 << 30) + 1, 8, 8, F32, 2) == ESHAPE
+
+
+@pytest.mark.parametrize("topk,experts,d,f", [(1, 1, 128, 128), (2, 8, 512, 384), (8, 64, 4096, 1408), (3, 60, 1003, 300)])
+def test_work_for_the_largest_call_is_enough_for_smaller_ones(topk, experts, d, f):
+    L = qw.lib()
+    edges = [4 * experts, 16 * experts, 64 * experts, 4096, 1 << 18, (1 << 18) * 3, 1 << 20]
+    ts = sorted({max(0, e // topk + i) for e in edges for i in (-1, 0, 1, 2, 200)} | set(range(20)))
+    for query in (lambda t: L.qw_moe_sort_work_bytes(t, topk, experts),
+                  lambda t: L.qw_moe_mlp_work_bytes(t, topk, experts, d, f),
+                  lambda t: L.qw_block_matmul_work_bytes(t, d)):
+        sizes = [query(t) for t in ts]
+        assert min(sizes) >= 0 and sizes == sorted(sizes)
+    for t in (4 * experts // topk, 64 * experts // topk + 1):
+        for e, dd, ff in ((experts + 1, d, f), (experts, d + 1, f), (experts, d, f + 1)):
+            assert L.qw_moe_mlp_work_bytes(t, topk, e, dd, ff) >= L.qw_moe_mlp_work_bytes(t, topk, experts, d, f)
