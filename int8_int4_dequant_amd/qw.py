@@ -890,19 +890,21 @@ def _output(out, rows, cols, dtype, like):
     if out is None:
         out = torch.empty((rows, cols), dtype=dtype, device=like.device)
     else:
-        _check_tensor(out, out.dtype if dtype is None else dtype, rows * cols, "out", (rows, cols))
+        _check_tensor(out, tuple(TYPES) if dtype is None else dtype, rows * cols, "out",
+                      (rows, cols))
     return out, _type(out.dtype, "out")
 
 
 @_on_stream
-def block_gemm(rec, x, out=None, out_dtype=torch.float32, stream=None):
+def block_gemm(rec, x, out=None, out_dtype=None, stream=None):
     """y [m][n] = x . W^T of two records: ``rec`` the weight [n][k], ``x`` m
-    rows of k values with 1 x 128 blocks."""
+    rows of k values with 1 x 128 blocks; of ``out``'s type, ``out_dtype`` or
+    fp32."""
     _, n, k, br, codes, scales = _check_block(rec, "record", (2,))
     _, m, kx, bx, xc, xs = _check_block(x, "x", (2,))
     if kx != k or bx != 1:
         raise ValueError(f"x must be a record of [m][{k}] with block_rows 1")
-    out, yt = _output(out, m, n, out_dtype, x["codes"])
+    out, yt = _output(out, m, n, out_dtype or (torch.float32 if out is None else None), x["codes"])
     dev = _device_of(rec["codes"], rec["scales"], x["codes"], x["scales"], out)
     _run("qw_block_gemm", dev, stream, lib().qw_block_gemm, br, n, k, codes, scales, m, xc, xs,
          yt, out.data_ptr())
@@ -941,17 +943,18 @@ def _workspace(work, need, like):
 
 
 @_on_stream
-def block_gemm_grouped(rec, x, offsets, out=None, out_dtype=torch.float32, stream=None):
+def block_gemm_grouped(rec, x, offsets, out=None, out_dtype=None, stream=None):
     """Rows sorted by expert times each expert's weight: ``rec`` [experts][n][k],
     ``x`` a record of [rows][k] with 1 x 128 blocks, ``offsets`` device int32
-    [experts + 1] (moe_sort).  Rows that no expert has are left as they are
-    in ``out``."""
+    [experts + 1] (moe_sort); y of ``out``'s type, ``out_dtype`` or fp32.  Rows
+    that no expert has are left as they are in ``out``."""
     e, n, k, br, codes, scales = _check_block(rec, "record", (3,))
     _, rows, kx, bx, xc, xs = _check_block(x, "x", (2,))
     if kx != k or bx != 1:
         raise ValueError(f"x must be a record of [rows][{k}] with block_rows 1")
     first = _fits(offsets, _I32, e + 1, "offsets")
-    out, yt = _output(out, rows, n, out_dtype, x["codes"])
+    out, yt = _output(out, rows, n, out_dtype or (torch.float32 if out is None else None),
+                      x["codes"])
     dev = _device_of(rec["codes"], rec["scales"], x["codes"], x["scales"], offsets, out)
     _run("qw_block_gemm_grouped", dev, stream, lib().qw_block_gemm_grouped, br, e, n, k, codes,
          scales, rows, xc, xs, first, yt, out.data_ptr())

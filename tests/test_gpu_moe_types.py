@@ -1,4 +1,4 @@
-"""The expert MLP's precision follows y's type."""
+"""The expert MLP's precision follows y's type, and products take the type of `out`."""
 
 import numpy as np
 import pytest
@@ -27,3 +27,23 @@ def test_fp32_mlp_is_the_calls_one_by_one(t, topk, experts, d, f, br):
     hr = qw.block_quantize_swiglu(h, r["offsets"][-1:])
     want = qw.moe_combine(qw.block_gemm_grouped(down, hr, r["offsets"]), r, w)
     assert y.dtype == torch.float32 and torch.equal(y, want)
+
+
+
+def test_products_take_the_type_of_out():
+    rec = qw.block_quantize(torch.randn(130, 300, device="cuda"), 128)
+    x = qw.block_quantize(torch.randn(20, 300, device="cuda"), 1)
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.empty(20, 130, dtype=dtype, device="cuda")
+        assert qw.block_gemm(rec, x, out=out) is out
+        assert torch.equal(out, qw.block_gemm(rec, x, out_dtype=dtype))
+        with pytest.raises(ValueError):
+            qw.block_gemm(rec, x, out=out, out_dtype=torch.float32 if dtype is torch.bfloat16 else torch.bfloat16)
+    assert qw.block_gemm(rec, x).dtype == torch.float32
+    experts = qw.block_quantize(torch.randn(3, 130, 300, device="cuda"), 128)
+    off = torch.tensor([0, 5, 5, 20], dtype=torch.int32, device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.empty(20, 130, dtype=dtype, device="cuda")
+        assert qw.block_gemm_grouped(experts, x, off, out=out) is out
+        assert torch.equal(out, qw.block_gemm_grouped(experts, x, off, out_dtype=dtype))
+    assert qw.block_gemm_grouped(experts, x, off).dtype == torch.float32
