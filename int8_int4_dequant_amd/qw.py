@@ -725,7 +725,7 @@ def gptq(w, h, bits, group, damp=0.01, stream=None):
 # [.., rows of blocks][pitch / 128].
 #
 # These calls run on the device that their tensors are on, and on its current
-# stream where none is given (`stream` is a keyword).
+# stream where none is given.
 
 
 def _rows_of_blocks(n, block_rows):
@@ -779,16 +779,32 @@ def _run(what, dev, stream, fn, *args):
         _check(status, what)
 
 
+def _device_among(args):
+    """Index of the device of the first tensor among a call's arguments."""
+    for a in args:
+        if isinstance(a, dict):
+            a = a.get("codes", a.get("pos"))
+        if isinstance(a, torch.Tensor) and a.get_device() >= 0:
+            return a.get_device()
+    return None
+
+
 def _on_stream(f):
-    """``stream`` (a torch stream or a hipStream_t) as the current stream of
-    the whole call, so that what it allocates belongs to that stream too."""
+    """``stream`` (a torch stream or a hipStream_t of the tensors' device) as
+    the current stream of the whole call, so that what it allocates belongs
+    to that stream too."""
+    last = f.__code__.co_varnames.index("stream")  # its place if not a keyword
+
     @functools.wraps(f)
     def call(*args, **kwargs):
         stream = kwargs.pop("stream", None) if kwargs else None
+        if len(args) == last + 1 and stream is None:
+            *args, stream = args
         if stream is None:
             return f(*args, **kwargs)
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            dev = _device_among((*args, *kwargs.values()))
+            stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
         with torch.cuda.stream(stream):
             return f(*args, stream=stream, **kwargs)
     return call
