@@ -494,14 +494,18 @@ int qw_block_unpack(int block_rows, int64_t count, int64_t n, int64_t k,
  *   x_codes, x_scales   m rows of k values, 1 x 128     (read)
  *   y                   [m][n]                          (written), m >= 0
  * A block of 128 is summed before its scales are applied; sums are held in
- * fp32.  Deterministic: the same call gives the same bits, and rows of x do not
- * influence each other.
+ * fp32, one block added after the other.  Deterministic: the same call gives
+ * the same bits, and rows of x do not influence each other.  With
+ * A = sum_j |x[r][j] * w[i][j]|:
  *   y_type QW_F32   on the bf16 matrix cores, which take the codes exactly:
- *                   error <= 1e-5 * sum_j |x[r][j] * w[i][j]|
+ *                   error <= (1e-5 + k/128 * 2^-24) * A
  *   y_type QW_BF16  on the 8-bit cores, twice as fast; they keep 13 bits below
  *                   the largest of 8 products that they add at a time:
- *                   error <= 1e-3 * sum_j |x[r][j] * w[i][j]| (about 1e-5 of
- *                   y's size for values of similar size), and y's rounding
+ *                   error <= (1e-3 + k/128 * 2^-24) * A (about 1e-5 of y's
+ *                   size for values of similar size), and y's rounding
+ * A block's two scales are multiplied with each other first: the bounds hold
+ * where that product, about max|x| max|w| / 2^18, is a normal fp32 number
+ * (2^-126 .. 2^128).
  */
 int qw_block_gemm(int block_rows, int64_t n, int64_t k, const uint8_t* codes,
                   const float* scales, int64_t m, const uint8_t* x_codes,
