@@ -459,7 +459,7 @@ bool type_ok(int type) { return type == QW_F32 || type == QW_BF16; }
 int check_block(int brows, int64_t count, int64_t n, int64_t k) {
   if (brows != 1 && brows != QW_BLOCK) return QW_EARG;
   if (!within(n, k) || !within(n, qw::pitch(k))) return QW_ESHAPE;
-  // n first rounded up to whole blocks, so that the number of scales fits too
+  // the codes; the scales are fewer, one for 128 of them at most
   if (!within(count, n) || !within(count * n, qw::pitch(k))) return QW_ESHAPE;
   return QW_OK;
 }

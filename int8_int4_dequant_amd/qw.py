@@ -1116,7 +1116,8 @@ def moe_mlp(gate_up, down, x, ids, weights=None, out=None, out_dtype=None, work=
     """A gated expert MLP in one call: x [t][d] (fp32 or bf16), ids [t][topk],
     weights fp32 [t][topk]; ``gate_up`` a record of [experts][2 f][d] (gate
     rows, then up rows), ``down`` of [experts][d][f].  y [t][d] of x's type or
-    ``out_dtype``."""
+    ``out_dtype``; fp32 y has fp32 sums in both products, bf16 y those of the 8-bit
+    cores where there are many rows (qw.h)."""
     e, f2, d, br, gc, gs = _check_block(gate_up, "gate_up", (3,))
     ed, dd, f, bd, dc, ds = _check_block(down, "down", (3,))
     if ed != e or dd != d or f2 != 2 * f or bd != br:
