@@ -21,32 +21,26 @@ def check(y, xrec, rec, k):
     return float((err / base).max())
 
 
-# the direct kernel's waves share k, the tiled one's do not
-SIZES = [(12, 200, False), (40, 200, False), (600, 1000, True)]
+# direct kernels, whose waves share k, and a tiled one, whose waves do not
+SIZES = [(12, 200), (40, 200), (600, 1000)]
 
 
-def is_tiled(m, n, k, dtype):
-    return qw.qw_block_debug_path(0, 0, m, n, k, qw.TYPES[dtype]) > 33000
-
-
-@pytest.mark.parametrize("m,n,tiled", SIZES)
+@pytest.mark.parametrize("m,n", SIZES)
 @pytest.mark.parametrize("k", [65600, 262144])
 @pytest.mark.parametrize("br,dtype", [(128, torch.float32), (1, torch.float32), (128, torch.bfloat16), (1, torch.bfloat16)])
-def test_long_sums_of_one_sign(m, n, tiled, k, br, dtype):
-    assert is_tiled(m, n, k, dtype) == tiled
+def test_long_sums_of_one_sign(m, n, k, br, dtype):
     g = torch.Generator(device="cuda").manual_seed(m + k)
     rec = qw.block_quantize(torch.rand(n, k, generator=g, device="cuda"), br)
     xrec = qw.block_quantize(torch.rand(m, k, generator=g, device="cuda"), 1)
     check(qw.block_gemm(rec, xrec, out_dtype=dtype), xrec, rec, k)
 
 
-@pytest.mark.parametrize("m,n,tiled", SIZES)
+@pytest.mark.parametrize("m,n", SIZES)
 @pytest.mark.parametrize("br", [1, 128])
-def test_long_sums_that_lose_every_block(m, n, tiled, br):
+def test_long_sums_that_lose_every_block(m, n, br):
     """A first block of 25690112 and 2047 of 0.76, less than half of fp32's step of
     2 there: one after another they are all lost, 6e-5 of the sum."""
     k = 262144
-    assert is_tiled(m, n, k, torch.float32) == tiled
     w = torch.full((n, k), 448.0, device="cuda")
     x = torch.full((m, k), 448 * 0.99 * 2.0 ** -25, device="cuda")
     x[:, :128] = 448.0

@@ -1,6 +1,9 @@
-"""Every tile of the block-scaled products and of the expert MLP, with more blocks
-of k than a wave's buffers hold and with more tiles than compute units, by the
-kernel that the choice reports; and sizes whose offsets pass 32 bits."""
+"""Every tile of the block-scaled products and every way of the expert MLP, with more
+blocks of k than a wave's buffers hold and with more tiles than compute units; the
+sizes are searched for by the kernel that the choice reports, so that they follow
+it.  And sizes whose offsets pass 32 bits."""
+
+import random
 
 import pytest
 import torch
@@ -36,26 +39,40 @@ def check(y, xv, wv):
     assert bool(((y.double() - ref).abs() <= bar + HALF[y.dtype] * (ref.abs() + bar)).all())
 
 
-# m, n, k, tile, tile of the rest
-TILES = [
-    (18, 16, 700, F32, 16032, 0), (33, 2078, 1300, F32, 32032, 0), (34, 4213, 700, F32, 64064, 0), (65, 8371, 700, F32, 128064, 0),
-    (5639, 265, 1100, F32, 128128, 0), (522, 6692, 1300, F32, 128256, 0), (5017, 1551, 700, F32, 128256, 16032),
-    (2560, 3265, 700, F32, 128256, 32032), (1036, 7636, 700, F32, 128256, 128064), (1046, 8854, 700, F32, 128256, 128128),
-    (18, 16, 700, BF16, 16032, 0), (33, 2078, 1300, BF16, 32032, 0), (4179, 17, 700, BF16, 64064, 0), (65, 8371, 700, BF16, 128064, 0),
-    (5639, 265, 700, BF16, 128128, 0), (6647, 1048, 700, BF16, 128256, 0), (522, 6692, 1300, BF16, 256128, 0),
-    (3353, 4668, 700, BF16, 256128, 64064), (7337, 2250, 700, BF16, 256128, 128064),
-    # the largest tile: below 16 blocks of k, and from there on with tiles that start at different ones
-    (769, 9288, 700, BF16, 256256, 0), (2048, 8192, 2048, BF16, 256256, 0), (2048, 8192, 2100, BF16, 256256, 0),
-    (2011, 8190, 2432, BF16, 256256, 0), (2048, 8192, 8192, BF16, 256256, 0), (5828, 4102, 700, BF16, 256256, 128256),
-    (2048, 28672, 2100, BF16, 256256, 256128),
-]
+def examples(dtype, grouped):
+    """{(tile, tile of the rest): the smallest size that takes them}, of 6000 drawn."""
+    rng = random.Random(3)
+    found = {}
+    for _ in range(6000):
+        m, n = int(2 ** rng.uniform(4.2, 13)), int(2 ** rng.uniform(4, 13.2))
+        k = rng.choice([700, 1100, 1300, 2100, 2432])
+        tiles = (path(2, m, n, k, dtype, 7), 0) if grouped else (path(0, m, n, k, dtype), path(1, m, n, k, dtype))
+        if tiles not in found or m * n * k < found[tiles][0]:
+            found[tiles] = (m * n * k, m, n, k)
+    return {tiles: size[1:] for tiles, size in found.items()}
+
+
+def cases(grouped):
+    return [(*size, dtype, *tiles) for dtype in (F32, BF16) for tiles, size in sorted(examples(dtype, grouped).items())]
+
+
+# the largest tile with fewer blocks of k and, starting at different ones, with 16, 17, 19, 64
+LARGEST = [(769, 9288, 700), (2048, 8192, 2048), (2048, 8192, 2100), (2011, 8190, 2432), (2048, 8192, 8192), (2048, 28672, 2100)]
+TILES = cases(False) + [(m, n, k, BF16, path(0, m, n, k, BF16), path(1, m, n, k, BF16)) for m, n, k in LARGEST]
+
+
+def test_the_cases_take_many_tiles():
+    for dtype, most in ((F32, 128 * 256), (BF16, 256 * 256)):
+        tiles = {c[4] for c in TILES if c[3] is dtype}
+        sizes = {(t // 1000) * (t % 1000) for t in tiles}
+        assert len(tiles) > 4 and most in sizes and any(c[5] for c in TILES if c[3] is dtype)
+    assert sum(c[4] == 256256 and c[2] >= 2048 and c[3] is BF16 for c in TILES) > 3
 
 
 @pytest.mark.parametrize("m,n,k,dtype,tile,rest", TILES)
 @pytest.mark.parametrize("br", [1, 128])
 def test_every_tile(m, n, k, dtype, tile, rest, br):
     print("tile", m, n, k, dtype, tile, rest, br, flush=True)
-    assert (path(0, m, n, k, dtype), path(1, m, n, k, dtype)) == (tile, rest)
     g = torch.Generator(device="cuda").manual_seed(m + n + k)
     rec, xrec = qw.block_quantize(rand(g, n, k), br), qw.block_quantize(rand(g, m, k), 1)
     y = torch.full((m + 1, n), 7.0, dtype=dtype, device="cuda")
@@ -65,24 +82,14 @@ def test_every_tile(m, n, k, dtype, tile, rest, br):
     assert torch.equal(qw.block_gemm(rec, xrec, out_dtype=dtype), y[:m])
 
 
-# rows of the experts, n, k, tile
-GROUPED = [
-    ([7, 0, 11], 16, 700, F32, 1), ([50, 0, 0], 16, 700, F32, 16032), ([1, 50, 2], 1128, 1300, F32, 32032), ([9, 0, 40], 2314, 700, F32, 64064),
-    ([3, 0, 46], 5976, 700, F32, 128064), ([20, 1, 0, 40, 3, 33, 17], 6370, 700, F32, 128128), ([20, 1, 0, 40, 3, 33, 17], 6733, 1300, F32, 128256),
-    ([50, 0, 0], 16, 700, BF16, 16032), ([9, 0, 40], 1182, 1300, BF16, 32032), ([1, 50, 2], 1128, 700, BF16, 64064),
-    ([3, 0, 46], 5976, 700, BF16, 128064), ([20, 1, 0, 40, 3, 33, 17], 6370, 700, BF16, 128128), ([4000, 3, 4100], 773, 700, BF16, 128256),
-    ([20, 1, 0, 40, 3, 33, 17], 6733, 1300, BF16, 256128), ([200, 1, 0, 100, 3, 33, 90], 8967, 700, BF16, 256256),
-    ([200, 1, 0, 100, 3, 33, 90], 8967, 2100, BF16, 256256),
-]
-
-
-@pytest.mark.parametrize("counts,n,k,dtype,tile", GROUPED)
+@pytest.mark.parametrize("rows,n,k,dtype,tile,rest", cases(True))
 @pytest.mark.parametrize("br", [1, 128])
-def test_every_grouped_tile(counts, n, k, dtype, tile, br):
-    e, used = len(counts), sum(counts)
-    rows = used + 5
-    print("grouped tile", counts, n, k, dtype, tile, br, flush=True)
-    assert path(2, used, n, k, dtype, e) == tile
+def test_every_grouped_tile(rows, n, k, dtype, tile, rest, br):
+    """Seven experts, one with most of the rows and two without any."""
+    print("grouped tile", rows, n, k, dtype, tile, br, flush=True)
+    counts = [rows // 5, 1, 0, rows // 7, 0, rows // 9]
+    counts.append(rows - sum(counts))
+    e, used, rows = 7, rows, rows + 5
     g = torch.Generator(device="cuda").manual_seed(n + k)
     rec, xrec = qw.block_quantize(rand(g, e, n, k), br), qw.block_quantize(rand(g, rows, k), 1)
     xrec = dict(xrec, shape=[used, k], codes=xrec["codes"][:used], scales=xrec["scales"][:used])
@@ -113,19 +120,25 @@ def mlp_reference(gate_up, down, x, ids, weights):
     return y
 
 
-# the way, and the second product's tile; the gated ones have more tiles than compute units
+# few rows an expert; more; many, with hidden values in whole blocks and not, and fp32 results
 MLP = [
-    (4099, 2, 6, 520, 1408, BF16, 3, 256128), (2600, 4, 8, 2048, 1408, BF16, 3, 256128), (4099, 6, 64, 2048, 1408, BF16, 3, 256256),
-    (1500, 4, 8, 1003, 512, BF16, 3, 256128), (500, 4, 64, 520, 1408, BF16, 2, 128128), (3000, 2, 5, 520, 1000, BF16, 2, 128128),
-    (4099, 2, 6, 520, 1408, F32, 2, 128256), (40, 6, 64, 520, 1408, F32, 1, 1),
+    (40, 6, 64, 520, 1408, BF16), (40, 6, 64, 520, 1408, F32), (500, 4, 64, 520, 1408, BF16), (500, 4, 64, 520, 1408, F32),
+    (4099, 2, 6, 520, 1408, BF16), (2600, 4, 8, 2048, 1408, BF16), (4099, 6, 64, 2048, 1408, BF16), (1500, 4, 8, 1003, 512, BF16),
+    (3000, 2, 5, 520, 1000, BF16), (4099, 2, 6, 520, 1408, F32),
 ]
 
 
-@pytest.mark.parametrize("t,topk,experts,d,f,dtype,way,tile", MLP)
+def test_the_cases_take_every_way():
+    ways = [(path(3, t * topk, f, d, dtype, e), t * topk * f / 128 ** 2) for t, topk, e, d, f, dtype in MLP]
+    assert {w for w, _ in ways} == {1, 2, 3}
+    assert sum(w == 3 and tiles > 512 for w, tiles in ways) > 1       # blocks with a second tile
+    assert any(path(2, t * topk, d, f, dtype, e) == 256256 for t, topk, e, d, f, dtype in MLP)
+
+
+@pytest.mark.parametrize("t,topk,experts,d,f,dtype", MLP)
 @pytest.mark.parametrize("br", [1, 128])
-def test_expert_mlp_ways(t, topk, experts, d, f, dtype, way, tile, br):
+def test_expert_mlp_ways(t, topk, experts, d, f, dtype, br):
     print("mlp", t, topk, experts, d, f, dtype, br, flush=True)
-    assert (path(3, t * topk, f, d, dtype, experts), path(2, t * topk, d, f, dtype, experts)) == (way, tile)
     g = torch.Generator(device="cuda").manual_seed(t + d)
     gate_up = qw.block_quantize(torch.randn(experts, 2 * f, d, generator=g, device="cuda") * d ** -0.5, br)
     down = qw.block_quantize(torch.randn(experts, d, f, generator=g, device="cuda") * f ** -0.5, br)
@@ -215,7 +228,7 @@ def test_more_than_2_to_32_elements():
 def test_product_with_more_than_2_to_32_outputs():
     """131072 x 131400 outputs, 17 billion, and more tiles of 64 x 64 than a launch holds."""
     m, n, k = 131072, 131400, 300
-    assert path(0, m, n, k, BF16) == 256256
+    assert path(0, m, n, k, BF16) > 33000      # tiled
     g = torch.Generator(device="cuda").manual_seed(2)
     rec, xrec = qw.block_quantize(rand(g, n, k), 128), qw.block_quantize(rand(g, m, k), 1)
     y = qw.block_gemm(rec, xrec, out_dtype=BF16)

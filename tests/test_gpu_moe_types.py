@@ -9,7 +9,8 @@ from int8_int4_dequant_amd import qw
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("t,topk,experts,d,f", [(40, 2, 8, 256, 128), (130, 4, 6, 300, 200), (300, 2, 3, 264, 136), (333, 3, 5, 128, 384), (900, 2, 6, 700, 256)])
+@pytest.mark.parametrize("t,topk,experts,d,f", [(1, 4, 8, 512, 384), (7, 2, 4, 130, 257), (2, 2, 3, 1300, 600), (3, 1, 1, 200, 9100),
+                                                (40, 2, 8, 256, 128), (130, 4, 6, 300, 200), (300, 2, 3, 264, 136), (333, 3, 5, 128, 384), (900, 2, 6, 700, 256)])
 @pytest.mark.parametrize("br", [1, 128])
 def test_fp32_mlp_is_the_calls_one_by_one(t, topk, experts, d, f, br):
     """y in fp32: the products of the one call have fp32 sums, as the grouped
