@@ -27,7 +27,7 @@ E4M3 = torch.float8_e4m3fn
 TOP = 448.0   # the largest e4m3 value
 BLOCK = 128   # values of an e4m3 scale
 MX = 32       # values of a 4-bit scale
-PITCH = 256   # a row of 4-bit codes holds a multiple of this many values
+PITCH = 512   # a row of 4-bit codes holds a multiple of this many values
 EPS = 1e-6
 
 #: cases ------------------------------------------------------------------
@@ -177,7 +177,7 @@ def _out(c):
 
 
 def _codes(w):
-    """4-bit codes (two to a byte, the first in the low half, rows of whole 256s) and scale bytes of a matrix (n, k), one for 32 values of a row.
+    """4-bit codes (two to a byte, the first in the low half, rows of whole 512s) and scale bytes of a matrix (n, k), one for 32 values of a row.
 
     A scale is 2^(e - 127) with e the exponent of the largest magnitude less 2, so that it lies in [4, 8) scales; codes are the nearest of
     0, 0.5, 1, 1.5, 2, 3, 4, 6 (ties to the even code) and bit 3 the sign.
