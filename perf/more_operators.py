@@ -295,7 +295,7 @@ def _own(state):
         y, h = qw.rms_norm(state["x"], state["gain"], residual=state.get("res"), eps=EPS, quantize="block" if c["out"] == "block" else None)
         return h, y if c["out"] == "float" else (y["codes"], y["scales"])
     if kind == "norm_backward":
-        return qw.rms_norm_backward(state["dy"], state["x"], state["gain"], eps=EPS, dres=state.get("res"))
+        return qw.rms_norm_backward(state["dy"], state["x"], state["gain"], eps=EPS, dsum=state.get("res"))
     d, f = c["d"], c["f"]
     gate_up = _rec(state["gate_up"], 2 * f, d)
     if kind == "mlp":
