@@ -1,0 +1,358 @@
+// Products of microscaled 4-bit matrices on the gfx950 matrix cores.
+//
+//   y[r][i] = sum_b 2^(sx[r][b] + sw[i][b] - 254) sum_{j in b} qx[r][j] qw[i][j]
+//
+// v_mfma_scale_f32_32x32x64_f8f6f4 multiplies 4-bit codes and applies both scales of
+// every block of 32 itself: a lane holds 32 consecutive values of one row, which are one
+// block, and that block's scale byte.  Its sums are fp32 (measured: within 2^-23 of the
+// sum of magnitudes, accumulator included, scales up to 2^20 apart).  It reaches 8.1
+// PFLOP/s here with nothing else to do, the 16x16x128 form 4.5.
+//
+// The weight is the A operand: output lane l holds token l % 32 and, of a fragment of 32
+// weight rows, 8 g + 4 (l / 32) + 0..3, g = 0..3.
+#include "mx_codes.h"
+#include "tiles.h"
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+namespace qw {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+struct MxArgs {
+  const uint8_t *w, *ws, *x, *xs;
+  int64_t n, m;       // outputs in a row (gated: f), rows
+  int64_t kp2, ksp;   // bytes of a row of codes, of scales
+  int kb;             // steps of 128 along k
+  void* y;
+  uint8_t* ys;
+  int64_t yp;         // MX_GATED_CODES: values in a row of codes
+  const void* dh;
+  void* h;
+  int64_t tiles_m, tiles;
+  int vec;            // 4 outputs of a row at a time may be stored as one
+};
+
+// Step S of two: blocks 2 (l / 32) + S of a step of 128; the scales in byte S.
+template <int S>
+__device__ __forceinline__ f32x16 mfma64(i32x4 a, i32x4 b, f32x16 c, int sa, int sb) {
+  const i32x8 a8 = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+  const i32x8 b8 = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, S, sa, S, sb);
+}
+
+// ---------------------------------------------------------------- results
+
+template <typename T>
+__device__ __forceinline__ void put4(T* p, const float v[4], int64_t left, bool vec) {
+  if (vec) {
+    store4(p, f32x4{v[0], v[1], v[2], v[3]});
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c < left) store1(p + c, v[c]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void get4(const T* p, float v[4], int64_t left) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v[c] = c < left ? load1(p + c) : 0.0f;
+}
+
+// dgate and dup, h.  With e = exp(-|gate|) neither t nor 1 - t overflows or cancels;
+// beyond |gate| = 200 one of them is zero in fp32.
+__device__ __forceinline__ void gate_gradients(float gate, float up, float dh, float& dgate,
+                                               float& dup, float& h) {
+  const float e = expf(-fabsf(gate));
+  const float one = 1.0f / (1.0f + e), other = e * one;
+  const bool neg = gate < 0.0f;
+  const float t = neg ? other : one, u = neg ? one : other;
+  const float near = fminf(fmaxf(gate, -200.0f), 200.0f);
+  const float silu = gate * t;
+  dgate = dh * up * (t * __builtin_fmaf(near, u, 1.0f));
+  dup = dh * silu;
+  h = silu * up;
+}
+
+// A fragment's 16 outputs of a lane: rows 8 g + 4 half + c of 32, for column col0 of
+// output row `row`.
+template <typename T>
+__device__ __forceinline__ void store_fragment(const MxArgs& a, f32x16 v, int64_t row,
+                                               int64_t col0, int half) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int64_t col = col0 + 8 * g + 4 * half;
+    if (col >= a.n) continue;
+    const float o[4] = {v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+    put4((T*)a.y + row * a.n + col, o, a.n - col, a.vec);
+  }
+}
+
+template <MxResult RES, typename T>
+__device__ __forceinline__ void store_gated(const MxArgs& a, f32x16 gate, f32x16 up, int64_t row,
+                                            int64_t col0, int half, bool have) {
+  if constexpr (RES == MX_GATED_BACKWARD) {
+    if (!have) return;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int64_t col = col0 + 8 * g + 4 * half, left = a.n - col;
+      if (left <= 0) continue;
+      float dh[4], dg[4], du[4], h[4];
+      get4((const T*)a.dh + row * a.n + col, dh, left);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        gate_gradients(gate[4 * g + c], up[4 * g + c], dh[c], dg[c], du[c], h[c]);
+      put4((T*)a.y + row * 2 * a.n + col, dg, left, a.vec);
+      put4((T*)a.y + row * 2 * a.n + a.n + col, du, left, a.vec);
+      if (a.h) put4((T*)a.h + row * a.n + col, h, left, a.vec);
+    }
+  } else {
+    float v[16], p[16], q[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      p[i] = gate[i];
+      q[i] = up[i];
+    }
+    gated<16>(p, q, v);
+    if constexpr (RES == MX_GATED) {
+      if (!have) return;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int64_t col = col0 + 8 * g + 4 * half;
+        if (col < a.n) put4((T*)a.y + row * a.n + col, v + 4 * g, a.n - col, a.vec);
+      }
+    } else {
+      // The 32 values are one block: half of them in the lane 32 away.
+      uint32_t top = top_of<16>(v);
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+      const uint32_t s = mx_scale(top);
+      const uint32_t lo = mx_codes8(v, s), hi = mx_codes8(v + 8, s);  // groups 0, 1 and 2, 3
+      // lane half 0 keeps groups 0 and 1 of both halves, half 1 groups 2 and 3
+      const uint32_t other = (uint32_t)__shfl_xor((int)(half ? lo : hi), 32);
+      const uint32_t own = half ? hi : lo;
+      const uint32_t h0 = half ? other : own, h1 = half ? own : other;
+      const u32x2 out = {(h0 & 0xFFFFu) | h1 << 16, h0 >> 16 | (h1 & 0xFFFF0000u)};
+      if (have && col0 < a.yp) {
+        *(u32x2*)((uint8_t*)a.y + (row * a.yp + col0) / 2 + 8 * half) = out;
+        if (half == 0) a.ys[(row * a.yp + col0) / 32] = (uint8_t)s;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- tiled kernel
+//
+// A block of WN x WM waves, each with 32 NF weight rows x 32 MF tokens, 128 values of k
+// at a time through a ring of STAGES LDS buffers that copies straight from memory fill.
+// Scales are copied for four steps at once (16 bytes a row).
+//
+// LDS rows are the 64 bytes of a step.  A phase of a 16-byte LDS read is 16 lanes, here
+// 16 consecutive rows at the same place in the row, and the 64 banks hold 4 rows: piece c
+// of row r is kept at c ^ (r / 4 % 4), so that the 16 lanes meet 16 different places.  The
+// copy writes LDS in lane order, so the lanes fetch the pieces in that order from memory.
+//
+// Gated results: the tile's rows are 32 gate rows and their 32 up rows in turn, so that a
+// lane holds both values of a result.
+
+template <int NF, int MF, int WN, int WM, int STAGES, MxResult RES, typename T>
+__global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(MxArgs a) {
+  constexpr int WAVES = WN * WM, BN = 32 * NF * WN, BM = 32 * MF * WM, ROWS = BN + BM;
+  constexpr bool GATED = RES != MX_STORE;
+  constexpr int COLS = GATED ? BN / 2 : BN;        // outputs of a row in a tile
+  constexpr int SEGS = ROWS / 16 / WAVES;          // 16-row pieces of a wave
+  constexpr int SCALES = ROWS / 64;                // 64-row pieces of scales
+  constexpr int SPER = (SCALES + WAVES - 1) / WAVES;
+  static_assert(ROWS / 16 % WAVES == 0 && BN % 64 == 0 && BM % 64 == 0, "whole pieces");
+  static_assert(!GATED || NF % 2 == 0, "gate and up rows in one wave");
+  static_assert(STAGES >= 3 && STAGES <= 6, "see the waits below");
+  __shared__ __align__(1024) uint8_t lds[STAGES][ROWS * 64];
+  __shared__ __align__(1024) uint8_t scales[2][ROWS * 16];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
+  const int wm = wave % WM * 32 * MF, wn = wave / WM * 32 * NF;
+  int64_t tm, tn;
+  tile_place(blockIdx.x, a.tiles, a.tiles_m, tm, tn);
+  const int64_t n0 = tn * COLS, m0 = tm * BM, end = min(m0 + BM, a.m);
+  // nothing is there behind the last output: only padding of a row of codes
+  const int64_t cols = max((int64_t)0, min(a.n - n0, (int64_t)COLS));
+  const i32x4 wbuf = buffer_of(a.w + n0 * a.kp2, (uint32_t)(cols * a.kp2));
+  const i32x4 ubuf = buffer_of(a.w + (GATED ? (a.n + n0) * a.kp2 : 0), (uint32_t)(cols * a.kp2));
+  const i32x4 xbuf = buffer_of(a.x + m0 * a.kp2, (uint32_t)((end - m0) * a.kp2));
+  const i32x4 wsbuf = buffer_of(a.ws + n0 * a.ksp, (uint32_t)(cols ? ((GATED ? a.n : 0) + cols) * a.ksp : 0));
+  const i32x4 xsbuf = buffer_of(a.xs + m0 * a.ksp, (uint32_t)((end - m0) * a.ksp));
+  const int kb = cols ? a.kb : 0;
+  uint32_t voff[SEGS];
+#pragma unroll
+  for (int s = 0; s < SEGS; ++s) {
+    const int row = (wave + WAVES * s) * 16 + (lane >> 2);
+    const int c = (lane & 3) ^ ((row >> 2) & 3);
+    const int at = row >= BN ? row - BN : GATED ? row / 64 * 32 + row % 32 : row;
+    voff[s] = (uint32_t)at * (uint32_t)a.kp2 + c * 16;
+  }
+  uint32_t soff[SPER];
+#pragma unroll
+  for (int s = 0; s < SPER; ++s) {
+    const int row = (wave + WAVES * s) * 64 + lane;
+    const int64_t at = row >= BN ? row - BN : GATED ? row / 64 * 32 + row % 32 + (row / 32 % 2 ? a.n : 0) : row;
+    soff[s] = (uint32_t)(at * a.ksp);
+  }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0];
+  const uint32_t lds1 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&scales[0][0];
+  // Behind the last step there is nothing to read, but the copy is issued all the same
+  // (as zeros, from an empty buffer), so that every step has as many.
+  auto fetch = [&](int b, int buf) {
+    const bool in = b < kb;
+#pragma unroll
+    for (int s = 0; s < SEGS; ++s) {
+      const int seg = wave + WAVES * s;
+      i32x4 from = seg >= BN / 16 ? xbuf : GATED && seg / 2 % 2 ? ubuf : wbuf;
+      from.z = in ? from.z : 0;
+      copy_to_lds(from, voff[s], in ? (uint32_t)b * 64 : 0, lds0 + buf * (ROWS * 64) + seg * 1024);
+    }
+  };
+  auto fetch_scales = [&](int u) {  // of steps 4 u .. 4 u + 3
+    const bool in = 4 * u < kb;
+#pragma unroll
+    for (int s = 0; s < SPER; ++s) {
+      const int seg = wave + WAVES * s;
+      if (seg >= SCALES) break;
+      i32x4 from = seg >= BN / 64 ? xsbuf : wsbuf;
+      from.z = in ? from.z : 0;
+      copy_to_lds(from, soff[s], in ? (uint32_t)u * 16 : 0, lds1 + (u & 1) * (ROWS * 16) + seg * 1024);
+    }
+  };
+  fetch_scales(0);
+  fetch_scales(1);
+#pragma unroll
+  for (int b = 0; b < STAGES; ++b) fetch(b, b);
+
+  f32x16 acc[NF][MF] = {};
+  i32x4 w0[NF], x0[MF], w1[NF], x1[MF];
+  int sw[NF], sx[MF], sw2[NF], sx2[MF];
+  const int swap = (r >> 2) & 3;  // the same for all rows a multiple of 32 apart
+  auto take = [&](int buf, int s, i32x4* w, i32x4* x) {
+    const uint8_t* p = &lds[buf][r * 64 + (((2 * half + s) ^ swap) << 4)];
+#pragma unroll
+    for (int i = 0; i < NF; ++i) w[i] = *(const i32x4*)(p + (wn + 32 * i) * 64);
+#pragma unroll
+    for (int j = 0; j < MF; ++j) x[j] = *(const i32x4*)(p + (BN + wm + 32 * j) * 64);
+  };
+  auto take_scales = [&](int b, int* w, int* x) {
+    const uint8_t* p = &scales[(b >> 2) & 1][r * 16 + (b & 3) * 4];
+#pragma unroll
+    for (int i = 0; i < NF; ++i) w[i] = *(const int*)(p + (wn + 32 * i) * 16);
+#pragma unroll
+    for (int j = 0; j < MF; ++j) x[j] = *(const int*)(p + (BN + wm + 32 * j) * 16);
+  };
+  // Copies that may be on their way when step b + 1 has to be there: those of the
+  // STAGES - 2 steps behind it.  Scales on their way only make the wait longer: they are
+  // issued four steps before they are read, so at least that many copies are newer.
+  constexpr int LEFT = (STAGES - 2) * SEGS;
+  landed<LEFT + SEGS>();
+  take(0, 0, w0, x0);
+  take_scales(0, sw, sx);
+  int buf = 0;
+  for (int b = 0; b < kb; ++b) {
+    const int next = buf + 1 < STAGES ? buf + 1 : 0;
+    take(buf, 1, w1, x1);
+#pragma unroll
+    for (int i = 0; i < NF; ++i) sw[i] >>= 16 * half;
+#pragma unroll
+    for (int j = 0; j < MF; ++j) sx[j] >>= 16 * half;
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < MF; ++j) acc[i][j] = mfma64<0>(w0[i], x0[j], acc[i][j], sw[i], sx[j]);
+    // This wave holds all that it needs of this buffer and of these scales; once every
+    // wave does, they are filled again.
+    landed<LEFT>();
+    take(next, 0, w0, x0);
+    take_scales(b + 1, sw2, sx2);
+    if ((b & 3) == 3) fetch_scales((b >> 2) + 2);
+    fetch(b + STAGES, buf);
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < MF; ++j) acc[i][j] = mfma64<1>(w1[i], x1[j], acc[i][j], sw[i], sx[j]);
+#pragma unroll
+    for (int i = 0; i < NF; ++i) sw[i] = sw2[i];
+#pragma unroll
+    for (int j = 0; j < MF; ++j) sx[j] = sx2[j];
+    buf = next;
+  }
+  landed<0>();  // the empty copies too, before the block's LDS is another's
+
+#pragma unroll
+  for (int j = 0; j < MF; ++j) {
+    const int64_t row = m0 + wm + 32 * j + r;
+    const bool have = row < end;
+    if constexpr (GATED) {
+#pragma unroll
+      for (int i = 0; i < NF; i += 2)
+        store_gated<RES, T>(a, acc[i][j], acc[i + 1][j], row, n0 + (wn + 32 * i) / 2, half, have);
+    } else {
+      if (!have) continue;
+#pragma unroll
+      for (int i = 0; i < NF; ++i) store_fragment<T>(a, acc[i][j], row, n0 + wn + 32 * i, half);
+    }
+  }
+}
+
+template <int NF, int MF, int WN, int WM, int STAGES>
+hipError_t run_tiled(MxArgs a, const MxGemm& g, hipStream_t stream) {
+  constexpr int BN = 32 * NF * WN, BM = 32 * MF * WM;
+  const int cols = g.result == MX_STORE ? BN : BN / 2;
+  a.tiles_m = (a.m + BM - 1) / BM;
+  a.tiles = a.tiles_m * (((g.result == MX_GATED_CODES ? a.yp : a.n) + cols - 1) / cols);
+  auto go = [&](auto result, auto type) {
+    mx_tiled<NF, MF, WN, WM, STAGES, decltype(result)::value, decltype(type)>
+        <<<(unsigned)a.tiles, WN * WM * 64, 0, stream>>>(a);
+  };
+  auto typed = [&](auto result) { g.y_type == QW_F32 ? go(result, 0.0f) : go(result, uint16_t{}); };
+  switch (g.result) {
+    case MX_STORE: typed(std::integral_constant<MxResult, MX_STORE>{}); break;
+    case MX_GATED: typed(std::integral_constant<MxResult, MX_GATED>{}); break;
+    case MX_GATED_CODES: go(std::integral_constant<MxResult, MX_GATED_CODES>{}, 0.0f); break;
+    default: typed(std::integral_constant<MxResult, MX_GATED_BACKWARD>{});
+  }
+  return hipGetLastError();
+}
+
+MxArgs args_of(const MxGemm& g) {
+  MxArgs a = {};
+  const int64_t kp = mx_pitch(g.k);
+  a.w = g.codes;
+  a.ws = g.scales;
+  a.x = g.xc;
+  a.xs = g.xs;
+  a.n = g.n;
+  a.m = g.m;
+  a.kp2 = kp / 2;
+  a.ksp = kp / 32;
+  a.kb = (int)((g.k + 127) / 128);
+  a.y = g.y;
+  a.ys = g.ys;
+  a.yp = mx_pitch(g.n);
+  a.dh = g.dh;
+  a.h = g.h;
+  const uintptr_t unit = g.y_type == QW_BF16 ? 8 : 16;
+  a.vec = g.n % 4 == 0 && aligned(g.y, unit) && aligned(g.h, unit);
+  return a;
+}
+
+}  // namespace
+
+hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t stream) {
+  const MxArgs a = args_of(g);
+  const int64_t rows = g.result == MX_STORE ? g.n : 2 * g.n;
+  auto tiles = [&](int t) { return ((g.m + t - 1) / t) * ((rows + t - 1) / t); };
+  if (tiles(256) >= 256 || tiles(64) > 1 << 22) return run_tiled<4, 2, 2, 4, 4>(a, g, stream);
+  if (tiles(128) >= 256) return run_tiled<2, 2, 2, 2, 4>(a, g, stream);
+  return run_tiled<2, 1, 1, 2, 4>(a, g, stream);
+}
+
+}  // namespace qw

@@ -1,0 +1,356 @@
+// RMS norm with the residual's addition, its output in float, as e4m3 codes or as
+// 4-bit codes, and its gradients, for gfx950.
+//
+//   s = x + residual,  r = 1 / sqrt(mean(s^2) + eps),  y = s r weight
+//   ds = r (u - s r^2 mean(u s)) + dsum with u = dy weight,  dweight = sum of dy s r
+//
+// Bound by HBM: every input is read once and every output written once.  The lanes of
+// a row hold it in registers between its sum and its results, 8 values of every
+// 8 LANES a lane; the block of a scale is then 16 (e4m3) or 4 (4 bits) lanes side by
+// side.
+#include "mx_codes.h"
+
+namespace qw {
+namespace {
+
+enum Form { FLOAT, BLOCK, MX };
+
+struct NormArgs {
+  int64_t rows, d;
+  const void *x, *res, *weight;
+  void *sum, *y, *scales;
+  float eps;
+  int w_type, y_type;
+  int64_t pitch;  // values in a row of codes, or of y
+};
+
+// 8 weights from j on of d; 1 without weights.
+__device__ __forceinline__ void load_weights(const void* w, int type, int64_t j, int64_t d,
+                                             float v[8]) {
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 1.0f;
+  } else if (type == QW_F32) {
+    load8_of_row<false>((const float*)w, j, d, v);
+  } else {
+    load8_of_row<false>((const uint16_t*)w, j, d, v);
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int h = 1; h < 64; h <<= 1) v += __shfl_xor(v, h);
+  return v;
+}
+
+// Sums over the LANES lanes of a row; `part`: a float for each wave of the block,
+// another at every call between two barriers.
+template <int LANES, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*part)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if (LANES == 64) return;
+  __syncthreads();  // the last sums have been read
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) part[threadIdx.x >> 6][i] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = part[0][i];
+#pragma unroll
+    for (int w = 1; w < LANES / 64; ++w) v[i] += part[w][i];
+  }
+}
+
+// As the type holds it.
+__device__ __forceinline__ float rounded(float v, float) { return v; }
+__device__ __forceinline__ float rounded(float v, uint16_t) {
+  return __uint_as_float((uint32_t)to_bf16(v) << 16);
+}
+
+// 8 results of a row from j on.
+template <Form FORM>
+__device__ __forceinline__ void store_results(const NormArgs& a, int64_t row, int64_t j,
+                                              const float v[8]) {
+  if (FORM == FLOAT) {
+    if (a.y_type == QW_F32)
+      store8_of_row<false>((float*)a.y + row * a.d, j, a.d, v);
+    else
+      store8_of_row<false>((uint16_t*)a.y + row * a.d, j, a.d, v);
+  } else if (FORM == BLOCK) {
+    const float s = block_scale(max16(amax8(v)));
+    const u32x2 c = codes8(v, s);
+    if (j < a.pitch) {
+      *(u32x2*)((uint8_t*)a.y + row * a.pitch + j) = c;
+      if (j % QW_BLOCK == 0) ((float*)a.scales)[(row * a.pitch + j) / QW_BLOCK] = s;
+    }
+  } else {
+    const uint32_t s = mx_scale(top_among<4>(top_of<8>(v)));
+    const uint32_t c = mx_codes8(v, s);
+    if (j < a.pitch) {
+      *(uint32_t*)((uint8_t*)a.y + (row * a.pitch + j) / 2) = c;
+      if (j % QW_MX_BLOCK == 0) ((uint8_t*)a.scales)[(row * a.pitch + j) / QW_MX_BLOCK] = (uint8_t)s;
+    }
+  }
+}
+
+// LANES lanes a row, CH times 8 values each; CH 0: as many as there are, in two passes
+// over the row.
+template <int LANES, int CH, Form FORM, typename T>
+__global__ __launch_bounds__(256) void norm(NormArgs a) {
+  constexpr int N = CH ? CH : 1, ROWS = 256 / LANES;
+  __shared__ float part[4][1];
+  const int lane = threadIdx.x % LANES;
+  // all waves of a block take as many rows: the block's barriers see all of them
+  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.rows; r0 += (int64_t)gridDim.x * ROWS) {
+    const int64_t row = r0 + threadIdx.x / LANES;
+    if (LANES == 64 && row >= a.rows) return;
+    const T* x = (const T*)a.x + row * a.d;
+    const T* res = a.res ? (const T*)a.res + row * a.d : nullptr;
+    T* sum = a.sum ? (T*)a.sum + row * a.d : nullptr;
+    float v[N][8], sq[1] = {0.0f};
+    auto load = [&](int64_t j, float* s) {
+      load8_of_row<false>(x, j, a.d, s);
+      if (res) {
+        float t[8];
+        load8_of_row<false>(res, j, a.d, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = rounded(s[i] + t[i], T{});
+      }
+    };
+    auto first = [&](int64_t j, float* s) {
+      load(j, s);
+      if (sum) store8_of_row<false>(sum, j, a.d, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sq[0] = __builtin_fmaf(s[i], s[i], sq[0]);
+    };
+    if (CH) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) first((int64_t)(c * LANES + lane) * 8, v[c]);
+    } else {
+      for (int64_t j = lane * 8; j < a.d; j += LANES * 8) first(j, v[0]);
+    }
+    row_sum<LANES>(sq, part);
+    const float r = 1.0f / __builtin_sqrtf(sq[0] / (float)a.d + a.eps);
+    auto second = [&](int64_t j, float* s) {
+      float w[8];
+      load_weights(a.weight, a.w_type, j, a.d, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = s[i] * r * w[i];
+      // behind the row: zeros, also of a row whose r is infinite
+      if (FORM != FLOAT && j + 8 > a.d)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = j + i < a.d ? s[i] : 0.0f;
+      store_results<FORM>(a, row, j, s);
+    };
+    if (CH) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) second((int64_t)(c * LANES + lane) * 8, v[c]);
+    } else {
+      // whole rounds of lanes: a block's lanes exchange its maximum
+      for (int64_t j = lane * 8; j - lane * 8 < a.pitch; j += LANES * 8) {
+        // this lane wrote what it reads here, where sum is x or the residual
+        if (sum && j < a.d)
+          load8_of_row<false>((const T*)sum, j, a.d, v[0]);
+        else
+          load(j, v[0]);
+        second(j, v[0]);
+      }
+    }
+  }
+}
+
+struct NormBackArgs {
+  int64_t rows, d;
+  const void *dy, *s, *weight, *dsum;
+  void* ds;
+  float* part;  // [grid][d]: each block's share of dweight
+  float eps;
+  int w_type;
+};
+
+// The rows of a block in turn; its share of dweight stays in registers (CH 0: in
+// memory, each lane adding to its own).
+template <int LANES, int CH, typename T>
+__global__ __launch_bounds__(256) void norm_backward(NormBackArgs a) {
+  constexpr int N = CH ? CH : 1, ROWS = 256 / LANES;
+  __shared__ float part[4][2];
+  __shared__ float join[LANES == 64 && CH ? N * 512 : 1];
+  const int lane = threadIdx.x % LANES;
+  float dw[N][8] = {};
+  float* const mine = a.part ? a.part + (int64_t)blockIdx.x * a.d : nullptr;
+  bool fresh = true;
+  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.rows; r0 += (int64_t)gridDim.x * ROWS) {
+    const int64_t row = r0 + threadIdx.x / LANES;
+    if (LANES == 64 && row >= a.rows) break;
+    const T* dy = (const T*)a.dy + row * a.d;
+    const T* s = (const T*)a.s + row * a.d;
+    float u[N][8], v[N][8], sums[2] = {0.0f, 0.0f};
+    auto first = [&](int64_t j, float* g, float* h) {
+      float w[8];
+      load8_of_row<false>(dy, j, a.d, g);
+      load8_of_row<false>(s, j, a.d, h);
+      load_weights(a.weight, a.w_type, j, a.d, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sums[0] = __builtin_fmaf(h[i], h[i], sums[0]);
+        sums[1] = __builtin_fmaf(g[i] * w[i], h[i], sums[1]);
+      }
+    };
+    if (CH) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) first((int64_t)(c * LANES + lane) * 8, u[c], v[c]);
+    } else {
+      for (int64_t j = lane * 8; j < a.d; j += LANES * 8) first(j, u[0], v[0]);
+    }
+    row_sum<LANES>(sums, part);
+    const float r = 1.0f / __builtin_sqrtf(sums[0] / (float)a.d + a.eps);
+    const float f = sums[1] / (float)a.d * r * r;
+    auto second = [&](int64_t j, const float* g, const float* h, float* share) {
+      if (a.ds) {
+        float w[8], t[8];
+        load_weights(a.weight, a.w_type, j, a.d, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = 0.0f;
+        if (a.dsum) load8_of_row<false>((const T*)a.dsum + row * a.d, j, a.d, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          t[i] = __builtin_fmaf(r, __builtin_fmaf(-h[i], f, g[i] * w[i]), t[i]);
+        store8_of_row<false>((T*)a.ds + row * a.d, j, a.d, t);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) share[i] = __builtin_fmaf(g[i], h[i] * r, share[i]);
+    };
+    if (CH) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) second((int64_t)(c * LANES + lane) * 8, u[c], v[c], dw[c]);
+    } else {
+      for (int64_t j = lane * 8; j < a.d; j += LANES * 8) {
+        load8_of_row<false>(dy, j, a.d, u[0]);
+        load8_of_row<false>(s, j, a.d, v[0]);
+        float share[8] = {};
+        if (mine && !fresh) load8_of_row<false>(mine, j, a.d, share);
+        second(j, u[0], v[0], share);
+        if (mine) store8_of_row<false>(mine, j, a.d, share);
+      }
+      fresh = false;
+    }
+  }
+  if (!CH || !mine) return;
+  if (LANES == 64) {
+    // the four waves' shares, one after the other
+    for (int w = 0; w < 4; ++w) {
+      __syncthreads();
+      if ((int)(threadIdx.x >> 6) != w) continue;
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float* to = &join[(c * 8 + i) * 64 + lane];
+          *to = w == 0 ? dw[c][i] : *to + dw[c][i];
+          dw[c][i] = *to;
+        }
+    }
+    if (threadIdx.x < 192) return;  // the last wave has the sum
+  }
+#pragma unroll
+  for (int c = 0; c < N; ++c) store8_of_row<false>(mine, (int64_t)(c * LANES + lane) * 8, a.d, dw[c]);
+}
+
+// dweight from the blocks' shares: a thread block takes 64 columns, a wave every fourth
+// share, in a fixed order.
+__global__ __launch_bounds__(256) void sum_shares(const float* __restrict__ part,
+                                                  float* __restrict__ dw, int64_t d, int count) {
+  __shared__ float waves[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < d; c0 += (int64_t)gridDim.x * 64) {
+    const int64_t c = c0 + lane;
+    float s = 0.0f;
+    if (c < d)
+      for (int i = wave; i < count; i += 4) s += part[(int64_t)i * d + c];
+    __syncthreads();
+    waves[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < d) dw[c] = (waves[0][lane] + waves[1][lane]) + (waves[2][lane] + waves[3][lane]);
+  }
+}
+
+template <Form FORM, typename T>
+hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
+  const int64_t lanes = (a.pitch + 7) / 8;  // chunks of 8 in a row
+  auto go = [&](auto lanes_of_row, auto chunks) {
+    constexpr int LANES = decltype(lanes_of_row)::value, CH = decltype(chunks)::value;
+    norm<LANES, CH, FORM, T><<<grid_for(a.rows, 256 / LANES), 256, 0, stream>>>(a);
+  };
+  using std::integral_constant;
+  if (lanes <= 64)
+    go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (lanes <= 128)
+    go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else if (lanes <= 256)
+    go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  else if (lanes <= 512)
+    go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  else if (lanes <= 1024)
+    go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  else if (lanes <= 2048)
+    go(integral_constant<int, 256>{}, integral_constant<int, 8>{});
+  else
+    go(integral_constant<int, 256>{}, integral_constant<int, 0>{});
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run_backward(const NormBackArgs& a, int grid, hipStream_t stream) {
+  const int64_t lanes = (a.d + 7) / 8;
+  auto go = [&](auto lanes_of_row, auto chunks) {
+    norm_backward<decltype(lanes_of_row)::value, decltype(chunks)::value, T>
+        <<<grid, 256, 0, stream>>>(a);
+  };
+  using std::integral_constant;
+  if (lanes <= 64)
+    go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (lanes <= 128)
+    go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else if (lanes <= 256)
+    go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  else if (lanes <= 512)
+    go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  else if (lanes <= 1024)
+    go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  else
+    go(integral_constant<int, 256>{}, integral_constant<int, 0>{});
+  return hipGetLastError();
+}
+
+// Most blocks of the backward kernel: as many shares of dweight are added up.
+constexpr int64_t kShares = 1024;
+
+}  // namespace
+
+hipError_t launch_rms_norm(const RmsNorm& g, hipStream_t stream) {
+  NormArgs a = {g.rows, g.d, g.x, g.res, g.weight, g.sum, g.y, g.scales, g.eps, g.w_type, g.y_type, 0};
+  a.pitch = g.form == 0 ? g.d : g.form == 1 ? pitch(g.d) : mx_pitch(g.d);
+  const bool f32 = g.type == QW_F32;
+  switch (g.form) {
+    case 0: return f32 ? run_norm<FLOAT, float>(a, stream) : run_norm<FLOAT, uint16_t>(a, stream);
+    case 1: return f32 ? run_norm<BLOCK, float>(a, stream) : run_norm<BLOCK, uint16_t>(a, stream);
+    default: return f32 ? run_norm<MX, float>(a, stream) : run_norm<MX, uint16_t>(a, stream);
+  }
+}
+
+int64_t rms_norm_shares(int64_t rows) { return rows < kShares ? rows : kShares; }
+
+hipError_t launch_rms_norm_backward(const RmsNormBackward& g, hipStream_t stream) {
+  const int grid = (int)rms_norm_shares(g.rows);
+  NormBackArgs a = {g.rows, g.d, g.dy, g.s, g.weight, g.dsum, g.ds,
+                    g.dweight ? (float*)g.work : nullptr, g.eps, g.w_type};
+  hipError_t e = g.type == QW_F32 ? run_backward<float>(a, grid, stream)
+                                  : run_backward<uint16_t>(a, grid, stream);
+  if (e != hipSuccess || !g.dweight) return e;
+  sum_shares<<<grid_for(g.d, 64), 256, 0, stream>>>(a.part, g.dweight, g.d, grid);
+  return hipGetLastError();
+}
+
+}  // namespace qw

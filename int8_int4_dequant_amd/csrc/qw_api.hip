@@ -2,6 +2,7 @@
 // dispatch to the HIP kernels.  No allocation, no synchronization.
 #include <string.h>
 
+#include <cmath>
 #include <mutex>
 #include <vector>
 
@@ -813,6 +814,268 @@ int qw_block_debug_path(int op, int64_t experts, int64_t m, int64_t n, int64_t k
   }
   if (op < 2) return qw::block_gemm_path(n, m, k, y_type == QW_F32, op == 1);
   return qw::block_gemm_grouped_path(n, m, k, experts, y_type == QW_F32);
+}
+
+}  // extern "C"
+
+// ------------------------------------------- microscaled 4-bit codes, RMS norm
+
+namespace {
+
+// An n x k matrix and its rows of 4-bit codes.
+bool mx_fits(int64_t n, int64_t k) {
+  return within(n, k) && within(k, 1) && within(n, qw::mx_pitch(k));
+}
+
+// x or y side of a product: m rows of n outputs and of k inputs.
+int check_mx_rows(int64_t m, int64_t n, int64_t k) {
+  if (k > QW_BLOCK_MAX_K) return QW_ESHAPE;
+  return within(m, n) && mx_fits(m, k) ? QW_OK : QW_EM;
+}
+
+// The weight of a gated product, 2 f x k, and its m rows of x and of results.
+int check_gated(int64_t f, int64_t k, int64_t m) {
+  if (!within(f, 2) || !mx_fits(2 * f, k)) return QW_ESHAPE;
+  const int st = check_mx_rows(m, 2 * f, k);
+  if (st != QW_OK) return st;
+  return mx_fits(m, f) ? QW_OK : QW_EM;
+}
+
+bool codes_ok(const void* codes, const void* scales) {
+  return qw::aligned(codes, 16) && qw::aligned(scales, 16);
+}
+
+int check_norm(int64_t rows, int64_t d, int type, int w_type, const void* weight, float eps) {
+  if (!within(rows, d)) return QW_ESHAPE;
+  if (!type_ok(type) || (weight && !type_ok(w_type))) return QW_EARG;
+  return std::isfinite(eps) && eps >= 0.0f ? QW_OK : QW_EARG;
+}
+
+// The buffers of qw_mx_mlp: the codes of x and of h, or h as floats.
+struct MxMlpWork {
+  int64_t xc, xs, hc, hs, bytes;
+  MxMlpWork(int64_t m, int64_t d, int64_t f) {
+    Carve c;
+    xc = c.take(m * (qw::mx_pitch(d) / 2));
+    xs = c.take(m * (qw::mx_pitch(d) / 32));
+    hc = c.take(m * (qw::mx_pitch(f) / 2));
+    hs = c.take(m * (qw::mx_pitch(f) / 32));
+    bytes = c.at;
+  }
+};
+
+int check_mx_mlp(int64_t m, int64_t d, int64_t f) {
+  if (!within(f, 2) || !within(d, 1) || d > QW_BLOCK_MAX_K || f > QW_BLOCK_MAX_K) return QW_ESHAPE;
+  if (!mx_fits(m, d) || !within(m, 2 * qw::mx_pitch(f))) return QW_EM;
+  return QW_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t qw_mx_pitch(int64_t k) { return within(k, 1) && within(qw::mx_pitch(k), 1) ? qw::mx_pitch(k) : -1; }
+
+int qw_mx_quantize(int transpose, int64_t n, int64_t k, int type, const void* w, uint8_t* codes,
+                   uint8_t* scales, void* stream) {
+  if (transpose != 0 && transpose != 1) return QW_EARG;
+  if (!within(n, k) || !(transpose ? mx_fits(k, n) : mx_fits(n, k))) return QW_ESHAPE;
+  if (!type_ok(type)) return QW_EARG;
+  if (n * k == 0) return QW_OK;
+  if (!w || !codes || !scales) return QW_ENULL;
+  if (!codes_ok(codes, scales)) return QW_EARG;
+  return record(qw::launch_mx_quantize(transpose, n, k, type, w, codes, scales,
+                                       (hipStream_t)stream));
+}
+
+int qw_mx_unpack(int64_t n, int64_t k, const uint8_t* codes, const uint8_t* scales, float* out,
+                 void* stream) {
+  if (!mx_fits(n, k)) return QW_ESHAPE;
+  if (n * k == 0) return QW_OK;
+  if (!codes || !scales || !out) return QW_ENULL;
+  if (!codes_ok(codes, scales)) return QW_EARG;
+  return record(qw::launch_mx_unpack(n, k, codes, scales, out, (hipStream_t)stream));
+}
+
+int qw_mx_gemm(int64_t n, int64_t k, const uint8_t* codes, const uint8_t* scales, int64_t m,
+               const uint8_t* x_codes, const uint8_t* x_scales, int y_type, void* y,
+               void* stream) {
+  if (!mx_fits(n, k)) return QW_ESHAPE;
+  const int st = check_mx_rows(m, n, k);
+  if (st != QW_OK) return st;
+  if (!type_ok(y_type)) return QW_EARG;
+  if (m * n == 0) return QW_OK;
+  if (!y || (k > 0 && (!codes || !scales || !x_codes || !x_scales))) return QW_ENULL;
+  if (!codes_ok(codes, scales) || !codes_ok(x_codes, x_scales)) return QW_EARG;
+  const qw::MxGemm g = {qw::MX_STORE, n, k, m, codes, scales, x_codes, x_scales, y_type, y,
+                        nullptr, nullptr, nullptr};
+  return record(qw::launch_mx_gemm(g, (hipStream_t)stream));
+}
+
+int64_t qw_mx_matmul_work_bytes(int64_t m, int64_t k) {
+  if (check_mx_rows(m, 1, k) != QW_OK) return -1;
+  Carve c;
+  c.take(m * (qw::mx_pitch(k) / 2));
+  c.take(m * (qw::mx_pitch(k) / 32));
+  return c.at;
+}
+
+int qw_mx_matmul(int64_t n, int64_t k, const uint8_t* codes, const uint8_t* scales, int64_t m,
+                 int x_type, const void* x, int y_type, void* y, void* work,
+                 int64_t work_bytes, void* stream) {
+  if (!mx_fits(n, k)) return QW_ESHAPE;
+  int st = check_mx_rows(m, n, k);
+  if (st != QW_OK) return st;
+  if (!type_ok(x_type) || !type_ok(y_type)) return QW_EARG;
+  if (m * n == 0) return QW_OK;
+  if (!y || (k > 0 && (!codes || !scales || !x))) return QW_ENULL;
+  if (!codes_ok(codes, scales)) return QW_EARG;
+  const int64_t need = qw_mx_matmul_work_bytes(m, k);
+  if (need > 0 && (!work || work_bytes < need || !qw::aligned(work, 16))) return QW_EWORK;
+  Carve c;
+  uint8_t* const xc = (uint8_t*)work + c.take(m * (qw::mx_pitch(k) / 2));
+  uint8_t* const xs = (uint8_t*)work + c.take(0);
+  if (k > 0) {
+    st = record(qw::launch_mx_quantize(0, m, k, x_type, x, xc, xs, (hipStream_t)stream));
+    if (st != QW_OK) return st;
+  }
+  const qw::MxGemm g = {qw::MX_STORE, n, k, m, codes, scales, xc, xs, y_type, y,
+                        nullptr, nullptr, nullptr};
+  return record(qw::launch_mx_gemm(g, (hipStream_t)stream));
+}
+
+int qw_rms_norm(int64_t rows, int64_t d, int type, const void* x, const void* residual,
+                void* sum, int weight_type, const void* weight, float eps, int y_type, void* y,
+                void* stream) {
+  const int st = check_norm(rows, d, type, weight_type, weight, eps);
+  if (st != QW_OK) return st;
+  if (!type_ok(y_type)) return QW_EARG;
+  if (rows * d == 0) return QW_OK;
+  if (!x || !y) return QW_ENULL;
+  return record(qw::launch_rms_norm({0, rows, d, type, x, residual, sum, weight_type, weight, eps,
+                                     y_type, y, nullptr}, (hipStream_t)stream));
+}
+
+int qw_rms_norm_block(int64_t rows, int64_t d, int type, const void* x, const void* residual,
+                      void* sum, int weight_type, const void* weight, float eps,
+                      uint8_t* codes, float* scales, void* stream) {
+  const int st = check_norm(rows, d, type, weight_type, weight, eps);
+  if (st != QW_OK) return st;
+  if (check_block(1, 1, rows, d) != QW_OK) return QW_ESHAPE;
+  if (rows * d == 0) return QW_OK;
+  if (!x || !codes || !scales) return QW_ENULL;
+  if (!qw::aligned(codes, 16)) return QW_EARG;
+  return record(qw::launch_rms_norm({1, rows, d, type, x, residual, sum, weight_type, weight, eps,
+                                     QW_F32, codes, scales}, (hipStream_t)stream));
+}
+
+int qw_rms_norm_mx(int64_t rows, int64_t d, int type, const void* x, const void* residual,
+                   void* sum, int weight_type, const void* weight, float eps, uint8_t* codes,
+                   uint8_t* scales, void* stream) {
+  const int st = check_norm(rows, d, type, weight_type, weight, eps);
+  if (st != QW_OK) return st;
+  if (!mx_fits(rows, d)) return QW_ESHAPE;
+  if (rows * d == 0) return QW_OK;
+  if (!x || !codes || !scales) return QW_ENULL;
+  if (!codes_ok(codes, scales)) return QW_EARG;
+  return record(qw::launch_rms_norm({2, rows, d, type, x, residual, sum, weight_type, weight, eps,
+                                     QW_F32, codes, scales}, (hipStream_t)stream));
+}
+
+int64_t qw_rms_norm_backward_work_bytes(int64_t rows, int64_t d) {
+  return within(rows, d) ? qw::rms_norm_shares(rows) * d * 4 : -1;
+}
+
+int qw_rms_norm_backward(int64_t rows, int64_t d, int type, const void* dy, const void* s,
+                         int weight_type, const void* weight, float eps, const void* dsum,
+                         void* ds, float* dweight, void* work, int64_t work_bytes,
+                         void* stream) {
+  const int st = check_norm(rows, d, type, weight_type, weight, eps);
+  if (st != QW_OK) return st;
+  if (d == 0 || (!ds && !dweight)) return QW_OK;
+  if (rows == 0)
+    return dweight ? record(qw::launch_fill_zero(dweight, d, (hipStream_t)stream)) : QW_OK;
+  if (!dy || !s) return QW_ENULL;
+  const int64_t need = qw_rms_norm_backward_work_bytes(rows, d);
+  if (dweight && (!work || work_bytes < need || !qw::aligned(work, 16))) return QW_EWORK;
+  return record(qw::launch_rms_norm_backward({rows, d, type, dy, s, weight_type, weight, eps, dsum,
+                                              ds, dweight, work}, (hipStream_t)stream));
+}
+
+int qw_mx_gated(int64_t f, int64_t k, const uint8_t* codes, const uint8_t* scales, int64_t m,
+                const uint8_t* x_codes, const uint8_t* x_scales, int h_type, void* h,
+                void* stream) {
+  const int st = check_gated(f, k, m);
+  if (st != QW_OK) return st;
+  if (!type_ok(h_type)) return QW_EARG;
+  if (m * f == 0) return QW_OK;
+  if (!h || (k > 0 && (!codes || !scales || !x_codes || !x_scales))) return QW_ENULL;
+  if (!codes_ok(codes, scales) || !codes_ok(x_codes, x_scales)) return QW_EARG;
+  const qw::MxGemm g = {qw::MX_GATED, f, k, m, codes, scales, x_codes, x_scales, h_type, h,
+                        nullptr, nullptr, nullptr};
+  return record(qw::launch_mx_gemm(g, (hipStream_t)stream));
+}
+
+int qw_mx_gated_codes(int64_t f, int64_t k, const uint8_t* codes, const uint8_t* scales,
+                      int64_t m, const uint8_t* x_codes, const uint8_t* x_scales,
+                      uint8_t* h_codes, uint8_t* h_scales, void* stream) {
+  const int st = check_gated(f, k, m);
+  if (st != QW_OK) return st;
+  if (m * f == 0) return QW_OK;
+  if (!h_codes || !h_scales || (k > 0 && (!codes || !scales || !x_codes || !x_scales)))
+    return QW_ENULL;
+  if (!codes_ok(codes, scales) || !codes_ok(x_codes, x_scales) || !codes_ok(h_codes, h_scales))
+    return QW_EARG;
+  const qw::MxGemm g = {qw::MX_GATED_CODES, f, k, m, codes, scales, x_codes, x_scales, QW_F32,
+                        h_codes, h_scales, nullptr, nullptr};
+  return record(qw::launch_mx_gemm(g, (hipStream_t)stream));
+}
+
+int qw_mx_gated_backward(int64_t f, int64_t k, const uint8_t* codes, const uint8_t* scales,
+                         int64_t m, const uint8_t* x_codes, const uint8_t* x_scales, int type,
+                         const void* dh, void* dgate_up, void* h, void* stream) {
+  const int st = check_gated(f, k, m);
+  if (st != QW_OK) return st;
+  if (!type_ok(type)) return QW_EARG;
+  if (m * f == 0) return QW_OK;
+  if (!dh || !dgate_up || (k > 0 && (!codes || !scales || !x_codes || !x_scales)))
+    return QW_ENULL;
+  if (!codes_ok(codes, scales) || !codes_ok(x_codes, x_scales)) return QW_EARG;
+  const qw::MxGemm g = {qw::MX_GATED_BACKWARD, f, k, m, codes, scales, x_codes, x_scales, type,
+                        dgate_up, nullptr, dh, h};
+  return record(qw::launch_mx_gemm(g, (hipStream_t)stream));
+}
+
+int64_t qw_mx_mlp_work_bytes(int64_t m, int64_t d, int64_t f) {
+  if (check_mx_mlp(m, d, f) != QW_OK) return -1;
+  return MxMlpWork(m, d, f).bytes;
+}
+
+int qw_mx_mlp(int64_t d, int64_t f, const uint8_t* gate_up, const uint8_t* gate_up_scales,
+              const uint8_t* down, const uint8_t* down_scales, int64_t m, int x_type,
+              const void* x, int y_type, void* y, void* work, int64_t work_bytes,
+              void* stream) {
+  int st = check_mx_mlp(m, d, f);
+  if (st != QW_OK) return st;
+  st = check_gated(f, d, m);
+  if (st != QW_OK) return st;
+  if (!mx_fits(d, f)) return QW_ESHAPE;
+  st = check_mx_rows(m, d, f);
+  if (st != QW_OK) return st;
+  if (!type_ok(x_type) || !type_ok(y_type)) return QW_EARG;
+  if (m * d == 0) return QW_OK;
+  if (!x || !y || (f > 0 && (!gate_up || !gate_up_scales || !down || !down_scales)))
+    return QW_ENULL;
+  if (!codes_ok(gate_up, gate_up_scales) || !codes_ok(down, down_scales)) return QW_EARG;
+  const MxMlpWork at(m, d, f);
+  if (!work || work_bytes < at.bytes || !qw::aligned(work, 16)) return QW_EWORK;
+  uint8_t* const b = (uint8_t*)work;
+  st = qw_mx_quantize(0, m, d, x_type, x, b + at.xc, b + at.xs, stream);
+  if (st != QW_OK) return st;
+  st = qw_mx_gated_codes(f, d, gate_up, gate_up_scales, m, b + at.xc, b + at.xs, b + at.hc,
+                         b + at.hs, stream);
+  if (st != QW_OK) return st;
+  return qw_mx_gemm(d, f, down, down_scales, m, b + at.hc, b + at.hs, y_type, y, stream);
 }
 
 // Which kernel family a call with these arguments would take (1 = fast,

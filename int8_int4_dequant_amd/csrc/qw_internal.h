@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/qw.h"
+#include "../../include/qw_mx.h"
 
 namespace qw {
 
@@ -131,6 +132,57 @@ hipError_t launch_moe_combine_backward(int64_t t, int64_t topk, int64_t d, int64
                                        int type, const void* dy, const void* ys,
                                        const int32_t* pos, const float* weights, void* dys,
                                        float* dweights, hipStream_t stream);
+
+// Microscaled 4-bit codes (mx.hip): codes are 16-byte aligned rows of mx_pitch(k) / 2
+// bytes, scales of mx_pitch(k) / 32.
+inline int64_t mx_pitch(int64_t k) { return (k + 511) / 512 * 512; }
+hipError_t launch_mx_quantize(int transpose, int64_t n, int64_t k, int type, const void* w,
+                              uint8_t* codes, uint8_t* scales, hipStream_t stream);
+hipError_t launch_mx_unpack(int64_t n, int64_t k, const uint8_t* codes, const uint8_t* scales,
+                            float* out, hipStream_t stream);
+
+// Products of 4-bit codes (mx_gemm.hip).
+enum MxResult { MX_STORE, MX_GATED, MX_GATED_CODES, MX_GATED_BACKWARD };
+struct MxGemm {
+  MxResult result;
+  int64_t n, k, m;  // outputs of a row (gated: f, of 2 f weight rows), reduction, rows
+  const uint8_t *codes, *scales, *xc, *xs;
+  int y_type;       // of y, dh and h
+  void* y;          // MX_GATED_CODES: codes; MX_GATED_BACKWARD: dgate | dup
+  uint8_t* ys;      // MX_GATED_CODES: their scales
+  const void* dh;
+  void* h;          // MX_GATED_BACKWARD: may be NULL
+};
+hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t stream);
+
+// RMS norm (norm.hip).
+struct RmsNorm {
+  int form;         // 0 float y, 1 e4m3 codes, 2 4-bit codes
+  int64_t rows, d;
+  int type;
+  const void *x, *res;
+  void* sum;
+  int w_type;
+  const void* weight;
+  float eps;
+  int y_type;
+  void *y, *scales;
+};
+hipError_t launch_rms_norm(const RmsNorm& g, hipStream_t stream);
+struct RmsNormBackward {
+  int64_t rows, d;
+  int type;
+  const void *dy, *s;
+  int w_type;
+  const void* weight;
+  float eps;
+  const void* dsum;
+  void* ds;
+  float* dweight;
+  void* work;       // fp32 [rms_norm_shares(rows)][d], for dweight
+};
+int64_t rms_norm_shares(int64_t rows);
+hipError_t launch_rms_norm_backward(const RmsNormBackward& g, hipStream_t stream);
 
 // Which kernel family a call takes (exposed for tests through qw_debug_path).
 enum Path { PATH_NONE = 0, PATH_FAST = 1, PATH_BLOCK = 2, PATH_GENERIC = 3, PATH_MATRIX = 4 };

@@ -45,6 +45,13 @@ EXPORTS = ["qw_payload_bytes", "qw_num_scales", "qw_status_string", "qw_last_err
            "qw_moe_combine", "qw_moe_combine_backward", "qw_moe_mlp_work_bytes", "qw_moe_mlp",
            "qw_block_debug_path"]
 
+#: symbols declared in include/qw_mx.h
+EXPORTS_MX = ["qw_mx_pitch", "qw_mx_quantize", "qw_mx_unpack", "qw_mx_gemm",
+              "qw_mx_matmul_work_bytes", "qw_mx_matmul", "qw_rms_norm", "qw_rms_norm_block",
+              "qw_rms_norm_mx", "qw_rms_norm_backward_work_bytes", "qw_rms_norm_backward",
+              "qw_mx_gated", "qw_mx_gated_codes", "qw_mx_gated_backward",
+              "qw_mx_mlp_work_bytes", "qw_mx_mlp"]
+
 
 # Rows up to which qw_matmul runs the codes GEMV (QW_MATMUL_GEMV_MAX_M in qw.h).
 MATMUL_GEMV_MAX_M = 4
@@ -53,6 +60,8 @@ MATMUL_NOALLOC_MAX_BYTES = 32 << 20
 
 # Values per scale along a row of block-scaled e4m3 codes (QW_BLOCK).
 BLOCK = 128
+# Values per scale of microscaled 4-bit codes (QW_MX_BLOCK).
+MX_BLOCK = 32
 # QW_F32 and QW_BF16 (enum qw_type), by tensor type.
 TYPES = {torch.float32: 0, torch.bfloat16: 1}
 # Most experts and slots of the expert calls (QW_MOE_MAX_EXPERTS, QW_MOE_MAX_SLOTS).
@@ -189,6 +198,39 @@ def lib():
     L.qw_moe_mlp.restype = i32
     L.qw_block_debug_path.argtypes = [i32, i64, i64, i64, i64, i32]
     L.qw_block_debug_path.restype = i32
+    f32 = ctypes.c_float
+    L.qw_mx_pitch.argtypes = [i64]
+    L.qw_mx_pitch.restype = i64
+    L.qw_mx_quantize.argtypes = [i32, i64, i64, i32, vp, vp, vp, vp]
+    L.qw_mx_quantize.restype = i32
+    L.qw_mx_unpack.argtypes = [i64, i64, vp, vp, vp, vp]
+    L.qw_mx_unpack.restype = i32
+    L.qw_mx_gemm.argtypes = [i64, i64, vp, vp, i64, vp, vp, i32, vp, vp]
+    L.qw_mx_gemm.restype = i32
+    L.qw_mx_matmul_work_bytes.argtypes = [i64, i64]
+    L.qw_mx_matmul_work_bytes.restype = i64
+    L.qw_mx_matmul.argtypes = [i64, i64, vp, vp, i64, i32, vp, i32, vp, vp, i64, vp]
+    L.qw_mx_matmul.restype = i32
+    L.qw_rms_norm.argtypes = [i64, i64, i32, vp, vp, vp, i32, vp, f32, i32, vp, vp]
+    L.qw_rms_norm.restype = i32
+    L.qw_rms_norm_block.argtypes = [i64, i64, i32, vp, vp, vp, i32, vp, f32, vp, vp, vp]
+    L.qw_rms_norm_block.restype = i32
+    L.qw_rms_norm_mx.argtypes = [i64, i64, i32, vp, vp, vp, i32, vp, f32, vp, vp, vp]
+    L.qw_rms_norm_mx.restype = i32
+    L.qw_rms_norm_backward_work_bytes.argtypes = [i64, i64]
+    L.qw_rms_norm_backward_work_bytes.restype = i64
+    L.qw_rms_norm_backward.argtypes = [i64, i64, i32, vp, vp, i32, vp, f32, vp, vp, vp, vp, i64, vp]
+    L.qw_rms_norm_backward.restype = i32
+    L.qw_mx_gated.argtypes = [i64, i64, vp, vp, i64, vp, vp, i32, vp, vp]
+    L.qw_mx_gated.restype = i32
+    L.qw_mx_gated_codes.argtypes = [i64, i64, vp, vp, i64, vp, vp, vp, vp, vp]
+    L.qw_mx_gated_codes.restype = i32
+    L.qw_mx_gated_backward.argtypes = [i64, i64, vp, vp, i64, vp, vp, i32, vp, vp, vp, vp]
+    L.qw_mx_gated_backward.restype = i32
+    L.qw_mx_mlp_work_bytes.argtypes = [i64, i64, i64]
+    L.qw_mx_mlp_work_bytes.restype = i64
+    L.qw_mx_mlp.argtypes = [i64, i64, vp, vp, vp, vp, i64, i32, vp, i32, vp, vp, i64, vp]
+    L.qw_mx_mlp.restype = i32
     _lib = L
     return L
 
@@ -432,6 +474,90 @@ def qw_moe_mlp(block_rows, experts, d, f, gate_up, gate_up_scales, down, down_sc
 
 def qw_block_debug_path(op, experts, m, n, k, y_type):
     return lib().qw_block_debug_path(op, experts, m, n, k, y_type)
+
+
+def qw_mx_pitch(k):
+    return lib().qw_mx_pitch(k)
+
+
+def qw_mx_quantize(transpose, n, k, type, w, codes, scales, stream=None):
+    return lib().qw_mx_quantize(transpose, n, k, type, _ptr(w), _ptr(codes), _ptr(scales),
+                                _stream(stream))
+
+
+def qw_mx_unpack(n, k, codes, scales, out, stream=None):
+    return lib().qw_mx_unpack(n, k, _ptr(codes), _ptr(scales), _ptr(out), _stream(stream))
+
+
+def qw_mx_gemm(n, k, codes, scales, m, x_codes, x_scales, y_type, y, stream=None):
+    return lib().qw_mx_gemm(n, k, _ptr(codes), _ptr(scales), m, _ptr(x_codes), _ptr(x_scales),
+                            y_type, _ptr(y), _stream(stream))
+
+
+def qw_mx_matmul_work_bytes(m, k):
+    return lib().qw_mx_matmul_work_bytes(m, k)
+
+
+def qw_mx_matmul(n, k, codes, scales, m, x_type, x, y_type, y, work, work_bytes, stream=None):
+    return lib().qw_mx_matmul(n, k, _ptr(codes), _ptr(scales), m, x_type, _ptr(x), y_type,
+                              _ptr(y), _ptr(work), work_bytes, _stream(stream))
+
+
+def qw_rms_norm(rows, d, type, x, residual, sum, weight_type, weight, eps, y_type, y,
+                stream=None):
+    return lib().qw_rms_norm(rows, d, type, _ptr(x), _ptr(residual), _ptr(sum), weight_type,
+                             _ptr(weight), eps, y_type, _ptr(y), _stream(stream))
+
+
+def qw_rms_norm_block(rows, d, type, x, residual, sum, weight_type, weight, eps, codes, scales,
+                      stream=None):
+    return lib().qw_rms_norm_block(rows, d, type, _ptr(x), _ptr(residual), _ptr(sum), weight_type,
+                                   _ptr(weight), eps, _ptr(codes), _ptr(scales), _stream(stream))
+
+
+def qw_rms_norm_mx(rows, d, type, x, residual, sum, weight_type, weight, eps, codes, scales,
+                   stream=None):
+    return lib().qw_rms_norm_mx(rows, d, type, _ptr(x), _ptr(residual), _ptr(sum), weight_type,
+                                _ptr(weight), eps, _ptr(codes), _ptr(scales), _stream(stream))
+
+
+def qw_rms_norm_backward_work_bytes(rows, d):
+    return lib().qw_rms_norm_backward_work_bytes(rows, d)
+
+
+def qw_rms_norm_backward(rows, d, type, dy, s, weight_type, weight, eps, dsum, ds, dweight, work,
+                         work_bytes, stream=None):
+    return lib().qw_rms_norm_backward(rows, d, type, _ptr(dy), _ptr(s), weight_type, _ptr(weight),
+                                      eps, _ptr(dsum), _ptr(ds), _ptr(dweight), _ptr(work),
+                                      work_bytes, _stream(stream))
+
+
+def qw_mx_gated(f, k, codes, scales, m, x_codes, x_scales, h_type, h, stream=None):
+    return lib().qw_mx_gated(f, k, _ptr(codes), _ptr(scales), m, _ptr(x_codes), _ptr(x_scales),
+                             h_type, _ptr(h), _stream(stream))
+
+
+def qw_mx_gated_codes(f, k, codes, scales, m, x_codes, x_scales, h_codes, h_scales, stream=None):
+    return lib().qw_mx_gated_codes(f, k, _ptr(codes), _ptr(scales), m, _ptr(x_codes),
+                                   _ptr(x_scales), _ptr(h_codes), _ptr(h_scales), _stream(stream))
+
+
+def qw_mx_gated_backward(f, k, codes, scales, m, x_codes, x_scales, type, dh, dgate_up, h,
+                         stream=None):
+    return lib().qw_mx_gated_backward(f, k, _ptr(codes), _ptr(scales), m, _ptr(x_codes),
+                                      _ptr(x_scales), type, _ptr(dh), _ptr(dgate_up), _ptr(h),
+                                      _stream(stream))
+
+
+def qw_mx_mlp_work_bytes(m, d, f):
+    return lib().qw_mx_mlp_work_bytes(m, d, f)
+
+
+def qw_mx_mlp(d, f, gate_up, gate_up_scales, down, down_scales, m, x_type, x, y_type, y, work,
+              work_bytes, stream=None):
+    return lib().qw_mx_mlp(d, f, _ptr(gate_up), _ptr(gate_up_scales), _ptr(down),
+                           _ptr(down_scales), m, x_type, _ptr(x), y_type, _ptr(y), _ptr(work),
+                           work_bytes, _stream(stream))
 
 
 # -------------------------------------------------------- convenience layer
@@ -1132,4 +1258,241 @@ def moe_mlp(gate_up, down, x, ids, weights=None, out=None, out_dtype=None, work=
     work, kp, kb = _workspace(work, lib().qw_moe_mlp_work_bytes(t, topk, e, d, f), x)
     _run("qw_moe_mlp", dev, stream, lib().qw_moe_mlp, br, e, d, f, gc, gs, dc, ds, t, topk, xt,
          x.data_ptr(), nbytes, ids.data_ptr(), wp, yt, out.data_ptr(), kp, kb)
+    return out
+
+
+# ------------------------------------------- microscaled 4-bit codes, RMS norm
+#
+# Records: ``{bits: 4, block: 32, shape: [n, k], codes (uint8 [n][pitch / 2]), scales
+# (uint8 [n][pitch / 32])}``, pitch being k rounded up to 512.
+
+
+_CODES4 = (torch.uint8, torch.float4_e2m1fn_x2)
+_SCALES4 = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _mx_pitch(k):
+    return (k + 511) // 512 * 512
+
+
+def _check_mx(rec, what="record"):
+    """Sizes and addresses of a 4-bit record whose codes and scales match its shape:
+    (n, k, codes, scales)."""
+    if rec.get("bits") != 4 or rec.get("block") != MX_BLOCK:
+        raise ValueError(f"{what}: not a record of 4-bit codes with a scale per {MX_BLOCK}")
+    n, k = _nk(rec["shape"])
+    kp = _mx_pitch(k)
+    codes = _fits(rec["codes"], _CODES4, n * kp // 2, f"{what} codes")
+    scales = _fits(rec["scales"], _SCALES4, n * kp // MX_BLOCK, f"{what} scales")
+    return n, k, codes, scales
+
+
+def _empty_mx(n, k, device):
+    kp = _mx_pitch(k)
+    return dict(bits=4, block=MX_BLOCK, shape=[n, k],
+                codes=torch.empty((n, kp // 2), dtype=torch.uint8, device=device),
+                scales=torch.empty((n, kp // MX_BLOCK), dtype=torch.uint8, device=device))
+
+
+def _check_x_mx(x, k, what="x"):
+    m, kx, codes, scales = _check_mx(x, what)
+    if kx != k:
+        raise ValueError(f"{what} must be a record of [m][{k}]")
+    return m, codes, scales
+
+
+@_on_stream
+def mx_quantize(w, transpose=False, stream=None):
+    """Quantize a contiguous fp32 or bf16 device tensor [n][k] to 4-bit
+    floating-point codes with a power-of-two scale per 32 values of a row; with
+    ``transpose`` the record is that of w's columns, [k][n].  Returns a record."""
+    t = _check_matrix(w, "w")
+    dev = _device_of(w)
+    n, k = w.shape
+    rec = _empty_mx(k, n, w.device) if transpose else _empty_mx(n, k, w.device)
+    _run("qw_mx_quantize", dev, stream, lib().qw_mx_quantize, 1 if transpose else 0, n, k, t,
+         w.data_ptr(), rec["codes"].data_ptr(), rec["scales"].data_ptr())
+    return rec
+
+
+@_on_stream
+def mx_unpack(rec, out=None, stream=None):
+    """The fp32 values that a record's 4-bit codes stand for."""
+    n, k, codes, scales = _check_mx(rec)
+    if out is None:
+        out = torch.empty((n, k), dtype=torch.float32, device=rec["codes"].device)
+    _check_tensor(out, torch.float32, n * k, "out", (n, k))
+    dev = _device_of(rec["codes"], rec["scales"], out)
+    _run("qw_mx_unpack", dev, stream, lib().qw_mx_unpack, n, k, codes, scales, out.data_ptr())
+    return out
+
+
+@_on_stream
+def mx_gemm(rec, x, out=None, out_dtype=None, stream=None):
+    """y [m][n] = x . W^T of two records: ``rec`` the weight [n][k], ``x`` m rows
+    of k values; of ``out``'s type, ``out_dtype`` or fp32."""
+    n, k, codes, scales = _check_mx(rec)
+    m, xc, xs = _check_x_mx(x, k)
+    out, yt = _output(out, m, n, out_dtype or (torch.float32 if out is None else None), x["codes"])
+    dev = _device_of(rec["codes"], rec["scales"], x["codes"], x["scales"], out)
+    _run("qw_mx_gemm", dev, stream, lib().qw_mx_gemm, n, k, codes, scales, m, xc, xs, yt,
+         out.data_ptr())
+    return out
+
+
+@_on_stream
+def mx_matmul(rec, x, out=None, out_dtype=None, work=None, stream=None):
+    """Float x [m][k] (fp32 or bf16, any m), quantized to 4 bits on the way, times
+    a record's weight; returns y [m][n] of x's type (or ``out_dtype``)."""
+    n, k, codes, scales = _check_mx(rec)
+    xt = _check_matrix(x, "x", None, k)
+    m = x.shape[0]
+    out, yt = _output(out, m, n, out_dtype or (x.dtype if out is None else None), x)
+    dev = _device_of(rec["codes"], rec["scales"], x, out, work)
+    work, wp, wb = _workspace(work, lib().qw_mx_matmul_work_bytes(m, k), x)
+    _run("qw_mx_matmul", dev, stream, lib().qw_mx_matmul, n, k, codes, scales, m, xt,
+         x.data_ptr(), yt, out.data_ptr(), wp, wb)
+    return out
+
+
+def _check_gain(weight, d):
+    """Type's code and address of a norm's weight (or None)."""
+    if weight is None:
+        return 0, None
+    return _type(weight.dtype, "weight"), _fits(weight, tuple(TYPES), d, "weight")
+
+
+@_on_stream
+def rms_norm(x, weight=None, residual=None, eps=1e-6, out=None, out_dtype=None, sum=None,
+             quantize=None, stream=None):
+    """RMS norm of s = x + residual (x itself without one), x [rows][d]: s / sqrt(mean
+    s^2 + eps) * weight.  Returns (y, s).  ``quantize``: None (y is a tensor of
+    ``out``'s type, ``out_dtype`` or x's), "block" (a record of e4m3 codes, 1 x 128
+    blocks) or "mx" (a record of 4-bit codes).  s has x's type and goes to ``sum`` if
+    given, which may be x or residual; weight [d] is fp32 or bf16."""
+    t = _check_matrix(x, "x")
+    rows, d = x.shape
+    wt, wp = _check_gain(weight, d)
+    if residual is not None:
+        _check_matrix(residual, "residual", rows, d, x.dtype)
+        if sum is None:
+            sum = torch.empty_like(x)
+    if sum is not None:
+        _check_matrix(sum, "sum", rows, d, x.dtype)
+    if quantize not in (None, "block", "mx"):
+        raise ValueError('quantize must be None, "block" or "mx"')
+    if quantize and (out is not None or out_dtype is not None):
+        raise ValueError("a quantized result has no out and no out_dtype")
+    dev = _device_of(x, weight, residual, sum, out)
+    args = (rows, d, t, x.data_ptr(), None if residual is None else residual.data_ptr(),
+            None if sum is None else sum.data_ptr(), wt, wp, eps)
+    if quantize:
+        y = _empty_block(1, (rows, d), x.device) if quantize == "block" else _empty_mx(rows, d, x.device)
+        name = "qw_rms_norm_" + quantize
+        _run(name, dev, stream, getattr(lib(), name), *args, y["codes"].data_ptr(),
+             y["scales"].data_ptr())
+    else:
+        y, yt = _output(out, rows, d, out_dtype or (x.dtype if out is None else None), x)
+        _run("qw_rms_norm", dev, stream, lib().qw_rms_norm, *args, yt, y.data_ptr())
+    return y, x if sum is None else sum
+
+
+@_on_stream
+def rms_norm_backward(dy, s, weight=None, eps=1e-6, dsum=None, ds=None, dweight=None, work=None,
+                      stream=None):
+    """Gradients of rms_norm for the output gradient dy [rows][d], s the sum that it
+    returned: (ds, dweight).  ds is the gradient of x and of the residual, with
+    ``dsum``, the gradient that reaches s past the norm, added.  dy, s, dsum and ds
+    have one type; dweight is fp32 [d], None without a weight."""
+    t = _check_matrix(s, "s")
+    rows, d = s.shape
+    _check_matrix(dy, "dy", rows, d, s.dtype)
+    wt, wp = _check_gain(weight, d)
+    if dsum is not None:
+        _check_matrix(dsum, "dsum", rows, d, s.dtype)
+    if ds is None:
+        ds = torch.empty_like(s)
+    _check_matrix(ds, "ds", rows, d, s.dtype)
+    if dweight is None and weight is not None:
+        dweight = torch.empty(d, dtype=torch.float32, device=s.device)
+    if dweight is not None:
+        _check_tensor(dweight, torch.float32, d, "dweight", (d,))
+    dev = _device_of(dy, s, weight, dsum, ds, dweight, work)
+    need = 0 if dweight is None else lib().qw_rms_norm_backward_work_bytes(rows, d)
+    work, kp, kb = _workspace(work, need, s)
+    _run("qw_rms_norm_backward", dev, stream, lib().qw_rms_norm_backward, rows, d, t,
+         dy.data_ptr(), s.data_ptr(), wt, wp, eps, None if dsum is None else dsum.data_ptr(),
+         ds.data_ptr(), None if dweight is None else dweight.data_ptr(), kp, kb)
+    return ds, dweight
+
+
+def _check_gate_up(rec):
+    """(f, k, codes, scales) of the record of a gate and an up matrix."""
+    n, k, codes, scales = _check_mx(rec, "gate_up")
+    if n % 2:
+        raise ValueError("gate_up must be a record of [2 f][k]")
+    return n // 2, k, codes, scales
+
+
+@_on_stream
+def mx_gated(gate_up, x, out=None, out_dtype=None, quantize=False, stream=None):
+    """silu(gate) * up in one product: ``gate_up`` a record of [2 f][k] (gate rows,
+    then up rows), ``x`` a record of [m][k].  Returns h [m][f] of ``out``'s type,
+    ``out_dtype`` or fp32, or with ``quantize`` its record of 4-bit codes."""
+    f, k, codes, scales = _check_gate_up(gate_up)
+    m, xc, xs = _check_x_mx(x, k)
+    dev = _device_of(gate_up["codes"], gate_up["scales"], x["codes"], x["scales"], out)
+    if quantize:
+        if out is not None or out_dtype is not None:
+            raise ValueError("a quantized result has no out and no out_dtype")
+        h = _empty_mx(m, f, x["codes"].device)
+        _run("qw_mx_gated_codes", dev, stream, lib().qw_mx_gated_codes, f, k, codes, scales, m, xc,
+             xs, h["codes"].data_ptr(), h["scales"].data_ptr())
+        return h
+    out, ht = _output(out, m, f, out_dtype or (torch.float32 if out is None else None), x["codes"])
+    _run("qw_mx_gated", dev, stream, lib().qw_mx_gated, f, k, codes, scales, m, xc, xs, ht,
+         out.data_ptr())
+    return out
+
+
+@_on_stream
+def mx_gated_backward(gate_up, x, dh, out=None, h=True, stream=None):
+    """Gradients of mx_gated with regard to gate and up for dh [m][f]: (dgate | dup
+    [m][2 f], h [m][f]), of dh's type.  gate and up are computed again.  ``h``: True,
+    a tensor for it, or False (None is returned for it)."""
+    f, k, codes, scales = _check_gate_up(gate_up)
+    m, xc, xs = _check_x_mx(x, k)
+    t = _check_matrix(dh, "dh", m, f)
+    if out is None:
+        out = torch.empty((m, 2 * f), dtype=dh.dtype, device=dh.device)
+    _check_matrix(out, "out", m, 2 * f, dh.dtype)
+    if h is True:
+        h = torch.empty_like(dh)
+    elif h is False:
+        h = None
+    if h is not None:
+        _check_matrix(h, "h", m, f, dh.dtype)
+    dev = _device_of(gate_up["codes"], gate_up["scales"], x["codes"], x["scales"], dh, out, h)
+    _run("qw_mx_gated_backward", dev, stream, lib().qw_mx_gated_backward, f, k, codes, scales, m,
+         xc, xs, t, dh.data_ptr(), out.data_ptr(), None if h is None else h.data_ptr())
+    return out, h
+
+
+@_on_stream
+def mx_mlp(gate_up, down, x, out=None, out_dtype=None, work=None, stream=None):
+    """A gated feed-forward block in one call: x [m][d] (fp32 or bf16), ``gate_up`` a
+    record of [2 f][d] (gate rows, then up rows), ``down`` of [d][f]; x and the gated
+    values are quantized to 4 bits on the way.  y [m][d] of x's type or ``out_dtype``."""
+    f, d, gc, gs = _check_gate_up(gate_up)
+    dd, df, dc, ds = _check_mx(down, "down")
+    if dd != d or df != f:
+        raise ValueError("gate_up must be a record of [2 f][d] and down of [d][f]")
+    xt = _check_matrix(x, "x", None, d)
+    m = x.shape[0]
+    out, yt = _output(out, m, d, out_dtype or (x.dtype if out is None else None), x)
+    dev = _device_of(gate_up["codes"], gate_up["scales"], down["codes"], down["scales"], x, out,
+                     work)
+    work, kp, kb = _workspace(work, lib().qw_mx_mlp_work_bytes(m, d, f), x)
+    _run("qw_mx_mlp", dev, stream, lib().qw_mx_mlp, d, f, gc, gs, dc, ds, m, xt, x.data_ptr(), yt,
+         out.data_ptr(), kp, kb)
     return out
