@@ -34,7 +34,7 @@ struct MxArgs {
   const void* dh;
   void* h;
   int64_t tiles_m, tiles;
-  int vec;            // 4 outputs of a row at a time may be stored as one
+  int vec;            // 16 bytes of outputs may be stored as one
 };
 
 // Step S of two: blocks 2 (l / 32) + S of a step of 128; the scales in byte S.
@@ -46,21 +46,53 @@ __device__ __forceinline__ f32x16 mfma64(i32x4 a, i32x4 b, f32x16 c, int sa, int
 }
 
 // ---------------------------------------------------------------- results
+//
+// A lane has 16 outputs of a fragment's 32.  Results of 2 bytes, and codes, are kept so that
+// weight row i of a fragment is its row i with bits 2 and 3 swapped: the lane's outputs are
+// then 8 consecutive ones at 8 (l / 32) and 8 at 16 + 8 (l / 32), which two lanes write as 32
+// bytes (4096 x 4096 bf16 outputs of k = 512: 18.9 us; in runs of 8 bytes 26.0).
+// For results of 4 bytes the runs are 4 long and 32 bytes as they are.
 
-template <typename T>
-__device__ __forceinline__ void put4(T* p, const float v[4], int64_t left, bool vec) {
-  if (vec) {
-    store4(p, f32x4{v[0], v[1], v[2], v[3]});
+template <MxResult RES, typename T>
+constexpr bool kSwapped = RES == MX_GATED_CODES || sizeof(T) == 2;
+
+__device__ __forceinline__ int swapped(int row) {  // bits 2 and 3
+  return (row & ~12) | (row & 4) << 1 | (row & 8) >> 1;
+}
+
+// A lane's runs of consecutive outputs: RUN of them from column at(g, half) on.
+template <typename T> struct Runs {
+  static constexpr int RUN = sizeof(T) == 2 ? 8 : 4;
+  static __device__ __forceinline__ int at(int g, int half) { return 2 * RUN * g + RUN * half; }
+};
+
+template <int RUN, typename T>
+__device__ __forceinline__ void put(T* p, const float* v, int64_t left, bool vec) {
+  if (vec && left >= RUN) {
+    if constexpr (RUN == 8)
+      store8<true>(p, v);
+    else
+      store4(p, f32x4{v[0], v[1], v[2], v[3]});
   } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < RUN; ++c)
       if (c < left) store1(p + c, v[c]);
   }
 }
-template <typename T>
-__device__ __forceinline__ void get4(const T* p, float v[4], int64_t left) {
+template <int RUN, typename T>
+__device__ __forceinline__ void get(const T* p, float* v, int64_t left, bool vec) {
+  if (vec && left >= RUN) {
+    if constexpr (RUN == 8) {
+      load8<true>(p, v);
+    } else {
+      const f32x4 t = *(const f32x4*)p;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) v[c] = c < left ? load1(p + c) : 0.0f;
+      for (int c = 0; c < RUN; ++c) v[c] = t[c];
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < RUN; ++c) v[c] = c < left ? load1(p + c) : 0.0f;
+  }
 }
 
 // dgate and dup, h.  With e = exp(-|gate|) neither t nor 1 - t overflows or cancels;
@@ -78,37 +110,40 @@ __device__ __forceinline__ void gate_gradients(float gate, float up, float dh, f
   h = silu * up;
 }
 
-// A fragment's 16 outputs of a lane: rows 8 g + 4 half + c of 32, for column col0 of
-// output row `row`.
+// A fragment's outputs, of columns from col0 on of output row `row`.
 template <typename T>
 __device__ __forceinline__ void store_fragment(const MxArgs& a, f32x16 v, int64_t row,
                                                int64_t col0, int half) {
+  using R = Runs<T>;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int64_t col = col0 + 8 * g + 4 * half;
-    if (col >= a.n) continue;
-    const float o[4] = {v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
-    put4((T*)a.y + row * a.n + col, o, a.n - col, a.vec);
+  for (int g = 0; g < 16 / R::RUN; ++g) {
+    const int64_t col = col0 + R::at(g, half);
+    float o[R::RUN];
+#pragma unroll
+    for (int c = 0; c < R::RUN; ++c) o[c] = v[R::RUN * g + c];
+    put<R::RUN>((T*)a.y + row * a.n + col, o, a.n - col, a.vec);
   }
 }
 
 template <MxResult RES, typename T>
 __device__ __forceinline__ void store_gated(const MxArgs& a, f32x16 gate, f32x16 up, int64_t row,
                                             int64_t col0, int half, bool have) {
+  using R = Runs<T>;
+  constexpr int RUN = R::RUN;
   if constexpr (RES == MX_GATED_BACKWARD) {
     if (!have) return;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int64_t col = col0 + 8 * g + 4 * half, left = a.n - col;
+    for (int g = 0; g < 16 / RUN; ++g) {
+      const int64_t col = col0 + R::at(g, half), left = a.n - col;
       if (left <= 0) continue;
-      float dh[4], dg[4], du[4], h[4];
-      get4((const T*)a.dh + row * a.n + col, dh, left);
+      float dh[RUN], dg[RUN], du[RUN], h[RUN];
+      get<RUN>((const T*)a.dh + row * a.n + col, dh, left, a.vec);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        gate_gradients(gate[4 * g + c], up[4 * g + c], dh[c], dg[c], du[c], h[c]);
-      put4((T*)a.y + row * 2 * a.n + col, dg, left, a.vec);
-      put4((T*)a.y + row * 2 * a.n + a.n + col, du, left, a.vec);
-      if (a.h) put4((T*)a.h + row * a.n + col, h, left, a.vec);
+      for (int c = 0; c < RUN; ++c)
+        gate_gradients(gate[RUN * g + c], up[RUN * g + c], dh[c], dg[c], du[c], h[c]);
+      put<RUN>((T*)a.y + row * 2 * a.n + col, dg, left, a.vec);
+      put<RUN>((T*)a.y + row * 2 * a.n + a.n + col, du, left, a.vec);
+      if (a.h) put<RUN>((T*)a.h + row * a.n + col, h, left, a.vec);
     }
   } else {
     float v[16], p[16], q[16];
@@ -121,23 +156,20 @@ __device__ __forceinline__ void store_gated(const MxArgs& a, f32x16 gate, f32x16
     if constexpr (RES == MX_GATED) {
       if (!have) return;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int64_t col = col0 + 8 * g + 4 * half;
-        if (col < a.n) put4((T*)a.y + row * a.n + col, v + 4 * g, a.n - col, a.vec);
+      for (int g = 0; g < 16 / RUN; ++g) {
+        const int64_t col = col0 + R::at(g, half);
+        put<RUN>((T*)a.y + row * a.n + col, v + RUN * g, a.n - col, a.vec);
       }
     } else {
       // The 32 values are one block: half of them in the lane 32 away.
       uint32_t top = top_of<16>(v);
       top = max(top, (uint32_t)__shfl_xor((int)top, 32));
       const uint32_t s = mx_scale(top);
-      const uint32_t lo = mx_codes8(v, s), hi = mx_codes8(v + 8, s);  // groups 0, 1 and 2, 3
-      // lane half 0 keeps groups 0 and 1 of both halves, half 1 groups 2 and 3
-      const uint32_t other = (uint32_t)__shfl_xor((int)(half ? lo : hi), 32);
-      const uint32_t own = half ? hi : lo;
-      const uint32_t h0 = half ? other : own, h1 = half ? own : other;
-      const u32x2 out = {(h0 & 0xFFFFu) | h1 << 16, h0 >> 16 | (h1 & 0xFFFF0000u)};
+      const uint32_t lo = mx_codes8(v, s), hi = mx_codes8(v + 8, s);
       if (have && col0 < a.yp) {
-        *(u32x2*)((uint8_t*)a.y + (row * a.yp + col0) / 2 + 8 * half) = out;
+        uint8_t* const to = (uint8_t*)a.y + (row * a.yp + col0) / 2 + 4 * half;
+        *(uint32_t*)to = lo;
+        *(uint32_t*)(to + 8) = hi;
         if (half == 0) a.ys[(row * a.yp + col0) / 32] = (uint8_t)s;
       }
     }
@@ -176,112 +208,140 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
   const int wm = wave % WM * 32 * MF, wn = wave / WM * 32 * NF;
   int64_t tm, tn;
   tile_place(blockIdx.x, a.tiles, a.tiles_m, tm, tn);
-  const int64_t n0 = tn * COLS, m0 = tm * BM, end = min(m0 + BM, a.m);
-  // nothing is there behind the last output: only padding of a row of codes
-  const int64_t cols = max((int64_t)0, min(a.n - n0, (int64_t)COLS));
-  const i32x4 wbuf = buffer_of(a.w + n0 * a.kp2, (uint32_t)(cols * a.kp2));
-  const i32x4 ubuf = buffer_of(a.w + (GATED ? (a.n + n0) * a.kp2 : 0), (uint32_t)(cols * a.kp2));
-  const i32x4 xbuf = buffer_of(a.x + m0 * a.kp2, (uint32_t)((end - m0) * a.kp2));
-  const i32x4 wsbuf = buffer_of(a.ws + n0 * a.ksp, (uint32_t)(cols ? ((GATED ? a.n : 0) + cols) * a.ksp : 0));
-  const i32x4 xsbuf = buffer_of(a.xs + m0 * a.ksp, (uint32_t)((end - m0) * a.ksp));
+  const int64_t n0 = uniform(tn) * COLS, m0 = uniform(tm) * BM;
+  const int rows = __builtin_amdgcn_readfirstlane((int)min(a.m - m0, (int64_t)BM));
+  // behind the last output there is nothing: only padding of a row of codes
+  const int cols = __builtin_amdgcn_readfirstlane((int)max((int64_t)0, min(a.n - n0, (int64_t)COLS)));
   const int kb = cols ? a.kb : 0;
+  // the weight row (of gate or up) that LDS row `row` holds
+  auto weight_row = [](int row) {
+    const int at = GATED ? row / 64 * 32 + row % 32 : row;
+    return kSwapped<RES, T> ? swapped(at) : at;
+  };
+  // each piece's buffer, of which its rows behind the last one are not a part
+  auto choose = [&](bool of_x, bool up, const uint8_t* xbase, const uint8_t* wbase, int64_t bytes) {
+    const int64_t size = of_x ? rows * bytes : cols * bytes;
+    return buffer_of((const uint8_t*)uniform((int64_t)(of_x ? xbase + m0 * bytes : wbase + (n0 + (up ? a.n : 0)) * bytes)),
+                     __builtin_amdgcn_readfirstlane((uint32_t)size));
+  };
   uint32_t voff[SEGS];
+  i32x4 from[SEGS];
 #pragma unroll
   for (int s = 0; s < SEGS; ++s) {
+    const int seg = wave + WAVES * s;
+    from[s] = choose(seg >= BN / 16, GATED && seg / 2 % 2, a.x, a.w, a.kp2);
     const int row = (wave + WAVES * s) * 16 + (lane >> 2);
     const int c = (lane & 3) ^ ((row >> 2) & 3);
-    const int at = row >= BN ? row - BN : GATED ? row / 64 * 32 + row % 32 : row;
+    const int at = row >= BN ? row - BN : weight_row(row);
     voff[s] = (uint32_t)at * (uint32_t)a.kp2 + c * 16;
   }
   uint32_t soff[SPER];
+  i32x4 sfrom[SPER];
 #pragma unroll
   for (int s = 0; s < SPER; ++s) {
-    const int row = (wave + WAVES * s) * 64 + lane;
-    const int64_t at = row >= BN ? row - BN : GATED ? row / 64 * 32 + row % 32 + (row / 32 % 2 ? a.n : 0) : row;
+    const int seg = wave + WAVES * s;
+    sfrom[s] = choose(seg >= BN / 64, false, a.xs, a.ws, a.ksp);
+    // gate and up rows in turn: in one buffer up to the last of the up rows
+    if (GATED && seg < BN / 64) sfrom[s].z = cols ? sfrom[s].z + (int)(uint32_t)(a.n * a.ksp) : 0;
+    const int row = seg * 64 + lane;
+    const int64_t at = row >= BN ? row - BN : weight_row(row) + (GATED && row / 32 % 2 ? a.n : 0);
     soff[s] = (uint32_t)(at * a.ksp);
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0];
   const uint32_t lds1 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&scales[0][0];
   // Behind the last step there is nothing to read, but the copy is issued all the same
   // (as zeros, from an empty buffer), so that every step has as many.
-  auto fetch = [&](int b, int buf) {
+  auto fetch = [&](int b, int buf, int s) {
+    if (s >= SEGS) return;
     const bool in = b < kb;
-#pragma unroll
-    for (int s = 0; s < SEGS; ++s) {
-      const int seg = wave + WAVES * s;
-      i32x4 from = seg >= BN / 16 ? xbuf : GATED && seg / 2 % 2 ? ubuf : wbuf;
-      from.z = in ? from.z : 0;
-      copy_to_lds(from, voff[s], in ? (uint32_t)b * 64 : 0, lds0 + buf * (ROWS * 64) + seg * 1024);
-    }
+    const int seg = wave + WAVES * s;
+    i32x4 buffer = from[s];
+    buffer.z = in ? buffer.z : 0;
+    copy_to_lds(buffer, voff[s], in ? (uint32_t)b * 64 : 0, lds0 + buf * (ROWS * 64) + seg * 1024);
   };
-  auto fetch_scales = [&](int u) {  // of steps 4 u .. 4 u + 3
+  auto fetch_scales = [&](int u, bool when) {  // of steps 4 u .. 4 u + 3
     const bool in = 4 * u < kb;
 #pragma unroll
     for (int s = 0; s < SPER; ++s) {
       const int seg = wave + WAVES * s;
-      if (seg >= SCALES) break;
-      i32x4 from = seg >= BN / 64 ? xsbuf : wsbuf;
-      from.z = in ? from.z : 0;
-      copy_to_lds(from, soff[s], in ? (uint32_t)u * 16 : 0, lds1 + (u & 1) * (ROWS * 16) + seg * 1024);
+      i32x4 buffer = sfrom[s];
+      buffer.z = in ? buffer.z : 0;
+      copy_to_lds_when(__builtin_amdgcn_readfirstlane(when && seg < SCALES ? 1 : 0), buffer, soff[s], in ? (uint32_t)u * 16 : 0,
+                       lds1 + (u & 1) * (ROWS * 16) + seg * 1024);
     }
   };
-  fetch_scales(0);
-  fetch_scales(1);
+  fetch_scales(0, true);
+  fetch_scales(1, true);
 #pragma unroll
-  for (int b = 0; b < STAGES; ++b) fetch(b, b);
+  for (int b = 0; b < STAGES; ++b)
+#pragma unroll
+    for (int s = 0; s < SEGS; ++s) fetch(b, b, s);
 
   f32x16 acc[NF][MF] = {};
-  i32x4 w0[NF], x0[MF], w1[NF], x1[MF];
+  i32x4 w[2][NF], x[2][MF];  // fragments of the two halves of a step
   int sw[NF], sx[MF], sw2[NF], sx2[MF];
   const int swap = (r >> 2) & 3;  // the same for all rows a multiple of 32 apart
-  auto take = [&](int buf, int s, i32x4* w, i32x4* x) {
-    const uint8_t* p = &lds[buf][r * 64 + (((2 * half + s) ^ swap) << 4)];
-#pragma unroll
-    for (int i = 0; i < NF; ++i) w[i] = *(const i32x4*)(p + (wn + 32 * i) * 64);
-#pragma unroll
-    for (int j = 0; j < MF; ++j) x[j] = *(const i32x4*)(p + (BN + wm + 32 * j) * 64);
+  // Read N of the fragments of half S of the step in buffer `buf`: the first products' first.
+  auto take = [&](int buf, auto half_of, int n) {
+    constexpr int S = decltype(half_of)::value;
+    const uint8_t* p = &lds[buf][r * 64 + (((2 * half + S) ^ swap) << 4)];
+    if (n < MF)
+      x[S][n] = *(const i32x4*)(p + (BN + wm + 32 * n) * 64);
+    else if (n < MF + NF)
+      w[S][n - MF] = *(const i32x4*)(p + (wn + 32 * (n - MF)) * 64);
   };
-  auto take_scales = [&](int b, int* w, int* x) {
+  auto take_scale = [&](int b, int n) {
     const uint8_t* p = &scales[(b >> 2) & 1][r * 16 + (b & 3) * 4];
-#pragma unroll
-    for (int i = 0; i < NF; ++i) w[i] = *(const int*)(p + (wn + 32 * i) * 16);
-#pragma unroll
-    for (int j = 0; j < MF; ++j) x[j] = *(const int*)(p + (BN + wm + 32 * j) * 16);
+    if (n < MF)
+      sx2[n] = *(const int*)(p + (BN + wm + 32 * n) * 16);
+    else if (n < MF + NF)
+      sw2[n - MF] = *(const int*)(p + (wn + 32 * (n - MF)) * 16);
   };
+  const std::integral_constant<int, 0> first;
+  const std::integral_constant<int, 1> second;
+  constexpr int FRAGS = NF + MF, PRODUCTS = NF * MF;
+  constexpr int TAKES = (FRAGS + PRODUCTS - 1) / PRODUCTS, COPIES = (SEGS + PRODUCTS - 1) / PRODUCTS;
   // Copies that may be on their way when step b + 1 has to be there: those of the
   // STAGES - 2 steps behind it.  Scales on their way only make the wait longer: they are
   // issued four steps before they are read, so at least that many copies are newer.
   constexpr int LEFT = (STAGES - 2) * SEGS;
   landed<LEFT + SEGS>();
-  take(0, 0, w0, x0);
-  take_scales(0, sw, sx);
+#pragma unroll
+  for (int n = 0; n < FRAGS; ++n) {
+    take(0, first, n);
+    take_scale(0, n);
+  }
   int buf = 0;
   for (int b = 0; b < kb; ++b) {
     const int next = buf + 1 < STAGES ? buf + 1 : 0;
-    take(buf, 1, w1, x1);
 #pragma unroll
-    for (int i = 0; i < NF; ++i) sw[i] >>= 16 * half;
+    for (int i = 0; i < NF; ++i) sw[i] = sw2[i] >> 16 * half;
 #pragma unroll
-    for (int j = 0; j < MF; ++j) sx[j] >>= 16 * half;
+    for (int j = 0; j < MF; ++j) sx[j] = sx2[j] >> 16 * half;
+    // The first half's products, and between them the reads for the second's.
 #pragma unroll
-    for (int i = 0; i < NF; ++i)
+    for (int p = 0; p < PRODUCTS; ++p) {
 #pragma unroll
-      for (int j = 0; j < MF; ++j) acc[i][j] = mfma64<0>(w0[i], x0[j], acc[i][j], sw[i], sx[j]);
+      for (int n = 0; n < TAKES; ++n) take(buf, second, p * TAKES + n);
+      acc[p / MF][p % MF] = mfma64<0>(w[0][p / MF], x[0][p % MF], acc[p / MF][p % MF], sw[p / MF], sx[p % MF]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     // This wave holds all that it needs of this buffer and of these scales; once every
     // wave does, they are filled again.
     landed<LEFT>();
-    take(next, 0, w0, x0);
-    take_scales(b + 1, sw2, sx2);
-    if ((b & 3) == 3) fetch_scales((b >> 2) + 2);
-    fetch(b + STAGES, buf);
+    fetch_scales((b >> 2) + 2, (b & 3) == 3);
 #pragma unroll
-    for (int i = 0; i < NF; ++i)
+    for (int p = 0; p < PRODUCTS; ++p) {
 #pragma unroll
-      for (int j = 0; j < MF; ++j) acc[i][j] = mfma64<1>(w1[i], x1[j], acc[i][j], sw[i], sx[j]);
+      for (int n = 0; n < TAKES; ++n) {
+        take(next, first, p * TAKES + n);
+        take_scale(b + 1, p * TAKES + n);
+      }
 #pragma unroll
-    for (int i = 0; i < NF; ++i) sw[i] = sw2[i];
-#pragma unroll
-    for (int j = 0; j < MF; ++j) sx[j] = sx2[j];
+      for (int n = 0; n < COPIES; ++n) fetch(b + STAGES, buf, p * COPIES + n);
+      acc[p / MF][p % MF] = mfma64<1>(w[1][p / MF], x[1][p % MF], acc[p / MF][p % MF], sw[p / MF], sx[p % MF]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     buf = next;
   }
   landed<0>();  // the empty copies too, before the block's LDS is another's
@@ -289,7 +349,7 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
 #pragma unroll
   for (int j = 0; j < MF; ++j) {
     const int64_t row = m0 + wm + 32 * j + r;
-    const bool have = row < end;
+    const bool have = wm + 32 * j + r < rows;
     if constexpr (GATED) {
 #pragma unroll
       for (int i = 0; i < NF; i += 2)
@@ -339,8 +399,7 @@ MxArgs args_of(const MxGemm& g) {
   a.yp = mx_pitch(g.n);
   a.dh = g.dh;
   a.h = g.h;
-  const uintptr_t unit = g.y_type == QW_BF16 ? 8 : 16;
-  a.vec = g.n % 4 == 0 && aligned(g.y, unit) && aligned(g.h, unit);
+  a.vec = g.n % (g.y_type == QW_BF16 ? 8 : 4) == 0 && aligned(g.y, 16) && aligned(g.h, 16) && aligned(g.dh, 16);
   return a;
 }
 

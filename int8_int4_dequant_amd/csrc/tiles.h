@@ -8,6 +8,12 @@ namespace qw {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+// A value that all lanes of a wave have alike, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
+         (int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32;
+}
+
 // A buffer descriptor of `bytes` from `base`: reads beyond give zeros.
 __device__ __forceinline__ i32x4 buffer_of(const void* base, uint32_t bytes) {
   const uint64_t p = (uint64_t)base;
@@ -21,6 +27,14 @@ __device__ __forceinline__ void copy_to_lds(i32x4 buffer, uint32_t voff, uint32_
                                             uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :: "s"(lds), "v"(voff), "s"(buffer), "s"(soff) : "memory");
+}
+// The same where `when` (one value for the wave) is not zero.  The compiler sees no branch:
+// at one it would move the products before it behind it.
+__device__ __forceinline__ void copy_to_lds_when(int when, i32x4 buffer, uint32_t voff,
+                                                 uint32_t soff, uint32_t lds) {
+  asm volatile("s_cmp_eq_u32 %4, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\t"
+               "buffer_load_dwordx4 %1, %2, %3 offen lds\n.Lskip%=:"
+               :: "s"(lds), "v"(voff), "s"(buffer), "s"(soff), "s"(when) : "memory", "scc");
 }
 // The same, 4 bytes a lane.
 __device__ __forceinline__ void copy4_to_lds(i32x4 buffer, uint32_t voff, uint32_t soff,
