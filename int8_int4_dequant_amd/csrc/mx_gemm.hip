@@ -27,7 +27,7 @@ struct MxArgs {
   const uint8_t *w, *ws, *x, *xs;
   int64_t n, m;       // outputs in a row (gated: f), rows
   int64_t kp2, ksp;   // bytes of a row of codes, of scales
-  int kb;             // steps of 128 along k
+  int kb;             // steps of 256 along k
   void* y;
   uint8_t* ys;
   int64_t yp;         // MX_GATED_CODES: values in a row of codes
@@ -37,7 +37,7 @@ struct MxArgs {
   int vec;            // 16 bytes of outputs may be stored as one
 };
 
-// Step S of two: blocks 2 (l / 32) + S of a step of 128; the scales in byte S.
+// The scales are in byte S.
 template <int S>
 __device__ __forceinline__ f32x16 mfma64(i32x4 a, i32x4 b, f32x16 c, int sa, int sb) {
   const i32x8 a8 = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
@@ -178,14 +178,23 @@ __device__ __forceinline__ void store_gated(const MxArgs& a, f32x16 gate, f32x16
 
 // ---------------------------------------------------------------- tiled kernel
 //
-// A block of WN x WM waves, each with 32 NF weight rows x 32 MF tokens, 128 values of k
-// at a time through a ring of STAGES LDS buffers that copies straight from memory fill.
-// Scales are copied for four steps at once (16 bytes a row).
+// A block of WN x WM waves, each with 32 NF weight rows x 32 MF tokens, 256 values of k (a
+// step) at a time through a ring of STAGES LDS buffers that copies straight from memory
+// fill.  Scales are copied for four steps at once (32 bytes a row), into two buffers.
 //
-// LDS rows are the 64 bytes of a step.  A phase of a 16-byte LDS read is 16 lanes, here
-// 16 consecutive rows at the same place in the row, and the 64 banks hold 4 rows: piece c
-// of row r is kept at c ^ (r / 4 % 4), so that the 16 lanes meet 16 different places.  The
+// What bounds it: the copies take whole lines of 128 bytes, since the rate of requests is
+// what limits them (alone, 256 x 256 tiles of 4096 x 4096 x 16384: 64-byte rows of half the
+// step 0.51 us for 128 values of k, 128-byte rows 0.37; scales of 16 bytes a row 0.11 more).
+// The products alone take 0.50 us for it, 0.82 with values that are not zero: the clock
+// falls with the power that they draw.
+//
+// LDS rows are the 128 bytes of a step.  A phase of a 16-byte LDS read is 16 lanes, here
+// 16 consecutive rows at the same place in the row, and the 64 banks hold 2 rows: piece c
+// of row r is kept at c ^ (r / 2 % 8), so that the 16 lanes meet 16 different places.  The
 // copy writes LDS in lane order, so the lanes fetch the pieces in that order from memory.
+//
+// A step has four products a fragment; of the t-th, a lane holds block 4 (l / 32) + t, so
+// that byte t of one word of its row's scales goes with it.
 //
 // Gated results: the tile's rows are 32 gate rows and their 32 up rows in turn, so that a
 // lane holds both values of a result.
@@ -195,14 +204,12 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
   constexpr int WAVES = WN * WM, BN = 32 * NF * WN, BM = 32 * MF * WM, ROWS = BN + BM;
   constexpr bool GATED = RES != MX_STORE;
   constexpr int COLS = GATED ? BN / 2 : BN;        // outputs of a row in a tile
-  constexpr int SEGS = ROWS / 16 / WAVES;          // 16-row pieces of a wave
-  constexpr int SCALES = ROWS / 64;                // 64-row pieces of scales
-  constexpr int SPER = (SCALES + WAVES - 1) / WAVES;
-  static_assert(ROWS / 16 % WAVES == 0 && BN % 64 == 0 && BM % 64 == 0, "whole pieces");
+  constexpr int SEGS = ROWS / 8 / WAVES;           // 8-row pieces of a wave
+  constexpr int SPER = ROWS / 32 / WAVES;          // 32-row pieces of scales of a wave
+  static_assert(ROWS / 32 % WAVES == 0 && BN % 64 == 0 && BM % 64 == 0, "whole pieces");
   static_assert(!GATED || NF % 2 == 0, "gate and up rows in one wave");
-  static_assert(STAGES >= 3 && STAGES <= 6, "see the waits below");
-  __shared__ __align__(1024) uint8_t lds[STAGES][ROWS * 64];
-  __shared__ __align__(1024) uint8_t scales[2][ROWS * 16];
+  __shared__ __align__(1024) uint8_t lds[STAGES][ROWS * 128];
+  __shared__ __align__(1024) uint8_t scales[2][ROWS * 32];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
   const int wm = wave % WM * 32 * MF, wn = wave / WM * 32 * NF;
@@ -229,9 +236,9 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
 #pragma unroll
   for (int s = 0; s < SEGS; ++s) {
     const int seg = wave + WAVES * s;
-    from[s] = choose(seg >= BN / 16, GATED && seg / 2 % 2, a.x, a.w, a.kp2);
-    const int row = (wave + WAVES * s) * 16 + (lane >> 2);
-    const int c = (lane & 3) ^ ((row >> 2) & 3);
+    from[s] = choose(seg >= BN / 8, GATED && seg / 4 % 2, a.x, a.w, a.kp2);
+    const int row = seg * 8 + (lane >> 3);
+    const int c = (lane & 7) ^ ((row >> 1) & 7);
     const int at = row >= BN ? row - BN : weight_row(row);
     voff[s] = (uint32_t)at * (uint32_t)a.kp2 + c * 16;
   }
@@ -240,12 +247,10 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
 #pragma unroll
   for (int s = 0; s < SPER; ++s) {
     const int seg = wave + WAVES * s;
-    sfrom[s] = choose(seg >= BN / 64, false, a.xs, a.ws, a.ksp);
-    // gate and up rows in turn: in one buffer up to the last of the up rows
-    if (GATED && seg < BN / 64) sfrom[s].z = cols ? sfrom[s].z + (int)(uint32_t)(a.n * a.ksp) : 0;
-    const int row = seg * 64 + lane;
-    const int64_t at = row >= BN ? row - BN : weight_row(row) + (GATED && row / 32 % 2 ? a.n : 0);
-    soff[s] = (uint32_t)(at * a.ksp);
+    sfrom[s] = choose(seg >= BN / 32, GATED && seg % 2, a.xs, a.ws, a.ksp);
+    const int row = seg * 32 + (lane >> 1);
+    const int at = row >= BN ? row - BN : weight_row(row);
+    soff[s] = (uint32_t)at * (uint32_t)a.ksp + (lane & 1) * 16;
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0];
   const uint32_t lds1 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&scales[0][0];
@@ -257,7 +262,7 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
     const int seg = wave + WAVES * s;
     i32x4 buffer = from[s];
     buffer.z = in ? buffer.z : 0;
-    copy_to_lds(buffer, voff[s], in ? (uint32_t)b * 64 : 0, lds0 + buf * (ROWS * 64) + seg * 1024);
+    copy_to_lds(buffer, voff[s], in ? (uint32_t)b * 128 : 0, lds0 + buf * (ROWS * 128) + seg * 1024);
   };
   auto fetch_scales = [&](int u, bool when) {  // of steps 4 u .. 4 u + 3
     const bool in = 4 * u < kb;
@@ -266,8 +271,8 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
       const int seg = wave + WAVES * s;
       i32x4 buffer = sfrom[s];
       buffer.z = in ? buffer.z : 0;
-      copy_to_lds_when(__builtin_amdgcn_readfirstlane(when && seg < SCALES ? 1 : 0), buffer, soff[s], in ? (uint32_t)u * 16 : 0,
-                       lds1 + (u & 1) * (ROWS * 16) + seg * 1024);
+      copy_to_lds_when(__builtin_amdgcn_readfirstlane(when ? 1 : 0), buffer, soff[s],
+                       in ? (uint32_t)u * 32 : 0, lds1 + (u & 1) * (ROWS * 32) + seg * 1024);
     }
   };
   fetch_scales(0, true);
@@ -278,70 +283,80 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
     for (int s = 0; s < SEGS; ++s) fetch(b, b, s);
 
   f32x16 acc[NF][MF] = {};
-  i32x4 w[2][NF], x[2][MF];  // fragments of the two halves of a step
+  i32x4 w[2][NF], x[2][MF];  // fragments of two products
   int sw[NF], sx[MF], sw2[NF], sx2[MF];
-  const int swap = (r >> 2) & 3;  // the same for all rows a multiple of 32 apart
-  // Read N of the fragments of half S of the step in buffer `buf`: the first products' first.
-  auto take = [&](int buf, auto half_of, int n) {
-    constexpr int S = decltype(half_of)::value;
-    const uint8_t* p = &lds[buf][r * 64 + (((2 * half + S) ^ swap) << 4)];
+  const int swap = (r >> 1) & 7;  // the same for all rows a multiple of 32 apart
+  // Read N of the fragments of product Q of the step in buffer `buf`: the first ones' first.
+  auto take = [&](int buf, auto product, int n) {
+    constexpr int Q = decltype(product)::value;
+    const uint8_t* p = &lds[buf][r * 128 + (((4 * half + Q) ^ swap) << 4)];
     if (n < MF)
-      x[S][n] = *(const i32x4*)(p + (BN + wm + 32 * n) * 64);
+      x[Q & 1][n] = *(const i32x4*)(p + (BN + wm + 32 * n) * 128);
     else if (n < MF + NF)
-      w[S][n - MF] = *(const i32x4*)(p + (wn + 32 * (n - MF)) * 64);
+      w[Q & 1][n - MF] = *(const i32x4*)(p + (wn + 32 * (n - MF)) * 128);
   };
   auto take_scale = [&](int b, int n) {
-    const uint8_t* p = &scales[(b >> 2) & 1][r * 16 + (b & 3) * 4];
+    const uint8_t* p = &scales[(b >> 2) & 1][r * 32 + (b & 3) * 8 + 4 * half];
     if (n < MF)
-      sx2[n] = *(const int*)(p + (BN + wm + 32 * n) * 16);
+      sx2[n] = *(const int*)(p + (BN + wm + 32 * n) * 32);
     else if (n < MF + NF)
-      sw2[n - MF] = *(const int*)(p + (wn + 32 * (n - MF)) * 16);
+      sw2[n - MF] = *(const int*)(p + (wn + 32 * (n - MF)) * 32);
   };
-  const std::integral_constant<int, 0> first;
-  const std::integral_constant<int, 1> second;
   constexpr int FRAGS = NF + MF, PRODUCTS = NF * MF;
   constexpr int TAKES = (FRAGS + PRODUCTS - 1) / PRODUCTS, COPIES = (SEGS + PRODUCTS - 1) / PRODUCTS;
   // Copies that may be on their way when step b + 1 has to be there: those of the
-  // STAGES - 2 steps behind it.  Scales on their way only make the wait longer: they are
-  // issued four steps before they are read, so at least that many copies are newer.
+  // STAGES - 2 steps behind it.  Scales are issued before the copies of their step and four
+  // steps ahead of their use: they only make the wait longer.
   constexpr int LEFT = (STAGES - 2) * SEGS;
+  static_assert(STAGES >= 2 && STAGES <= 4, "scales have landed by then");
   landed<LEFT + SEGS>();
 #pragma unroll
   for (int n = 0; n < FRAGS; ++n) {
-    take(0, first, n);
+    take(0, std::integral_constant<int, 0>{}, n);
     take_scale(0, n);
   }
   int buf = 0;
   for (int b = 0; b < kb; ++b) {
     const int next = buf + 1 < STAGES ? buf + 1 : 0;
 #pragma unroll
-    for (int i = 0; i < NF; ++i) sw[i] = sw2[i] >> 16 * half;
+    for (int i = 0; i < NF; ++i) sw[i] = sw2[i];
 #pragma unroll
-    for (int j = 0; j < MF; ++j) sx[j] = sx2[j] >> 16 * half;
-    // The first half's products, and between them the reads for the second's.
+    for (int j = 0; j < MF; ++j) sx[j] = sx2[j];
+    // Product Q of all fragments, and between them what comes next.
+    auto products = [&](auto product, auto between) {
+      constexpr int Q = decltype(product)::value;
 #pragma unroll
-    for (int p = 0; p < PRODUCTS; ++p) {
+      for (int p = 0; p < PRODUCTS; ++p) {
+        between(p);
+        acc[p / MF][p % MF] = mfma64<Q>(w[Q & 1][p / MF], x[Q & 1][p % MF], acc[p / MF][p % MF],
+                                        sw[p / MF], sx[p % MF]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    auto with_reads = [&](auto product) {
+      constexpr int Q = decltype(product)::value;
+      products(product, [&](int p) {
 #pragma unroll
-      for (int n = 0; n < TAKES; ++n) take(buf, second, p * TAKES + n);
-      acc[p / MF][p % MF] = mfma64<0>(w[0][p / MF], x[0][p % MF], acc[p / MF][p % MF], sw[p / MF], sx[p % MF]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+        for (int n = 0; n < TAKES; ++n)
+          take(buf, std::integral_constant<int, Q + 1>{}, p * TAKES + n);
+      });
+    };
+    with_reads(std::integral_constant<int, 0>{});
+    with_reads(std::integral_constant<int, 1>{});
+    with_reads(std::integral_constant<int, 2>{});
     // This wave holds all that it needs of this buffer and of these scales; once every
     // wave does, they are filled again.
     landed<LEFT>();
     fetch_scales((b >> 2) + 2, (b & 3) == 3);
-#pragma unroll
-    for (int p = 0; p < PRODUCTS; ++p) {
-#pragma unroll
-      for (int n = 0; n < TAKES; ++n) {
-        take(next, first, p * TAKES + n);
-        take_scale(b + 1, p * TAKES + n);
-      }
+    products(std::integral_constant<int, 3>{}, [&](int p) {
 #pragma unroll
       for (int n = 0; n < COPIES; ++n) fetch(b + STAGES, buf, p * COPIES + n);
-      acc[p / MF][p % MF] = mfma64<1>(w[1][p / MF], x[1][p % MF], acc[p / MF][p % MF], sw[p / MF], sx[p % MF]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+#pragma unroll
+      for (int n = 0; n < TAKES; ++n) {
+        take(next, std::integral_constant<int, 0>{}, p * TAKES + n);
+        take_scale(b + 1, p * TAKES + n);
+      }
+    });
     buf = next;
   }
   landed<0>();  // the empty copies too, before the block's LDS is another's
@@ -393,7 +408,7 @@ MxArgs args_of(const MxGemm& g) {
   a.m = g.m;
   a.kp2 = kp / 2;
   a.ksp = kp / 32;
-  a.kb = (int)((g.k + 127) / 128);
+  a.kb = (int)((g.k + 255) / 256);
   a.y = g.y;
   a.ys = g.ys;
   a.yp = mx_pitch(g.n);
@@ -409,9 +424,9 @@ hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t stream) {
   const MxArgs a = args_of(g);
   const int64_t rows = g.result == MX_STORE ? g.n : 2 * g.n;
   auto tiles = [&](int t) { return ((g.m + t - 1) / t) * ((rows + t - 1) / t); };
-  if (tiles(256) >= 256 || tiles(64) > 1 << 22) return run_tiled<4, 2, 2, 4, 4>(a, g, stream);
-  if (tiles(128) >= 256) return run_tiled<2, 2, 2, 2, 4>(a, g, stream);
-  return run_tiled<2, 1, 1, 2, 4>(a, g, stream);
+  if (tiles(256) >= 256 || tiles(64) > 1 << 22) return run_tiled<4, 2, 2, 4, 2>(a, g, stream);
+  if (tiles(128) >= 256) return run_tiled<2, 2, 2, 2, 2>(a, g, stream);
+  return run_tiled<2, 1, 1, 2, 3>(a, g, stream);
 }
 
 }  // namespace qw
