@@ -196,6 +196,11 @@ __device__ __forceinline__ void store_gated(const MxArgs& a, f32x16 gate, f32x16
 // A step has four products a fragment; of the t-th, a lane holds block 4 (l / 32) + t, so
 // that byte t of one word of its row's scales goes with it.
 //
+// A block takes tile after tile (in steps of the grid) and the copies run on: behind the
+// last step of a tile come the first ones of the next, which are on their way while the
+// results are written.  `chunks` of 4 steps and the two buffers of their scales are counted
+// through in the same way.
+//
 // Gated results: the tile's rows are 32 gate rows and their 32 up rows in turn, so that a
 // lane holds both values of a result.
 
@@ -213,68 +218,86 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
   const int wm = wave % WM * 32 * MF, wn = wave / WM * 32 * NF;
-  int64_t tm, tn;
-  tile_place(blockIdx.x, a.tiles, a.tiles_m, tm, tn);
-  const int64_t n0 = uniform(tn) * COLS, m0 = uniform(tm) * BM;
-  const int rows = __builtin_amdgcn_readfirstlane((int)min(a.m - m0, (int64_t)BM));
-  // behind the last output there is nothing: only padding of a row of codes
-  const int cols = __builtin_amdgcn_readfirstlane((int)max((int64_t)0, min(a.n - n0, (int64_t)COLS)));
-  const int kb = cols ? a.kb : 0;
   // the weight row (of gate or up) that LDS row `row` holds
   auto weight_row = [](int row) {
     const int at = GATED ? row / 64 * 32 + row % 32 : row;
     return kSwapped<RES, T> ? swapped(at) : at;
   };
-  // each piece's buffer, of which its rows behind the last one are not a part
-  auto choose = [&](bool of_x, bool up, const uint8_t* xbase, const uint8_t* wbase, int64_t bytes) {
-    const int64_t size = of_x ? rows * bytes : cols * bytes;
-    return buffer_of((const uint8_t*)uniform((int64_t)(of_x ? xbase + m0 * bytes : wbase + (n0 + (up ? a.n : 0)) * bytes)),
-                     __builtin_amdgcn_readfirstlane((uint32_t)size));
-  };
-  uint32_t voff[SEGS];
-  i32x4 from[SEGS];
+  uint32_t voff[SEGS], soff[SPER];
 #pragma unroll
   for (int s = 0; s < SEGS; ++s) {
-    const int seg = wave + WAVES * s;
-    from[s] = choose(seg >= BN / 8, GATED && seg / 4 % 2, a.x, a.w, a.kp2);
-    const int row = seg * 8 + (lane >> 3);
+    const int row = (wave + WAVES * s) * 8 + (lane >> 3);
     const int c = (lane & 7) ^ ((row >> 1) & 7);
     const int at = row >= BN ? row - BN : weight_row(row);
     voff[s] = (uint32_t)at * (uint32_t)a.kp2 + c * 16;
   }
-  uint32_t soff[SPER];
-  i32x4 sfrom[SPER];
 #pragma unroll
   for (int s = 0; s < SPER; ++s) {
-    const int seg = wave + WAVES * s;
-    sfrom[s] = choose(seg >= BN / 32, GATED && seg % 2, a.xs, a.ws, a.ksp);
-    const int row = seg * 32 + (lane >> 1);
+    const int row = (wave + WAVES * s) * 32 + (lane >> 1);
     const int at = row >= BN ? row - BN : weight_row(row);
     soff[s] = (uint32_t)at * (uint32_t)a.ksp + (lane & 1) * 16;
   }
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0];
-  const uint32_t lds1 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&scales[0][0];
-  // Behind the last step there is nothing to read, but the copy is issued all the same
-  // (as zeros, from an empty buffer), so that every step has as many.
-  auto fetch = [&](int b, int buf, int s) {
-    if (s >= SEGS) return;
-    const bool in = b < kb;
-    const int seg = wave + WAVES * s;
-    i32x4 buffer = from[s];
-    buffer.z = in ? buffer.z : 0;
-    copy_to_lds(buffer, voff[s], in ? (uint32_t)b * 128 : 0, lds0 + buf * (ROWS * 128) + seg * 1024);
+  // A tile, and each piece's buffer, of which the rows behind the last one are not a part.
+  struct Place {
+    int64_t n0, m0;
+    int rows;
+    i32x4 from[SEGS], sfrom[SPER];
   };
-  auto fetch_scales = [&](int u, bool when) {  // of steps 4 u .. 4 u + 3
-    const bool in = 4 * u < kb;
+  auto place = [&](int64_t tile, Place& p) {
+    int64_t tm, tn;
+    const bool there = tile < a.tiles;
+    tile_place(there ? tile : 0, a.tiles, a.tiles_m, tm, tn);
+    p.n0 = uniform(tn) * COLS;
+    p.m0 = uniform(tm) * BM;
+    p.rows = __builtin_amdgcn_readfirstlane(there ? (int)min(a.m - p.m0, (int64_t)BM) : 0);
+    // behind the last output (padding of a row of codes) there are no weight rows
+    const int cols = __builtin_amdgcn_readfirstlane(there ? (int)max((int64_t)0, min(a.n - p.n0, (int64_t)COLS)) : 0);
+    auto choose = [&](bool of_x, bool up, const uint8_t* xbase, const uint8_t* wbase, int64_t bytes) {
+      return buffer_of((const uint8_t*)uniform((int64_t)(of_x ? xbase + p.m0 * bytes : wbase + (p.n0 + (up ? a.n : 0)) * bytes)),
+                       __builtin_amdgcn_readfirstlane((uint32_t)((of_x ? p.rows : cols) * bytes)));
+    };
+#pragma unroll
+    for (int s = 0; s < SEGS; ++s) {
+      const int seg = wave + WAVES * s;
+      p.from[s] = choose(seg >= BN / 8, GATED && seg / 4 % 2, a.x, a.w, a.kp2);
+    }
 #pragma unroll
     for (int s = 0; s < SPER; ++s) {
       const int seg = wave + WAVES * s;
-      i32x4 buffer = sfrom[s];
-      buffer.z = in ? buffer.z : 0;
-      copy_to_lds_when(__builtin_amdgcn_readfirstlane(when ? 1 : 0), buffer, soff[s],
-                       in ? (uint32_t)u * 32 : 0, lds1 + (u & 1) * (ROWS * 32) + seg * 1024);
+      p.sfrom[s] = choose(seg >= BN / 32, GATED && seg % 2, a.xs, a.ws, a.ksp);
     }
   };
+  const int kb = a.kb, chunks = (kb + 3) >> 2;
+  Place here, then;
+  place(blockIdx.x, here);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0];
+  const uint32_t lds1 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&scales[0][0];
+  // Behind the last tile there is nothing to read, but the copy is issued all the same (as
+  // zeros, from an empty buffer), so that every step has as many.
+  auto fetch = [&](int b, int buf, int s) {
+    if (s >= SEGS) return;
+    const bool in = b < kb;
+    i32x4 buffer = here.from[s];
+#pragma unroll
+    for (int c = 0; c < 3; ++c) buffer[c] = in ? buffer[c] : then.from[s][c];
+    copy_to_lds(buffer, voff[s], (uint32_t)(in ? b : b - kb) * 128,
+                lds0 + buf * (ROWS * 128) + (wave + WAVES * s) * 1024);
+  };
+  int base = 0;  // which of the two buffers holds the tile's first scales
+  auto fetch_scales = [&](int u, bool when) {  // of steps 4 u .. 4 u + 3
+    const bool in = u < chunks;
+#pragma unroll
+    for (int s = 0; s < SPER; ++s) {
+      i32x4 buffer = here.sfrom[s];
+#pragma unroll
+      for (int c = 0; c < 3; ++c) buffer[c] = in ? buffer[c] : then.sfrom[s][c];
+      copy_to_lds_when(__builtin_amdgcn_readfirstlane(when ? 1 : 0), buffer, soff[s],
+                       (uint32_t)(in ? u : u - chunks) * 32,
+                       lds1 + ((base + u) & 1) * (ROWS * 32) + (wave + WAVES * s) * 1024);
+    }
+  };
+  int64_t tile = blockIdx.x + gridDim.x;
+  place(tile, then);
   fetch_scales(0, true);
   fetch_scales(1, true);
 #pragma unroll
@@ -282,7 +305,6 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
 #pragma unroll
     for (int s = 0; s < SEGS; ++s) fetch(b, b, s);
 
-  f32x16 acc[NF][MF] = {};
   i32x4 w[2][NF], x[2][MF];  // fragments of two products
   int sw[NF], sx[MF], sw2[NF], sx2[MF];
   const int swap = (r >> 1) & 7;  // the same for all rows a multiple of 32 apart
@@ -296,7 +318,8 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
       w[Q & 1][n - MF] = *(const i32x4*)(p + (wn + 32 * (n - MF)) * 128);
   };
   auto take_scale = [&](int b, int n) {
-    const uint8_t* p = &scales[(b >> 2) & 1][r * 32 + (b & 3) * 8 + 4 * half];
+    const int u = b < kb ? b >> 2 : chunks, in = b < kb ? b & 3 : 0;  // behind the last: the next tile's first
+    const uint8_t* p = &scales[(base + u) & 1][r * 32 + in * 8 + 4 * half];
     if (n < MF)
       sx2[n] = *(const int*)(p + (BN + wm + 32 * n) * 32);
     else if (n < MF + NF)
@@ -316,6 +339,8 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
     take_scale(0, n);
   }
   int buf = 0;
+  for (;;) {
+  f32x16 acc[NF][MF] = {};
   for (int b = 0; b < kb; ++b) {
     const int next = buf + 1 < STAGES ? buf + 1 : 0;
 #pragma unroll
@@ -347,7 +372,7 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
     // This wave holds all that it needs of this buffer and of these scales; once every
     // wave does, they are filled again.
     landed<LEFT>();
-    fetch_scales((b >> 2) + 2, (b & 3) == 3);
+    fetch_scales((b >> 2) + 2, (b & 3) == 3 || b + 1 == kb);
     products(std::integral_constant<int, 3>{}, [&](int p) {
 #pragma unroll
       for (int n = 0; n < COPIES; ++n) fetch(b + STAGES, buf, p * COPIES + n);
@@ -359,33 +384,44 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
     });
     buf = next;
   }
-  landed<0>();  // the empty copies too, before the block's LDS is another's
-
 #pragma unroll
   for (int j = 0; j < MF; ++j) {
-    const int64_t row = m0 + wm + 32 * j + r;
-    const bool have = wm + 32 * j + r < rows;
+    const int64_t row = here.m0 + wm + 32 * j + r;
+    const bool have = wm + 32 * j + r < here.rows;
     if constexpr (GATED) {
 #pragma unroll
       for (int i = 0; i < NF; i += 2)
-        store_gated<RES, T>(a, acc[i][j], acc[i + 1][j], row, n0 + (wn + 32 * i) / 2, half, have);
+        store_gated<RES, T>(a, acc[i][j], acc[i + 1][j], row, here.n0 + (wn + 32 * i) / 2, half, have);
     } else {
       if (!have) continue;
 #pragma unroll
-      for (int i = 0; i < NF; ++i) store_fragment<T>(a, acc[i][j], row, n0 + wn + 32 * i, half);
+      for (int i = 0; i < NF; ++i) store_fragment<T>(a, acc[i][j], row, here.n0 + wn + 32 * i, half);
     }
   }
+  if (tile >= a.tiles) break;
+  here = then;
+  base += chunks;
+  tile += gridDim.x;
+  place(tile, then);
+  }
+  landed<0>();  // the empty copies too, before the block's LDS is another's
 }
 
-template <int NF, int MF, int WN, int WM, int STAGES>
+constexpr int kUnits = 256;  // compute units
+
+// PER_UNIT: blocks that a compute unit holds.
+template <int NF, int MF, int WN, int WM, int STAGES, int PER_UNIT>
 hipError_t run_tiled(MxArgs a, const MxGemm& g, hipStream_t stream) {
   constexpr int BN = 32 * NF * WN, BM = 32 * MF * WM;
   const int cols = g.result == MX_STORE ? BN : BN / 2;
   a.tiles_m = (a.m + BM - 1) / BM;
   a.tiles = a.tiles_m * (((g.result == MX_GATED_CODES ? a.yp : a.n) + cols - 1) / cols);
+  // Tile after tile where there are more than the units hold; copies that run on into the
+  // next tile need two chunks of scales in each.
+  const unsigned grid = (unsigned)(a.kb > 4 ? std::min<int64_t>(a.tiles, kUnits * PER_UNIT) : a.tiles);
   auto go = [&](auto result, auto type) {
     mx_tiled<NF, MF, WN, WM, STAGES, decltype(result)::value, decltype(type)>
-        <<<(unsigned)a.tiles, WN * WM * 64, 0, stream>>>(a);
+        <<<grid, WN * WM * 64, 0, stream>>>(a);
   };
   auto typed = [&](auto result) { g.y_type == QW_F32 ? go(result, 0.0f) : go(result, uint16_t{}); };
   switch (g.result) {
@@ -424,9 +460,9 @@ hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t stream) {
   const MxArgs a = args_of(g);
   const int64_t rows = g.result == MX_STORE ? g.n : 2 * g.n;
   auto tiles = [&](int t) { return ((g.m + t - 1) / t) * ((rows + t - 1) / t); };
-  if (tiles(256) >= 256 || tiles(64) > 1 << 22) return run_tiled<4, 2, 2, 4, 2>(a, g, stream);
-  if (tiles(128) >= 256) return run_tiled<2, 2, 2, 2, 2>(a, g, stream);
-  return run_tiled<2, 1, 1, 2, 3>(a, g, stream);
+  if (tiles(256) >= 256 || tiles(64) > 1 << 22) return run_tiled<2, 4, 4, 2, 2, 1>(a, g, stream);
+  if (tiles(128) >= 256) return run_tiled<2, 2, 2, 2, 2, 2>(a, g, stream);
+  return run_tiled<2, 1, 1, 2, 3, 2>(a, g, stream);
 }
 
 }  // namespace qw
