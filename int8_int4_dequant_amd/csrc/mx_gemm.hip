@@ -25,7 +25,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 struct MxArgs {
   const uint8_t *w, *ws, *x, *xs;
-  int64_t n, m;       // outputs in a row (gated: f), rows
+  const void* xfloat; // stream kernel: float rows
+  int64_t n, m, k;    // outputs of a row in this launch (gated: f), rows, values of a row of x
+  int64_t ldy;        // outputs in a row of y
   int64_t kp2, ksp;   // bytes of a row of codes, of scales
   int kb;             // steps of 256 along k
   void* y;
@@ -34,7 +36,6 @@ struct MxArgs {
   const void* dh;
   void* h;
   int64_t tiles_m, tiles;
-  int vec;            // 16 bytes of outputs may be stored as one
 };
 
 // The scales are in byte S.
@@ -66,13 +67,15 @@ template <typename T> struct Runs {
   static __device__ __forceinline__ int at(int g, int half) { return 2 * RUN * g + RUN * half; }
 };
 
+// 16 bytes at the alignment of an element, which the hardware splits where it has to: rows
+// of any length take them.
 template <int RUN, typename T>
-__device__ __forceinline__ void put(T* p, const float* v, int64_t left, bool vec) {
-  if (vec && left >= RUN) {
+__device__ __forceinline__ void put(T* p, const float* v, int64_t left) {
+  if (left >= RUN) {
     if constexpr (RUN == 8)
-      store8<true>(p, v);
+      store8<false>(p, v);
     else
-      store4(p, f32x4{v[0], v[1], v[2], v[3]});
+      *(f32x4_u*)p = f32x4_u{v[0], v[1], v[2], v[3]};
   } else {
 #pragma unroll
     for (int c = 0; c < RUN; ++c)
@@ -80,12 +83,12 @@ __device__ __forceinline__ void put(T* p, const float* v, int64_t left, bool vec
   }
 }
 template <int RUN, typename T>
-__device__ __forceinline__ void get(const T* p, float* v, int64_t left, bool vec) {
-  if (vec && left >= RUN) {
+__device__ __forceinline__ void get(const T* p, float* v, int64_t left) {
+  if (left >= RUN) {
     if constexpr (RUN == 8) {
-      load8<true>(p, v);
+      load8<false>(p, v);
     } else {
-      const f32x4 t = *(const f32x4*)p;
+      const f32x4_u t = *(const f32x4_u*)p;
 #pragma unroll
       for (int c = 0; c < RUN; ++c) v[c] = t[c];
     }
@@ -121,7 +124,7 @@ __device__ __forceinline__ void store_fragment(const MxArgs& a, f32x16 v, int64_
     float o[R::RUN];
 #pragma unroll
     for (int c = 0; c < R::RUN; ++c) o[c] = v[R::RUN * g + c];
-    put<R::RUN>((T*)a.y + row * a.n + col, o, a.n - col, a.vec);
+    put<R::RUN>((T*)a.y + row * a.ldy + col, o, a.n - col);
   }
 }
 
@@ -137,13 +140,13 @@ __device__ __forceinline__ void store_gated(const MxArgs& a, f32x16 gate, f32x16
       const int64_t col = col0 + R::at(g, half), left = a.n - col;
       if (left <= 0) continue;
       float dh[RUN], dg[RUN], du[RUN], h[RUN];
-      get<RUN>((const T*)a.dh + row * a.n + col, dh, left, a.vec);
+      get<RUN>((const T*)a.dh + row * a.n + col, dh, left);
 #pragma unroll
       for (int c = 0; c < RUN; ++c)
         gate_gradients(gate[RUN * g + c], up[RUN * g + c], dh[c], dg[c], du[c], h[c]);
-      put<RUN>((T*)a.y + row * 2 * a.n + col, dg, left, a.vec);
-      put<RUN>((T*)a.y + row * 2 * a.n + a.n + col, du, left, a.vec);
-      if (a.h) put<RUN>((T*)a.h + row * a.n + col, h, left, a.vec);
+      put<RUN>((T*)a.y + row * 2 * a.n + col, dg, left);
+      put<RUN>((T*)a.y + row * 2 * a.n + a.n + col, du, left);
+      if (a.h) put<RUN>((T*)a.h + row * a.n + col, h, left);
     }
   } else {
     float v[16], p[16], q[16];
@@ -158,7 +161,7 @@ __device__ __forceinline__ void store_gated(const MxArgs& a, f32x16 gate, f32x16
 #pragma unroll
       for (int g = 0; g < 16 / RUN; ++g) {
         const int64_t col = col0 + R::at(g, half);
-        put<RUN>((T*)a.y + row * a.n + col, v + RUN * g, a.n - col, a.vec);
+        put<RUN>((T*)a.y + row * a.n + col, v + RUN * g, a.n - col);
       }
     } else {
       // The 32 values are one block: half of them in the lane 32 away.
@@ -210,8 +213,8 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
   constexpr bool GATED = RES != MX_STORE;
   constexpr int COLS = GATED ? BN / 2 : BN;        // outputs of a row in a tile
   constexpr int SEGS = ROWS / 8 / WAVES;           // 8-row pieces of a wave
-  constexpr int SPER = ROWS / 32 / WAVES;          // 32-row pieces of scales of a wave
-  static_assert(ROWS / 32 % WAVES == 0 && BN % 64 == 0 && BM % 64 == 0, "whole pieces");
+  constexpr int SPER = (ROWS / 32 + WAVES - 1) / WAVES;  // 32-row pieces of scales of a wave
+  static_assert(ROWS / 8 % WAVES == 0 && BN % 64 == 0 && BM % 32 == 0, "whole pieces");
   static_assert(!GATED || NF % 2 == 0, "gate and up rows in one wave");
   __shared__ __align__(1024) uint8_t lds[STAGES][ROWS * 128];
   __shared__ __align__(1024) uint8_t scales[2][ROWS * 32];
@@ -291,7 +294,7 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
       i32x4 buffer = here.sfrom[s];
 #pragma unroll
       for (int c = 0; c < 3; ++c) buffer[c] = in ? buffer[c] : then.sfrom[s][c];
-      copy_to_lds_when(__builtin_amdgcn_readfirstlane(when ? 1 : 0), buffer, soff[s],
+      copy_to_lds_when(__builtin_amdgcn_readfirstlane(when && wave + WAVES * s < ROWS / 32 ? 1 : 0), buffer, soff[s],
                        (uint32_t)(in ? u : u - chunks) * 32,
                        lds1 + ((base + u) & 1) * (ROWS * 32) + (wave + WAVES * s) * 1024);
     }
@@ -440,8 +443,10 @@ MxArgs args_of(const MxGemm& g) {
   a.ws = g.scales;
   a.x = g.xc;
   a.xs = g.xs;
-  a.n = g.n;
+  a.n = a.ldy = g.n;
   a.m = g.m;
+  a.k = g.k;
+  a.xfloat = g.x;
   a.kp2 = kp / 2;
   a.ksp = kp / 32;
   a.kb = (int)((g.k + 255) / 256);
@@ -450,19 +455,341 @@ MxArgs args_of(const MxGemm& g) {
   a.yp = mx_pitch(g.n);
   a.dh = g.dh;
   a.h = g.h;
-  a.vec = g.n % (g.y_type == QW_BF16 ? 8 : 4) == 0 && aligned(g.y, 16) && aligned(g.h, 16) && aligned(g.dh, 16);
   return a;
+}
+
+// ---------------------------------------------------------------- stream kernel
+//
+// For up to 16 MT rows of x: bound by reading the weight once.  A block takes 16 weight rows
+// (gated: 16 gate and their 16 up rows) after 16 weight rows; its 8 waves share k, each
+// with U consecutive units of 512 values, one line of scales a row and unit.  A wave
+// quantizes (or loads) its part of x once and keeps it in registers; a unit of the weight is
+// replaced by a later one as soon as its products are issued, so that RING units (4.3 KiB
+// each) are always on their way.  The waves' sums meet in LDS, once for 16 weight rows.
+//
+// v_mfma_scale_f32_16x16x128_f8f6f4: lane l holds row l % 16 and, with q = l / 16, one block
+// of 32; of product t of a unit's four, block 4 t + q, whose scale is byte q of word t.
+
+constexpr int kStreamWaves = 8;
+
+// What x is: rows of float values, or codes (x and xs).
+template <typename XT> struct is_codes { static constexpr bool value = false; };
+template <> struct is_codes<uint8_t> { static constexpr bool value = true; };
+
+__device__ __forceinline__ f32x4 mfma128(i32x4 a, i32x4 b, f32x4 c, int sa, int sb) {
+  const i32x8 a8 = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+  const i32x8 b8 = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, sa, 0, sb);
+}
+
+// This wave's units of float x as fragments and their scales (in byte 0): the 64 lanes
+// quantize a unit of a row, 8 values each, as quantize_rows does, up to 4 rows at a time; the
+// codes change lanes through LDS of the wave's own.
+template <int U, bool VEC, typename XT>
+__device__ __forceinline__ void quantize_part(const MxArgs& a, int unit0, uint8_t (*codes)[272],
+                                              int lane, i32x4 (*xf)[4], int (*sx)[4]) {
+  const int r = lane & 15, q = lane >> 4, m = (int)a.m;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t j = (int64_t)(unit0 + u) * 512 + lane * 8;
+    for (int row = 0; row < m; row += 4) {
+      float v[4][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load8_of_row<VEC>((const XT*)a.xfloat + min(row + i, m - 1) * a.k, j, a.k, v[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t s = mx_scale(top_among<4>(top_of<8>(v[i])));
+        const uint32_t c = mx_codes8(v[i], s);
+        if (row + i < m) {
+          *(uint32_t*)&codes[row + i][lane * 4] = c;
+          if ((lane & 3) == 0) codes[row + i][256 + (lane >> 2)] = (uint8_t)s;
+        }
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own writes, by other lanes
+#pragma unroll
+    for (int t = 0; t < 4; ++t) xf[u][t] = *(const i32x4*)&codes[r][(4 * t + q) * 16];
+    const i32x4 s = *(const i32x4*)&codes[r][256];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) sx[u][t] = s[t] >> 8 * q;
+  }
+}
+
+template <int U, int MT, bool GATED, bool VEC, typename XT, typename T>
+__global__ __launch_bounds__(kStreamWaves * 64, 2) void mx_stream(MxArgs a) {
+  constexpr int H = GATED ? 2 : 1;  // weight rows of an output
+  constexpr int RING = U > 4 || (GATED && U > 3) ? 2 : U;  // what the registers hold
+  constexpr int BUFS = MT == 1 ? 2 : 1;
+  static_assert(U % RING == 0, "the next tile's units take the places of this one's");
+  __shared__ __align__(16) float part[BUFS][kStreamWaves][H][16 * MT][20];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int units = (int)(a.kp2 / 256), unit0 = wave * U;
+  const int64_t tiles_n = (a.n + 15) / 16;
+  i32x4 w[RING][H][4], ws[RING][H];
+  // Unit u of the tile; behind the last unit, and behind the last row, the last one again.
+  auto load = [&](int64_t tile, int u) {
+    const int64_t at = min(unit0 + u, units - 1);
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const int64_t row = min(tile * 16 + r, a.n - 1) + (h ? a.n : 0);
+      const uint8_t* p = a.w + row * a.kp2 + at * 256 + q * 16;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) w[u % RING][h][t] = *(const i32x4*)(p + 64 * t);
+      ws[u % RING][h] = *(const i32x4*)(a.ws + row * a.ksp + at * 16);
+    }
+  };
+  int64_t tile = blockIdx.x;
+#pragma unroll
+  for (int u = 0; u < RING; ++u) load(tile, u);
+  i32x4 xf[MT][U][4];
+  int sx[MT][U][4];
+  if constexpr (is_codes<XT>::value) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      const int64_t row = min((int64_t)(16 * j + r), a.m - 1);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t at = min(unit0 + u, units - 1);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          xf[j][u][t] = *(const i32x4*)(a.x + row * a.kp2 + at * 256 + t * 64 + q * 16);
+        const i32x4 s = *(const i32x4*)(a.xs + row * a.ksp + at * 16);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) sx[j][u][t] = s[t] >> 8 * q;
+      }
+    }
+  } else {
+    static_assert(MT == 1, "float rows: 16 at most");
+    __shared__ __align__(16) uint8_t codes[kStreamWaves][16][272];
+    quantize_part<U, VEC, XT>(a, unit0, codes[wave], lane, xf[0], sx[0]);
+  }
+  // a row or a unit that is not there counts nothing, whatever was read in its place
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (16 * j + r >= (int)a.m || unit0 + u >= units) {
+          xf[j][u][t] = i32x4{};
+          sx[j][u][t] = 127;
+        }
+  int buf = 0;
+  auto step = [&](auto more) {
+    constexpr bool MORE = decltype(more)::value;  // a tile after this one
+    f32x4 acc[H][MT] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int s = unit0 + u < units ? ws[u % RING][h][t] >> 8 * q : 127;
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+            acc[h][j] = mfma128(w[u % RING][h][t], xf[j][u][t], acc[h][j], s, sx[j][u][t]);
+        }
+      if (u + RING < U)
+        load(tile, u + RING);
+      else if (MORE)
+        load(tile + gridDim.x, u + RING - U);
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) *(f32x4*)&part[buf][wave][h][16 * j + r][4 * q] = acc[h][j];
+    // The weight's loads stay on their way.  With two buffers one barrier a tile: the other
+    // one is written next, and read no later than the next barrier.
+    lds_barrier();
+    for (int o = threadIdx.x; o < 256 * MT; o += kStreamWaves * 64) {
+      const int t = o >> 4, c = o & 15;
+      const int64_t col = tile * 16 + c;
+      if (t < (int)a.m && col < a.n) {
+        float sum[H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          sum[h] = part[buf][0][h][t][c];
+#pragma unroll
+          for (int v = 1; v < kStreamWaves; ++v) sum[h] += part[buf][v][h][t][c];
+        }
+        float out = sum[0];
+        if constexpr (GATED) gated<1>(&sum[0], &sum[1], &out);
+        store1((T*)a.y + t * a.ldy + col, out);
+      }
+    }
+    if (BUFS == 1 && MORE) lds_barrier();
+    buf = BUFS - 1 - buf;
+  };
+  for (; tile + gridDim.x < tiles_n; tile += gridDim.x) step(std::true_type{});
+  step(std::false_type{});
+}
+
+template <int U, int MT, bool GATED, bool VEC, typename XT>
+hipError_t run_stream(const MxArgs& a, const MxGemm& g, hipStream_t stream) {
+  const int64_t tiles_n = (a.n + 15) / 16;
+  // two blocks a compute unit where the registers allow it
+  const unsigned grid = (unsigned)std::min<int64_t>(tiles_n, kUnits * (U * (GATED ? 2 : 1) * MT <= 2 ? 2 : 1));
+  if (g.y_type == QW_F32)
+    mx_stream<U, MT, GATED, VEC, XT, float><<<grid, kStreamWaves * 64, 0, stream>>>(a);
+  else
+    mx_stream<U, MT, GATED, VEC, XT, uint16_t><<<grid, kStreamWaves * 64, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+// Units of 512 that each of the waves takes of k.
+int units_of_wave(int64_t k) { return (int)((mx_pitch(k) / 512 + kStreamWaves - 1) / kStreamWaves); }
+
+// The most units of a wave that the stream kernel takes, for MT times 16 rows of x: they stay
+// in registers, and the weight's ring beside them.
+template <int MT, bool GATED>
+constexpr int kMostUnits = MT == 1 ? (GATED ? 4 : 6) : MT == 2 ? (GATED ? 2 : 3) : GATED ? 1 : 2;
+
+template <int MT, bool GATED, bool VEC, typename XT>
+hipError_t run_stream(const MxArgs& a, const MxGemm& g, hipStream_t stream) {
+  constexpr int MOST = kMostUnits<MT, GATED>;
+  const int each = units_of_wave(g.k);
+  if (each <= 1) return run_stream<1, MT, GATED, VEC, XT>(a, g, stream);
+  if constexpr (MOST >= 2)
+    if (each <= 2) return run_stream<2, MT, GATED, VEC, XT>(a, g, stream);
+  if constexpr (MOST >= 3)
+    if (each <= 3) return run_stream<3, MT, GATED, VEC, XT>(a, g, stream);
+  if constexpr (MOST >= 4)
+    if (each <= 4) return run_stream<4, MT, GATED, VEC, XT>(a, g, stream);
+  return run_stream<MOST, MT, GATED, VEC, XT>(a, g, stream);
+}
+
+template <bool GATED>
+hipError_t run_stream(const MxArgs& a, const MxGemm& g, hipStream_t stream) {
+  if (g.x_type < 0) {
+    if (g.m <= 16) return run_stream<1, GATED, true, uint8_t>(a, g, stream);
+    return g.m <= 32 ? run_stream<2, GATED, true, uint8_t>(a, g, stream)
+                     : run_stream<4, GATED, true, uint8_t>(a, g, stream);
+  }
+  const bool vec = g.k % 8 == 0 && aligned(g.x, 16);
+  if (g.x_type == QW_F32)
+    return vec ? run_stream<1, GATED, true, float>(a, g, stream) : run_stream<1, GATED, false, float>(a, g, stream);
+  return vec ? run_stream<1, GATED, true, uint16_t>(a, g, stream) : run_stream<1, GATED, false, uint16_t>(a, g, stream);
+}
+
+// ---------------------------------------------------------------- choice
+//
+// Which tile: the one with the least estimated time, from what each takes for a round of
+// the compute units (weight rows x tokens; us with bf16 results).  A tile takes
+//   start + (lo + (hi - lo) fill) for each step of 256 values of k,
+// fill being the share of the round that there are tiles for: alone on the chip a tile is
+// bound by its own latencies, all together by the clock that falls with the power.  Measured
+// with k = 4096 and 16384: 4096 x 4096 43.7 and 133 us with 256 x 256, 48.5 and 157 with 128 x
+// 256, 50.0 and 164 with 128 x 128, 66 and 215 with 128 x 64, 70 and 230 with 64 x 64; 2048 x
+// 2048 x 4096 30.9, 21.7, 18.4, 19.4, 19.5; 1024 x 1024 x 4096 28.6, 18.9, 15.8, 13.1, 12.3.
+// (256 x 128 loses to 128 x 256 by 2 to 5 in a hundred at each of these.)
+// A product whose last round is only partly filled may be cut in two along the weight rows,
+// the rest with smaller tiles, for 2 us of a second launch.
+struct Shape {
+  int bn, bm;    // weight rows x tokens of a tile
+  int per_unit;  // tiles that a compute unit holds
+  double start, lo, hi;
+};
+constexpr Shape kShapes[] = {
+    {256, 256, 1, 3.5, 0.85, 1.91}, {128, 256, 1, 2.5, 0.57, 1.13}, {128, 128, 2, 2.5, 0.40, 1.19},
+    {128, 64, 2, 2.0, 0.27, 0.78},  {64, 64, 4, 2.0, 0.21, 0.83},
+};
+constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
+
+// Estimated us of n weight rows against m tokens.
+double cost_of(const Shape& s, int64_t n, int64_t m, int kb) {
+  const int64_t tiles = ((m + s.bm - 1) / s.bm) * ((n + s.bn - 1) / s.bn);
+  if (tiles > 1 << 22) return 1e30;  // a launch holds fewer than 2^32 threads
+  const double slots = (double)kUnits * s.per_unit, whole = std::floor(tiles / slots);
+  const double fill = tiles / slots - whole;
+  double us = whole * (s.start + kb * s.hi);
+  if (fill > 0) us += s.start + kb * (s.lo + (s.hi - s.lo) * fill);
+  return us + s.start;
+}
+
+int best_shape(int64_t n, int64_t m, int kb, double* cost) {
+  int best = 0;
+  *cost = 1e31;
+  for (int i = 0; i < kShapeCount; ++i) {
+    const double c = cost_of(kShapes[i], n, m, kb);
+    if (c < *cost) {
+      *cost = c;
+      best = i;
+    }
+  }
+  return best;
+}
+
+// How a product is run: with one shape, or (cut > 0) with `shape` up to weight row `cut` and
+// with `rest` from there on.
+struct Plan {
+  int shape, rest;
+  int64_t cut;
+};
+
+Plan plan_of(MxResult result, int64_t n, int64_t m, int kb) {
+  const int64_t wrows = result == MX_STORE ? n : 2 * n;
+  double cost;
+  const int shape = best_shape(wrows, m, kb, &cost);
+  const Shape& s = kShapes[shape];
+  const int64_t tiles_m = (m + s.bm - 1) / s.bm, tiles_n = (wrows + s.bn - 1) / s.bn;
+  const int64_t slots = kUnits * s.per_unit, cut = tiles_m * tiles_n / slots * slots / tiles_m * s.bn;
+  if (result == MX_STORE && cut > 0 && cut < n) {
+    double rest;
+    const int other = best_shape(n - cut, m, kb, &rest);
+    if (cost_of(s, cut, m, kb) + rest + 2.0 < cost) return {shape, other, cut};
+  }
+  return {shape, 0, 0};
+}
+
+hipError_t run_shape(int shape, const MxArgs& a, const MxGemm& g, hipStream_t stream) {
+  switch (shape) {
+    case 0: return run_tiled<2, 4, 4, 2, 2, 1>(a, g, stream);
+    case 1: return run_tiled<2, 2, 2, 4, 2, 1>(a, g, stream);
+    case 2: return run_tiled<2, 2, 2, 2, 2, 2>(a, g, stream);
+    case 3: return run_tiled<2, 1, 2, 2, 2, 2>(a, g, stream);
+    default: return run_tiled<2, 1, 1, 2, 2, 4>(a, g, stream);
+  }
 }
 
 }  // namespace
 
+// The products that the stream kernel takes: up to 32 rows of x wherever it holds them (us
+// against the tiles: 4096 x 4096 8.0 and 12.1, 4096 x 11008 10.5 and 23.7, 28672 x 4096 15.5 and
+// 16.6, 28672 x 8192 29.2 and 27.8), up to 64 where the weight has at most 16384 rows (33 rows
+// of 11008 x 4096 9.0 and 12.3, of 28672 x 4096 17.0 and 16.8; 64 rows 11.1 and 12.4, 19.3 and
+// 17.4), since every block reads all rows of x.
+bool mx_gemm_streams(MxResult result, int64_t n, int64_t m, int64_t k) {
+  if ((result != MX_STORE && result != MX_GATED) || m > 64 || k == 0) return false;
+  const bool gated = result == MX_GATED;
+  if (m > 32 && (gated ? 2 * n : n) > 16384) return false;
+  const int most = m <= 16 ? (gated ? kMostUnits<1, true> : kMostUnits<1, false>)
+                 : m <= 32 ? (gated ? kMostUnits<2, true> : kMostUnits<2, false>)
+                           : (gated ? kMostUnits<4, true> : kMostUnits<4, false>);
+  return units_of_wave(k) <= most;
+}
+
+// The stream kernel quantizes x itself up to this many rows times units of a wave: every
+// block pays for it (28672 x 8192 at 4 rows 26.9 us, at 8 rows 31.3; with codes 26.2 and 26.7,
+// and 4.7 for a kernel that makes them; 4096 x 4096 at 16 rows 9.6, 7.6 and 2.1).
+bool mx_gemm_fuses(MxResult result, int64_t m, int64_t k) {
+  return m <= 16 && mx_gemm_streams(result, 0, m, k) && m * units_of_wave(k) <= 8;
+}
+
 hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t stream) {
   const MxArgs a = args_of(g);
-  const int64_t rows = g.result == MX_STORE ? g.n : 2 * g.n;
-  auto tiles = [&](int t) { return ((g.m + t - 1) / t) * ((rows + t - 1) / t); };
-  if (tiles(256) >= 256 || tiles(64) > 1 << 22) return run_tiled<2, 4, 4, 2, 2, 1>(a, g, stream);
-  if (tiles(128) >= 256) return run_tiled<2, 2, 2, 2, 2, 2>(a, g, stream);
-  return run_tiled<2, 1, 1, 2, 3, 2>(a, g, stream);
+  if (mx_gemm_streams(g.result, g.n, g.m, g.k))
+    return g.result == MX_GATED ? run_stream<true>(a, g, stream) : run_stream<false>(a, g, stream);
+  const Plan plan = plan_of(g.result, g.n, g.m, a.kb);
+  if (plan.cut == 0) return run_shape(plan.shape, a, g, stream);
+  MxArgs head = a, tail = a;
+  head.n = plan.cut;
+  tail.n = g.n - plan.cut;
+  tail.w += plan.cut * a.kp2;
+  tail.ws += plan.cut * a.ksp;
+  tail.y = (char*)a.y + plan.cut * (g.y_type == QW_BF16 ? 2 : 4);
+  const hipError_t e = run_shape(plan.shape, head, g, stream);
+  return e != hipSuccess ? e : run_shape(plan.rest, tail, g, stream);
 }
 
 }  // namespace qw

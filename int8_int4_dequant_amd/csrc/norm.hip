@@ -258,21 +258,33 @@ __global__ __launch_bounds__(256) void norm_backward(NormBackArgs a) {
   for (int c = 0; c < N; ++c) store8_of_row<false>(mine, (int64_t)(c * LANES + lane) * 8, a.d, dw[c]);
 }
 
-// dweight from the blocks' shares: a thread block takes 64 columns, a wave every fourth
-// share, in a fixed order.
-__global__ __launch_bounds__(256) void sum_shares(const float* __restrict__ part,
-                                                  float* __restrict__ dw, int64_t d, int count) {
-  __shared__ float waves[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < d; c0 += (int64_t)gridDim.x * 64) {
+// dweight from the blocks' shares: a thread block takes 32 columns, each of its 32 halves of
+// waves every 32nd share, in a fixed order.
+__global__ __launch_bounds__(1024) void sum_shares(const float* __restrict__ part,
+                                                   float* __restrict__ dw, int64_t d, int count) {
+  __shared__ float sums[32][33];
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < d; c0 += (int64_t)gridDim.x * 32) {
     const int64_t c = c0 + lane;
     float s = 0.0f;
-    if (c < d)
-      for (int i = wave; i < count; i += 4) s += part[(int64_t)i * d + c];
+    if (c < d) {
+      int i = group;
+      for (; i + 7 * 32 < count; i += 8 * 32) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = part[(int64_t)(i + 32 * j) * d + c];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += v[j];
+      }
+      for (; i < count; i += 32) s += part[(int64_t)i * d + c];
+    }
     __syncthreads();
-    waves[wave][lane] = s;
+    sums[group][lane] = s;
     __syncthreads();
-    if (wave == 0 && c < d) dw[c] = (waves[0][lane] + waves[1][lane]) + (waves[2][lane] + waves[3][lane]);
+    float t = sums[lane][group];  // share `lane` of column `group`
+#pragma unroll
+    for (int h = 1; h < 32; h <<= 1) t += __shfl_xor(t, h);
+    if (lane == 0 && c0 + group < d) dw[c0 + group] = t;
   }
 }
 
@@ -292,8 +304,12 @@ hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
     go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
   else if (lanes <= 512)
     go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  else if (lanes <= 768)
+    go(integral_constant<int, 256>{}, integral_constant<int, 3>{});
   else if (lanes <= 1024)
     go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  else if (lanes <= 1536)
+    go(integral_constant<int, 256>{}, integral_constant<int, 6>{});
   else if (lanes <= 2048)
     go(integral_constant<int, 256>{}, integral_constant<int, 8>{});
   else
@@ -317,6 +333,8 @@ hipError_t run_backward(const NormBackArgs& a, int grid, hipStream_t stream) {
     go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
   else if (lanes <= 512)
     go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  else if (lanes <= 768)
+    go(integral_constant<int, 256>{}, integral_constant<int, 3>{});
   else if (lanes <= 1024)
     go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
   else
@@ -349,7 +367,7 @@ hipError_t launch_rms_norm_backward(const RmsNormBackward& g, hipStream_t stream
   hipError_t e = g.type == QW_F32 ? run_backward<float>(a, grid, stream)
                                   : run_backward<uint16_t>(a, grid, stream);
   if (e != hipSuccess || !g.dweight) return e;
-  sum_shares<<<grid_for(g.d, 64), 256, 0, stream>>>(a.part, g.dweight, g.d, grid);
+  sum_shares<<<grid_for(g.d, 32), 1024, 0, stream>>>(a.part, g.dweight, g.d, grid);
   return hipGetLastError();
 }
 

@@ -851,15 +851,17 @@ int check_norm(int64_t rows, int64_t d, int type, int w_type, const void* weight
   return std::isfinite(eps) && eps >= 0.0f ? QW_OK : QW_EARG;
 }
 
-// The buffers of qw_mx_mlp: the codes of x and of h, or h as floats.
+// The buffers of qw_mx_mlp: the codes of x and of h, and h as floats for few rows.
 struct MxMlpWork {
-  int64_t xc, xs, hc, hs, bytes;
+  int64_t xc, xs, hc, hs, h, bytes;
   MxMlpWork(int64_t m, int64_t d, int64_t f) {
     Carve c;
     xc = c.take(m * (qw::mx_pitch(d) / 2));
     xs = c.take(m * (qw::mx_pitch(d) / 32));
     hc = c.take(m * (qw::mx_pitch(f) / 2));
     hs = c.take(m * (qw::mx_pitch(f) / 32));
+    // for every size of the call, so that what is enough for the largest is for all smaller ones
+    h = c.take((m < 64 ? m : 64) * f * 4);
     bytes = c.at;
   }
 };
@@ -908,7 +910,7 @@ int qw_mx_gemm(int64_t n, int64_t k, const uint8_t* codes, const uint8_t* scales
   if (!y || (k > 0 && (!codes || !scales || !x_codes || !x_scales))) return QW_ENULL;
   if (!codes_ok(codes, scales) || !codes_ok(x_codes, x_scales)) return QW_EARG;
   const qw::MxGemm g = {qw::MX_STORE, n, k, m, codes, scales, x_codes, x_scales, y_type, y,
-                        nullptr, nullptr, nullptr};
+                        nullptr, nullptr, nullptr, -1, nullptr};
   return record(qw::launch_mx_gemm(g, (hipStream_t)stream));
 }
 
@@ -930,17 +932,23 @@ int qw_mx_matmul(int64_t n, int64_t k, const uint8_t* codes, const uint8_t* scal
   if (m * n == 0) return QW_OK;
   if (!y || (k > 0 && (!codes || !scales || !x))) return QW_ENULL;
   if (!codes_ok(codes, scales)) return QW_EARG;
+  qw::MxGemm g = {qw::MX_STORE, n, k, m, codes, scales, nullptr, nullptr, y_type, y,
+                  nullptr, nullptr, nullptr, x_type, x};
   const int64_t need = qw_mx_matmul_work_bytes(m, k);
   if (need > 0 && (!work || work_bytes < need || !qw::aligned(work, 16))) return QW_EWORK;
-  Carve c;
-  uint8_t* const xc = (uint8_t*)work + c.take(m * (qw::mx_pitch(k) / 2));
-  uint8_t* const xs = (uint8_t*)work + c.take(0);
-  if (k > 0) {
-    st = record(qw::launch_mx_quantize(0, m, k, x_type, x, xc, xs, (hipStream_t)stream));
-    if (st != QW_OK) return st;
+  if (!qw::mx_gemm_fuses(qw::MX_STORE, m, k)) {
+    Carve c;
+    uint8_t* const xc = (uint8_t*)work + c.take(m * (qw::mx_pitch(k) / 2));
+    uint8_t* const xs = (uint8_t*)work + c.take(0);
+    if (k > 0) {
+      st = record(qw::launch_mx_quantize(0, m, k, x_type, x, xc, xs, (hipStream_t)stream));
+      if (st != QW_OK) return st;
+    }
+    g.x_type = -1;
+    g.x = nullptr;
+    g.xc = xc;
+    g.xs = xs;
   }
-  const qw::MxGemm g = {qw::MX_STORE, n, k, m, codes, scales, xc, xs, y_type, y,
-                        nullptr, nullptr, nullptr};
   return record(qw::launch_mx_gemm(g, (hipStream_t)stream));
 }
 
@@ -1012,7 +1020,7 @@ int qw_mx_gated(int64_t f, int64_t k, const uint8_t* codes, const uint8_t* scale
   if (!h || (k > 0 && (!codes || !scales || !x_codes || !x_scales))) return QW_ENULL;
   if (!codes_ok(codes, scales) || !codes_ok(x_codes, x_scales)) return QW_EARG;
   const qw::MxGemm g = {qw::MX_GATED, f, k, m, codes, scales, x_codes, x_scales, h_type, h,
-                        nullptr, nullptr, nullptr};
+                        nullptr, nullptr, nullptr, -1, nullptr};
   return record(qw::launch_mx_gemm(g, (hipStream_t)stream));
 }
 
@@ -1027,7 +1035,7 @@ int qw_mx_gated_codes(int64_t f, int64_t k, const uint8_t* codes, const uint8_t*
   if (!codes_ok(codes, scales) || !codes_ok(x_codes, x_scales) || !codes_ok(h_codes, h_scales))
     return QW_EARG;
   const qw::MxGemm g = {qw::MX_GATED_CODES, f, k, m, codes, scales, x_codes, x_scales, QW_F32,
-                        h_codes, h_scales, nullptr, nullptr};
+                        h_codes, h_scales, nullptr, nullptr, -1, nullptr};
   return record(qw::launch_mx_gemm(g, (hipStream_t)stream));
 }
 
@@ -1042,7 +1050,7 @@ int qw_mx_gated_backward(int64_t f, int64_t k, const uint8_t* codes, const uint8
     return QW_ENULL;
   if (!codes_ok(codes, scales) || !codes_ok(x_codes, x_scales)) return QW_EARG;
   const qw::MxGemm g = {qw::MX_GATED_BACKWARD, f, k, m, codes, scales, x_codes, x_scales, type,
-                        dgate_up, nullptr, dh, h};
+                        dgate_up, nullptr, dh, h, -1, nullptr};
   return record(qw::launch_mx_gemm(g, (hipStream_t)stream));
 }
 
@@ -1070,12 +1078,37 @@ int qw_mx_mlp(int64_t d, int64_t f, const uint8_t* gate_up, const uint8_t* gate_
   const MxMlpWork at(m, d, f);
   if (!work || work_bytes < at.bytes || !qw::aligned(work, 16)) return QW_EWORK;
   uint8_t* const b = (uint8_t*)work;
-  st = qw_mx_quantize(0, m, d, x_type, x, b + at.xc, b + at.xs, stream);
-  if (st != QW_OK) return st;
-  st = qw_mx_gated_codes(f, d, gate_up, gate_up_scales, m, b + at.xc, b + at.xs, b + at.hc,
-                         b + at.hs, stream);
-  if (st != QW_OK) return st;
-  return qw_mx_gemm(d, f, down, down_scales, m, b + at.hc, b + at.hs, y_type, y, stream);
+  const hipStream_t s = (hipStream_t)stream;
+  // few rows: gated values as floats, the sums of both products shared by waves
+  const bool few = qw::mx_gemm_streams(qw::MX_GATED, f, m, d) && qw::mx_gemm_streams(qw::MX_STORE, d, m, f);
+  qw::MxGemm up = {qw::MX_GATED, f, d, m, gate_up, gate_up_scales, b + at.xc, b + at.xs, QW_F32,
+                   b + at.h, nullptr, nullptr, nullptr, -1, nullptr};
+  if (few && qw::mx_gemm_fuses(qw::MX_GATED, m, d)) {
+    up.x_type = x_type;
+    up.x = x;
+  } else {
+    st = qw_mx_quantize(0, m, d, x_type, x, b + at.xc, b + at.xs, stream);
+    if (st != QW_OK) return st;
+  }
+  if (!few) {
+    up.result = qw::MX_GATED_CODES;
+    up.y = b + at.hc;
+    up.ys = b + at.hs;
+  }
+  if (f > 0) {
+    st = record(qw::launch_mx_gemm(up, s));
+    if (st != QW_OK) return st;
+  }
+  qw::MxGemm out = {qw::MX_STORE, d, f, m, down, down_scales, b + at.hc, b + at.hs, y_type, y,
+                    nullptr, nullptr, nullptr, -1, nullptr};
+  if (few && qw::mx_gemm_fuses(qw::MX_STORE, m, f)) {
+    out.x_type = QW_F32;
+    out.x = b + at.h;
+  } else if (few) {
+    st = qw_mx_quantize(0, m, f, QW_F32, b + at.h, b + at.hc, b + at.hs, stream);
+    if (st != QW_OK) return st;
+  }
+  return record(qw::launch_mx_gemm(out, s));
 }
 
 // Which kernel family a call with these arguments would take (1 = fast,

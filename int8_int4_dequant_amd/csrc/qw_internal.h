@@ -152,7 +152,13 @@ struct MxGemm {
   uint8_t* ys;      // MX_GATED_CODES: their scales
   const void* dh;
   void* h;          // MX_GATED_BACKWARD: may be NULL
+  int x_type;       // QW_F32 or QW_BF16: x, not xc and xs (where mx_gemm_fuses), or -1
+  const void* x;
 };
+// Whether launch_mx_gemm takes few rows by the kernel that shares k among its waves.
+bool mx_gemm_streams(MxResult result, int64_t n, int64_t m, int64_t k);
+// Whether launch_mx_gemm takes float x of these sizes and quantizes it itself.
+bool mx_gemm_fuses(MxResult result, int64_t m, int64_t k);
 hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t stream);
 
 // RMS norm (norm.hip).

@@ -270,13 +270,20 @@ def test_gated(m, f, k, dtype):
 
 
 @pytest.mark.parametrize("m,f,k", GATED)
-def test_gated_codes_are_those_of_the_values(m, f, k):
-    """The same sums, so bit for bit."""
+def test_gated_codes(m, f, k):
+    """The codes of the values: of more than 64 rows, whose floats have the same sums, bit
+    for bit; of fewer, whose floats are summed in another order, within half a step."""
     print("gated codes", m, f, k, flush=True)
     rec, xrec = gated_case(m, f, k)[:2]
-    got, want = qw.mx_gated(rec, xrec, quantize=True), qw.mx_quantize(qw.mx_gated(rec, xrec))
+    got, h = qw.mx_gated(rec, xrec, quantize=True), qw.mx_gated(rec, xrec)
+    want = qw.mx_quantize(h)
     assert got["shape"] == [m, f]
-    assert torch.equal(got["scales"], want["scales"]) and torch.equal(got["codes"], want["codes"])
+    if m > 64:
+        assert torch.equal(got["scales"], want["scales"]) and torch.equal(got["codes"], want["codes"])
+    s = np.repeat(2.0 ** (bytes_of(got["scales"]).astype(np.float64) - 127), 32, 1)[:, :f]
+    assert np.all(np.abs(value(got) - host(h)) <= np.maximum(np.abs(host(h)), s) / 4 * (1 + 1e-4))
+    kp = om.pitch(f)
+    assert not bytes_of(got["codes"])[:, -(-f // 32) * 16:].any() and np.all(bytes_of(got["scales"])[:, -(-f // 32):kp // 32] == 127)
 
 
 @pytest.mark.parametrize("m,f,k", GATED)
