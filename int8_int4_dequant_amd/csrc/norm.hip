@@ -70,14 +70,14 @@ __device__ __forceinline__ float rounded(float v, uint16_t) {
 }
 
 // 8 results of a row from j on.
-template <Form FORM>
+template <Form FORM, bool NT>
 __device__ __forceinline__ void store_results(const NormArgs& a, int64_t row, int64_t j,
                                               const float v[8]) {
   if (FORM == FLOAT) {
     if (a.y_type == QW_F32)
-      store8_of_row<false>((float*)a.y + row * a.d, j, a.d, v);
+      store8_of_row<false, NT>((float*)a.y + row * a.d, j, a.d, v);
     else
-      store8_of_row<false>((uint16_t*)a.y + row * a.d, j, a.d, v);
+      store8_of_row<false, NT>((uint16_t*)a.y + row * a.d, j, a.d, v);
   } else if (FORM == BLOCK) {
     const float s = block_scale(max16(amax8(v)));
     const u32x2 c = codes8(v, s);
@@ -97,7 +97,7 @@ __device__ __forceinline__ void store_results(const NormArgs& a, int64_t row, in
 
 // LANES lanes a row, CH times 8 values each; CH 0: as many as there are, in two passes
 // over the row.
-template <int LANES, int CH, Form FORM, typename T>
+template <int LANES, int CH, bool NT, Form FORM, typename T>
 __global__ __launch_bounds__(256) void norm(NormArgs a) {
   constexpr int N = CH ? CH : 1, ROWS = 256 / LANES;
   __shared__ float part[4][1];
@@ -111,17 +111,17 @@ __global__ __launch_bounds__(256) void norm(NormArgs a) {
     T* sum = a.sum ? (T*)a.sum + row * a.d : nullptr;
     float v[N][8], sq[1] = {0.0f};
     auto load = [&](int64_t j, float* s) {
-      load8_of_row<false>(x, j, a.d, s);
+      load8_of_row<false, NT>(x, j, a.d, s);
       if (res) {
         float t[8];
-        load8_of_row<false>(res, j, a.d, t);
+        load8_of_row<false, NT>(res, j, a.d, t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] = rounded(s[i] + t[i], T{});
       }
     };
     auto first = [&](int64_t j, float* s) {
       load(j, s);
-      if (sum) store8_of_row<false>(sum, j, a.d, s);
+      if (sum) store8_of_row<false, NT>(sum, j, a.d, s);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sq[0] = __builtin_fmaf(s[i], s[i], sq[0]);
     };
@@ -142,7 +142,7 @@ __global__ __launch_bounds__(256) void norm(NormArgs a) {
       if (FORM != FLOAT && j + 8 > a.d)
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] = j + i < a.d ? s[i] : 0.0f;
-      store_results<FORM>(a, row, j, s);
+      store_results<FORM, NT>(a, row, j, s);
     };
     if (CH) {
 #pragma unroll
@@ -288,12 +288,24 @@ __global__ __launch_bounds__(1024) void sum_shares(const float* __restrict__ par
   }
 }
 
+// Whether rows go past the caches: large ones of 2 bytes, whose lanes read whole runs of 16
+// bytes (8192 x 8192 bf16 into e4m3: 115 -> 109 us; fp32 rows, a lane's 32 bytes in two
+// loads, lose).
+template <typename T>
+bool past_caches(int64_t rows, int64_t d) {
+  return sizeof(T) == 2 && d % 8 == 0 && rows * d >= 16ll << 20;
+}
+
 template <Form FORM, typename T>
 hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
   const int64_t lanes = (a.pitch + 7) / 8;  // chunks of 8 in a row
   auto go = [&](auto lanes_of_row, auto chunks) {
     constexpr int LANES = decltype(lanes_of_row)::value, CH = decltype(chunks)::value;
-    norm<LANES, CH, FORM, T><<<grid_for(a.rows, 256 / LANES), 256, 0, stream>>>(a);
+    // a row that is read twice stays in the caches
+    if (CH && past_caches<T>(a.rows, a.d))
+      norm<LANES, CH, CH && sizeof(T) == 2, FORM, T><<<grid_for(a.rows, 256 / LANES), 256, 0, stream>>>(a);
+    else
+      norm<LANES, CH, false, FORM, T><<<grid_for(a.rows, 256 / LANES), 256, 0, stream>>>(a);
   };
   using std::integral_constant;
   if (lanes <= 64)
@@ -315,6 +327,14 @@ hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
   else
     go(integral_constant<int, 256>{}, integral_constant<int, 0>{});
   return hipGetLastError();
+}
+
+// Blocks of the backward kernel, each with a share of dweight: as many as are on the chip at
+// once, since each takes as many rows (registers: three of a compute unit from three chunks
+// on, four below; 4099 x 5003 fp32 104 us with 1024 blocks, 87 with 768).
+int64_t shares_of(int64_t rows, int64_t d) {
+  const int64_t most = (d + 7) / 8 > 512 ? 768 : 1024;
+  return rows < most ? rows : most;
 }
 
 template <typename T>
@@ -342,9 +362,6 @@ hipError_t run_backward(const NormBackArgs& a, int grid, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Most blocks of the backward kernel: as many shares of dweight are added up.
-constexpr int64_t kShares = 1024;
-
 }  // namespace
 
 hipError_t launch_rms_norm(const RmsNorm& g, hipStream_t stream) {
@@ -358,10 +375,11 @@ hipError_t launch_rms_norm(const RmsNorm& g, hipStream_t stream) {
   }
 }
 
-int64_t rms_norm_shares(int64_t rows) { return rows < kShares ? rows : kShares; }
+// A size that grows with every argument: the most shares, whatever the width.
+int64_t rms_norm_shares(int64_t rows) { return rows < 1024 ? rows : 1024; }
 
 hipError_t launch_rms_norm_backward(const RmsNormBackward& g, hipStream_t stream) {
-  const int grid = (int)rms_norm_shares(g.rows);
+  const int grid = (int)shares_of(g.rows, g.d);
   NormBackArgs a = {g.rows, g.d, g.dy, g.s, g.weight, g.dsum, g.ds,
                     g.dweight ? (float*)g.work : nullptr, g.eps, g.w_type};
   hipError_t e = g.type == QW_F32 ? run_backward<float>(a, grid, stream)
