@@ -207,46 +207,50 @@ __device__ __forceinline__ void store_gated(const MxArgs& a, f32x16 gate, f32x16
 // Gated results: the tile's rows are 32 gate rows and their 32 up rows in turn, so that a
 // lane holds both values of a result.
 
-template <int NF, int MF, int WN, int WM, int STAGES, MxResult RES, typename T>
-__global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(MxArgs a) {
-  constexpr int WAVES = WN * WM, BN = 32 * NF * WN, BM = 32 * MF * WM, ROWS = BN + BM;
-  constexpr bool GATED = RES != MX_STORE;
-  constexpr int COLS = GATED ? BN / 2 : BN;        // outputs of a row in a tile
-  constexpr int SEGS = ROWS / 8 / WAVES;           // 8-row pieces of a wave
-  constexpr int SPER = (ROWS / 32 + WAVES - 1) / WAVES;  // 32-row pieces of scales of a wave
+// What the waves of a block copy for a tile of BN weight rows and BM tokens.
+template <int BN, int BM, int WAVES, bool GATED, bool SWAPPED>
+struct Feed {
+  static constexpr int ROWS = BN + BM;
+  static constexpr int COLS = GATED ? BN / 2 : BN;       // outputs of a row in a tile
+  static constexpr int SEGS = ROWS / 8 / WAVES;          // 8-row pieces of a wave
+  static constexpr int SPER = (ROWS / 32 + WAVES - 1) / WAVES;  // 32-row pieces of scales of a wave
   static_assert(ROWS / 8 % WAVES == 0 && BN % 64 == 0 && BM % 32 == 0, "whole pieces");
-  static_assert(!GATED || NF % 2 == 0, "gate and up rows in one wave");
-  __shared__ __align__(1024) uint8_t lds[STAGES][ROWS * 128];
-  __shared__ __align__(1024) uint8_t scales[2][ROWS * 32];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
-  const int wm = wave % WM * 32 * MF, wn = wave / WM * 32 * NF;
-  // the weight row (of gate or up) that LDS row `row` holds
-  auto weight_row = [](int row) {
-    const int at = GATED ? row / 64 * 32 + row % 32 : row;
-    return kSwapped<RES, T> ? swapped(at) : at;
-  };
-  uint32_t voff[SEGS], soff[SPER];
-#pragma unroll
-  for (int s = 0; s < SEGS; ++s) {
-    const int row = (wave + WAVES * s) * 8 + (lane >> 3);
-    const int c = (lane & 7) ^ ((row >> 1) & 7);
-    const int at = row >= BN ? row - BN : weight_row(row);
-    voff[s] = (uint32_t)at * (uint32_t)a.kp2 + c * 16;
-  }
-#pragma unroll
-  for (int s = 0; s < SPER; ++s) {
-    const int row = (wave + WAVES * s) * 32 + (lane >> 1);
-    const int at = row >= BN ? row - BN : weight_row(row);
-    soff[s] = (uint32_t)at * (uint32_t)a.ksp + (lane & 1) * 16;
-  }
   // A tile, and each piece's buffer, of which the rows behind the last one are not a part.
   struct Place {
     int64_t n0, m0;
     int rows;
     i32x4 from[SEGS], sfrom[SPER];
   };
-  auto place = [&](int64_t tile, Place& p) {
+  const MxArgs& a;
+  const int wave, kb, chunks;
+  int base = 0;  // which of the two buffers holds the tile's first scales
+  uint32_t lds0, lds1, voff[SEGS], soff[SPER];
+  Place here, then;
+
+  // the weight row (of gate or up) that LDS row `row` holds
+  static __device__ __forceinline__ int weight_row(int row) {
+    const int at = GATED ? row / 64 * 32 + row % 32 : row;
+    return SWAPPED ? swapped(at) : at;
+  }
+  __device__ __forceinline__ Feed(const MxArgs& args, int wave, int lane, uint8_t* lds, uint8_t* scales)
+      : a(args), wave(wave), kb(args.kb), chunks((args.kb + 3) >> 2) {
+    lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    lds1 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)scales;
+#pragma unroll
+    for (int s = 0; s < SEGS; ++s) {
+      const int row = (wave + WAVES * s) * 8 + (lane >> 3);
+      const int c = (lane & 7) ^ ((row >> 1) & 7);
+      const int at = row >= BN ? row - BN : weight_row(row);
+      voff[s] = (uint32_t)at * (uint32_t)a.kp2 + c * 16;
+    }
+#pragma unroll
+    for (int s = 0; s < SPER; ++s) {
+      const int row = (wave + WAVES * s) * 32 + (lane >> 1);
+      const int at = row >= BN ? row - BN : weight_row(row);
+      soff[s] = (uint32_t)at * (uint32_t)a.ksp + (lane & 1) * 16;
+    }
+  }
+  __device__ __forceinline__ void place(int64_t tile, Place& p) const {
     int64_t tm, tn;
     const bool there = tile < a.tiles;
     tile_place(there ? tile : 0, a.tiles, a.tiles_m, tm, tn);
@@ -269,15 +273,11 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
       const int seg = wave + WAVES * s;
       p.sfrom[s] = choose(seg >= BN / 32, GATED && seg % 2, a.xs, a.ws, a.ksp);
     }
-  };
-  const int kb = a.kb, chunks = (kb + 3) >> 2;
-  Place here, then;
-  place(blockIdx.x, here);
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0];
-  const uint32_t lds1 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&scales[0][0];
-  // Behind the last tile there is nothing to read, but the copy is issued all the same (as
-  // zeros, from an empty buffer), so that every step has as many.
-  auto fetch = [&](int b, int buf, int s) {
+  }
+  // Piece S of step b into buffer `buf`.  Behind the tile's last step: of the next tile.  Behind
+  // the last tile there is nothing to read, but the copy is issued all the same (as zeros,
+  // from an empty buffer), so that every step has as many.
+  __device__ __forceinline__ void fetch(int b, int buf, int s) const {
     if (s >= SEGS) return;
     const bool in = b < kb;
     i32x4 buffer = here.from[s];
@@ -285,9 +285,9 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
     for (int c = 0; c < 3; ++c) buffer[c] = in ? buffer[c] : then.from[s][c];
     copy_to_lds(buffer, voff[s], (uint32_t)(in ? b : b - kb) * 128,
                 lds0 + buf * (ROWS * 128) + (wave + WAVES * s) * 1024);
-  };
-  int base = 0;  // which of the two buffers holds the tile's first scales
-  auto fetch_scales = [&](int u, bool when) {  // of steps 4 u .. 4 u + 3
+  }
+  // The scales of steps 4 u .. 4 u + 3.
+  __device__ __forceinline__ void fetch_scales(int u, bool when) const {
     const bool in = u < chunks;
 #pragma unroll
     for (int s = 0; s < SPER; ++s) {
@@ -298,15 +298,37 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
                        (uint32_t)(in ? u : u - chunks) * 32,
                        lds1 + ((base + u) & 1) * (ROWS * 32) + (wave + WAVES * s) * 1024);
     }
-  };
+  }
+  // A block's first tile and the one behind it: their places, and the first copies.
+  template <int STAGES>
+  __device__ __forceinline__ void start(int64_t tile, int64_t next) {
+    place(tile, here);
+    place(next, then);
+    fetch_scales(0, true);
+    fetch_scales(1, true);
+#pragma unroll
+    for (int b = 0; b < STAGES; ++b)
+#pragma unroll
+      for (int s = 0; s < SEGS; ++s) fetch(b, b, s);
+  }
+};
+
+template <int NF, int MF, int WN, int WM, int STAGES, MxResult RES, typename T>
+__global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(MxArgs a) {
+  constexpr int WAVES = WN * WM, BN = 32 * NF * WN, BM = 32 * MF * WM;
+  constexpr bool GATED = RES != MX_STORE;
+  using F = Feed<BN, BM, WAVES, GATED, kSwapped<RES, T>>;
+  constexpr int ROWS = F::ROWS, SEGS = F::SEGS;
+  static_assert(!GATED || NF % 2 == 0, "gate and up rows in one wave");
+  __shared__ __align__(1024) uint8_t lds[STAGES][ROWS * 128];
+  __shared__ __align__(1024) uint8_t scales[2][ROWS * 32];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
+  const int wm = wave % WM * 32 * MF, wn = wave / WM * 32 * NF;
+  F feed(a, wave, lane, lds[0], scales[0]);
+  const int kb = a.kb;
   int64_t tile = blockIdx.x + gridDim.x;
-  place(tile, then);
-  fetch_scales(0, true);
-  fetch_scales(1, true);
-#pragma unroll
-  for (int b = 0; b < STAGES; ++b)
-#pragma unroll
-    for (int s = 0; s < SEGS; ++s) fetch(b, b, s);
+  feed.template start<STAGES>(blockIdx.x, tile);
 
   i32x4 w[2][NF], x[2][MF];  // fragments of two products
   int sw[NF], sx[MF], sw2[NF], sx2[MF];
@@ -321,8 +343,8 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
       w[Q & 1][n - MF] = *(const i32x4*)(p + (wn + 32 * (n - MF)) * 128);
   };
   auto take_scale = [&](int b, int n) {
-    const int u = b < kb ? b >> 2 : chunks, in = b < kb ? b & 3 : 0;  // behind the last: the next tile's first
-    const uint8_t* p = &scales[(base + u) & 1][r * 32 + in * 8 + 4 * half];
+    const int u = b < kb ? b >> 2 : feed.chunks, in = b < kb ? b & 3 : 0;  // behind the last: the next tile's first
+    const uint8_t* p = &scales[(feed.base + u) & 1][r * 32 + in * 8 + 4 * half];
     if (n < MF)
       sx2[n] = *(const int*)(p + (BN + wm + 32 * n) * 32);
     else if (n < MF + NF)
@@ -331,10 +353,10 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
   constexpr int FRAGS = NF + MF, PRODUCTS = NF * MF;
   constexpr int TAKES = (FRAGS + PRODUCTS - 1) / PRODUCTS, COPIES = (SEGS + PRODUCTS - 1) / PRODUCTS;
   // Copies that may be on their way when step b + 1 has to be there: those of the
-  // STAGES - 2 steps behind it.  Scales are issued before the copies of their step and four
-  // steps ahead of their use: they only make the wait longer.
+  // STAGES - 2 steps behind it.  Scales are issued before the copies of their step and at least
+  // one step ahead of the wait before their use (a tile's last chunk may be one step).
   constexpr int LEFT = (STAGES - 2) * SEGS;
-  static_assert(STAGES >= 2 && STAGES <= 4, "scales have landed by then");
+  static_assert(STAGES == 2 || STAGES == 3, "scales have landed by then");
   landed<LEFT + SEGS>();
 #pragma unroll
   for (int n = 0; n < FRAGS; ++n) {
@@ -375,10 +397,10 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
     // This wave holds all that it needs of this buffer and of these scales; once every
     // wave does, they are filled again.
     landed<LEFT>();
-    fetch_scales((b >> 2) + 2, (b & 3) == 3 || b + 1 == kb);
+    feed.fetch_scales((b >> 2) + 2, (b & 3) == 3 || b + 1 == kb);
     products(std::integral_constant<int, 3>{}, [&](int p) {
 #pragma unroll
-      for (int n = 0; n < COPIES; ++n) fetch(b + STAGES, buf, p * COPIES + n);
+      for (int n = 0; n < COPIES; ++n) feed.fetch(b + STAGES, buf, p * COPIES + n);
 #pragma unroll
       for (int n = 0; n < TAKES; ++n) {
         take(next, std::integral_constant<int, 0>{}, p * TAKES + n);
@@ -389,43 +411,121 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
   }
 #pragma unroll
   for (int j = 0; j < MF; ++j) {
-    const int64_t row = here.m0 + wm + 32 * j + r;
-    const bool have = wm + 32 * j + r < here.rows;
+    const int64_t row = feed.here.m0 + wm + 32 * j + r;
+    const bool have = wm + 32 * j + r < feed.here.rows;
     if constexpr (GATED) {
 #pragma unroll
       for (int i = 0; i < NF; i += 2)
-        store_gated<RES, T>(a, acc[i][j], acc[i + 1][j], row, here.n0 + (wn + 32 * i) / 2, half, have);
+        store_gated<RES, T>(a, acc[i][j], acc[i + 1][j], row, feed.here.n0 + (wn + 32 * i) / 2, half, have);
     } else {
       if (!have) continue;
 #pragma unroll
-      for (int i = 0; i < NF; ++i) store_fragment<T>(a, acc[i][j], row, here.n0 + wn + 32 * i, half);
+      for (int i = 0; i < NF; ++i) store_fragment<T>(a, acc[i][j], row, feed.here.n0 + wn + 32 * i, half);
     }
   }
   if (tile >= a.tiles) break;
-  here = then;
-  base += chunks;
+  feed.here = feed.then;
+  feed.base += feed.chunks;
   tile += gridDim.x;
-  place(tile, then);
+  feed.place(tile, feed.then);
   }
   landed<0>();  // the empty copies too, before the block's LDS is another's
 }
 
+// The same for few tiles, which are bound by the latency of a step: a block's four waves
+// share the four products of each step of one tile of 64 x 64, and their sums meet in LDS.
+// (256 values of k take 0.31 us, with two waves above that walk them in turn 0.48.)
+template <int STAGES, MxResult RES, typename T>
+__global__ __launch_bounds__(256, 2) void mx_split(MxArgs a) {
+  constexpr bool GATED = RES != MX_STORE;
+  using F = Feed<64, 64, 4, GATED, kSwapped<RES, T>>;
+  constexpr int ROWS = F::ROWS, SEGS = F::SEGS, LEFT = (STAGES - 2) * SEGS;
+  static_assert(STAGES == 4, "the sums take the place of four steps; scales have landed");
+  __shared__ __align__(1024) uint8_t lds[STAGES][ROWS * 128];
+  __shared__ __align__(1024) uint8_t scales[2][ROWS * 32];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, r = lane & 31, half = lane >> 5;
+  F feed(a, wave, lane, lds[0], scales[0]);
+  const int kb = a.kb;
+  feed.template start<STAGES>(blockIdx.x, a.tiles);
+
+  f32x16 acc[2][2] = {};
+  i32x4 f[2][4];  // fragments of two steps: weight, weight, token, token
+  int sc[2][4];
+  const uint8_t* const mine = &lds[0][r * 128 + (((4 * half + wave) ^ (r >> 1 & 7)) << 4)];
+  auto take = [&](int b, int buf, auto parity) {
+    constexpr int P = decltype(parity)::value;
+    const uint8_t* sp = &scales[(b >> 2) & 1][r * 32 + (b & 3) * 8 + 4 * half];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[P][i] = *(const i32x4*)(mine + buf * (ROWS * 128) + 32 * i * 128);
+      sc[P][i] = *(const int*)(sp + 32 * i * 32);
+    }
+  };
+  landed<LEFT + SEGS>();
+  take(0, 0, std::integral_constant<int, 0>{});
+  auto step = [&](int b, auto parity) {
+    constexpr int P = decltype(parity)::value;
+    const int buf = b & (STAGES - 1);
+    // the next step is there, and every wave has this one in registers
+    landed<LEFT>();
+    feed.fetch_scales((b >> 2) + 2, (b & 3) == 3);
+#pragma unroll
+    for (int s = 0; s < SEGS; ++s) feed.fetch(b + STAGES, buf, s);
+    take(b + 1, (b + 1) & (STAGES - 1), std::integral_constant<int, 1 - P>{});
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sc[P][i] >>= 8 * wave;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        acc[i][j] = mfma64<0>(f[P][i], f[P][2 + j], acc[i][j], sc[P][i], sc[P][2 + j]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  for (int b = 0; b < kb; b += 2) {
+    step(b, std::integral_constant<int, 0>{});
+    if (b + 1 < kb) step(b + 1, std::integral_constant<int, 1>{});
+  }
+  landed<0>();
+  // four fragments of four waves, a lane's values together
+  f32x4* const sums = (f32x4*)&lds[0][0];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        sums[((wave * 4 + i * 2 + j) * 4 + g) * 64 + lane] =
+            f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+  lds_barrier();
+  auto joined = [&](int fragment) {
+    f32x16 t;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      f32x4 v = sums[(fragment * 4 + g) * 64 + lane];
+#pragma unroll
+      for (int o = 1; o < 4; ++o) v += sums[((o * 4 + fragment) * 4 + g) * 64 + lane];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) t[4 * g + c] = v[c];
+    }
+    return t;
+  };
+  const int j = wave & 1, at = 32 * j + r;
+  const int64_t row = feed.here.m0 + at;
+  const bool have = at < feed.here.rows;
+  if constexpr (GATED) {
+    if (wave < 2) store_gated<RES, T>(a, joined(j), joined(2 + j), row, feed.here.n0, half, have);
+  } else {
+    const f32x16 v = joined(wave);  // fragment i, j = wave / 2, wave % 2
+    if (have) store_fragment<T>(a, v, row, feed.here.n0 + 32 * (wave >> 1), half);
+  }
+}
+
 constexpr int kUnits = 256;  // compute units
 
-// PER_UNIT: blocks that a compute unit holds.
-template <int NF, int MF, int WN, int WM, int STAGES, int PER_UNIT>
-hipError_t run_tiled(MxArgs a, const MxGemm& g, hipStream_t stream) {
-  constexpr int BN = 32 * NF * WN, BM = 32 * MF * WM;
-  const int cols = g.result == MX_STORE ? BN : BN / 2;
-  a.tiles_m = (a.m + BM - 1) / BM;
-  a.tiles = a.tiles_m * (((g.result == MX_GATED_CODES ? a.yp : a.n) + cols - 1) / cols);
-  // Tile after tile where there are more than the units hold; copies that run on into the
-  // next tile need two chunks of scales in each.
-  const unsigned grid = (unsigned)(a.kb > 4 ? std::min<int64_t>(a.tiles, kUnits * PER_UNIT) : a.tiles);
-  auto go = [&](auto result, auto type) {
-    mx_tiled<NF, MF, WN, WM, STAGES, decltype(result)::value, decltype(type)>
-        <<<grid, WN * WM * 64, 0, stream>>>(a);
-  };
+// go(result, type) of a call's.
+template <typename Go>
+void with_result(const MxGemm& g, Go go) {
   auto typed = [&](auto result) { g.y_type == QW_F32 ? go(result, 0.0f) : go(result, uint16_t{}); };
   switch (g.result) {
     case MX_STORE: typed(std::integral_constant<MxResult, MX_STORE>{}); break;
@@ -433,6 +533,33 @@ hipError_t run_tiled(MxArgs a, const MxGemm& g, hipStream_t stream) {
     case MX_GATED_CODES: go(std::integral_constant<MxResult, MX_GATED_CODES>{}, 0.0f); break;
     default: typed(std::integral_constant<MxResult, MX_GATED_BACKWARD>{});
   }
+}
+
+void count_tiles(MxArgs& a, const MxGemm& g, int bn, int bm) {
+  const int cols = g.result == MX_STORE ? bn : bn / 2;
+  a.tiles_m = (a.m + bm - 1) / bm;
+  a.tiles = a.tiles_m * (((g.result == MX_GATED_CODES ? a.yp : a.n) + cols - 1) / cols);
+}
+
+// PER_UNIT: blocks that a compute unit holds.
+template <int NF, int MF, int WN, int WM, int STAGES, int PER_UNIT>
+hipError_t run_tiled(MxArgs a, const MxGemm& g, hipStream_t stream) {
+  count_tiles(a, g, 32 * NF * WN, 32 * MF * WM);
+  // Tile after tile where there are more than the units hold; copies that run on into the
+  // next tile need two chunks of scales in each.
+  const unsigned grid = (unsigned)(a.kb > 4 ? std::min<int64_t>(a.tiles, kUnits * PER_UNIT) : a.tiles);
+  with_result(g, [&](auto result, auto type) {
+    mx_tiled<NF, MF, WN, WM, STAGES, decltype(result)::value, decltype(type)>
+        <<<grid, WN * WM * 64, 0, stream>>>(a);
+  });
+  return hipGetLastError();
+}
+
+hipError_t run_split(MxArgs a, const MxGemm& g, hipStream_t stream) {
+  count_tiles(a, g, 64, 64);
+  with_result(g, [&](auto result, auto type) {
+    mx_split<4, decltype(result)::value, decltype(type)><<<(unsigned)a.tiles, 256, 0, stream>>>(a);
+  });
   return hipGetLastError();
 }
 
@@ -674,25 +801,32 @@ hipError_t run_stream(const MxArgs& a, const MxGemm& g, hipStream_t stream) {
 
 // ---------------------------------------------------------------- choice
 //
-// Which tile: the one with the least estimated time, from what each takes for a round of
-// the compute units (weight rows x tokens; us with bf16 results).  A tile takes
-//   start + (lo + (hi - lo) fill) for each step of 256 values of k,
-// fill being the share of the round that there are tiles for: alone on the chip a tile is
-// bound by its own latencies, all together by the clock that falls with the power.  Measured
-// with k = 4096 and 16384: 4096 x 4096 43.7 and 133 us with 256 x 256, 48.5 and 157 with 128 x
-// 256, 50.0 and 164 with 128 x 128, 66 and 215 with 128 x 64, 70 and 230 with 64 x 64; 2048 x
-// 2048 x 4096 30.9, 21.7, 18.4, 19.4, 19.5; 1024 x 1024 x 4096 28.6, 18.9, 15.8, 13.1, 12.3.
-// (256 x 128 loses to 128 x 256 by 2 to 5 in a hundred at each of these.)
+// Which tile: the one with the least estimated time,
+//   first + again for every further round of the compute units + step for each 256 values of
+//   k of each round,
+// step being `lo` with hardly a tile on the chip, `mid` with one on every unit and `hi` with as
+// many as the units hold: a lone tile is bound by its own latencies, all together by the
+// clock that falls with the power.  From (us, bf16 results; tokens x weight rows x k):
+//                    256x256  128x256  128x128   128x64    64x64  64x64 split
+//   4096 4096 16384    133.0    156.6    164.0    214.9    229.7
+//   4096 4096  4096     43.7     48.5     50.0     66.2     70.0
+//   2048 2048  4096     30.9     21.7     18.9     19.4     20.5     23.8
+//   1024 4096  4096                       18.7     20.0     20.5     23.3
+//    512 4096  4096     29.1     19.5     16.2     14.1     17.3     12.6
+//    128 4096  4096                       15.4     12.7     12.7      9.4
+//    128 4096 11008                       31.4     26.3     26.1     17.7
+// (256 x 128, weight rows first, loses to 128 x 256 by 2 to 5 in a hundred.)
 // A product whose last round is only partly filled may be cut in two along the weight rows,
-// the rest with smaller tiles, for 2 us of a second launch.
+// the rest with smaller tiles.
 struct Shape {
   int bn, bm;    // weight rows x tokens of a tile
   int per_unit;  // tiles that a compute unit holds
-  double start, lo, hi;
+  double first, again, lo, mid, hi;
 };
 constexpr Shape kShapes[] = {
-    {256, 256, 1, 3.5, 0.85, 1.91}, {128, 256, 1, 2.5, 0.57, 1.13}, {128, 128, 2, 2.5, 0.40, 1.19},
-    {128, 64, 2, 2.0, 0.27, 0.78},  {64, 64, 4, 2.0, 0.21, 0.83},
+    {256, 256, 1, 14.0, 4.0, 0.85, 1.91, 1.91}, {128, 256, 1, 9.0, 5.0, 0.57, 1.13, 1.13},
+    {128, 128, 2, 6.0, 5.0, 0.57, 0.78, 1.19},  {128, 64, 2, 4.6, 2.5, 0.50, 0.58, 0.80},
+    {64, 64, 4, 5.0, 2.5, 0.48, 0.50, 0.83},    {64, 64, 2, 4.5, 3.0, 0.29, 0.31, 0.48},
 };
 constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
 
@@ -701,10 +835,17 @@ double cost_of(const Shape& s, int64_t n, int64_t m, int kb) {
   const int64_t tiles = ((m + s.bm - 1) / s.bm) * ((n + s.bn - 1) / s.bn);
   if (tiles > 1 << 22) return 1e30;  // a launch holds fewer than 2^32 threads
   const double slots = (double)kUnits * s.per_unit, whole = std::floor(tiles / slots);
-  const double fill = tiles / slots - whole;
-  double us = whole * (s.start + kb * s.hi);
-  if (fill > 0) us += s.start + kb * (s.lo + (s.hi - s.lo) * fill);
-  return us + s.start;
+  const double rest = tiles - whole * slots;
+  // short sums end before the results of the round before are written (4096 x 4096 x 256 16.1
+  // us with 256 x 256 in one round, 19.9 with 128 x 128 in two)
+  const double again = s.again + (kb <= 2 ? 3.0 : 0.0);
+  double us = s.first + whole * (again + kb * s.hi) - again;
+  if (rest > 0) {
+    const double step = rest <= kUnits ? s.lo + (s.mid - s.lo) * rest / kUnits
+                                       : s.mid + (s.hi - s.mid) * (rest - kUnits) / (slots - kUnits);
+    us += again + kb * step;
+  }
+  return us;
 }
 
 int best_shape(int64_t n, int64_t m, int kb, double* cost) {
@@ -737,7 +878,9 @@ Plan plan_of(MxResult result, int64_t n, int64_t m, int kb) {
   if (result == MX_STORE && cut > 0 && cut < n) {
     double rest;
     const int other = best_shape(n - cut, m, kb, &rest);
-    if (cost_of(s, cut, m, kb) + rest + 2.0 < cost) return {shape, other, cut};
+    // what the estimate cannot tell apart stays whole (2048 x 5504 x 1024, 3 in a hundred by it:
+    // 19 us, cut in two 24)
+    if (cost_of(s, cut, m, kb) + rest < 0.94 * cost) return {shape, other, cut};
   }
   return {shape, 0, 0};
 }
@@ -748,7 +891,8 @@ hipError_t run_shape(int shape, const MxArgs& a, const MxGemm& g, hipStream_t st
     case 1: return run_tiled<2, 2, 2, 4, 2, 1>(a, g, stream);
     case 2: return run_tiled<2, 2, 2, 2, 2, 2>(a, g, stream);
     case 3: return run_tiled<2, 1, 2, 2, 2, 2>(a, g, stream);
-    default: return run_tiled<2, 1, 1, 2, 2, 4>(a, g, stream);
+    case 4: return run_tiled<2, 1, 1, 2, 2, 4>(a, g, stream);
+    default: return run_split(a, g, stream);
   }
 }
 
