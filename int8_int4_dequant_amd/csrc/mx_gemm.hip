@@ -26,8 +26,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 struct MxArgs {
   const uint8_t *w, *ws, *x, *xs;
   const void* xfloat; // stream kernel: float rows
-  int64_t n, m, k;    // outputs of a row in this launch (gated: f), rows, values of a row of x
-  int64_t ldy;        // outputs in a row of y
+  int64_t n, m, k;    // outputs in a row (gated: f), rows, values of a row of x
   int64_t kp2, ksp;   // bytes of a row of codes, of scales
   int kb;             // steps of 256 along k
   void* y;
@@ -124,7 +123,7 @@ __device__ __forceinline__ void store_fragment(const MxArgs& a, f32x16 v, int64_
     float o[R::RUN];
 #pragma unroll
     for (int c = 0; c < R::RUN; ++c) o[c] = v[R::RUN * g + c];
-    put<R::RUN>((T*)a.y + row * a.ldy + col, o, a.n - col);
+    put<R::RUN>((T*)a.y + row * a.n + col, o, a.n - col);
   }
 }
 
@@ -314,7 +313,7 @@ struct Feed {
 };
 
 template <int NF, int MF, int WN, int WM, int STAGES, MxResult RES, typename T>
-__global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(MxArgs a) {
+__global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled(MxArgs a) {
   constexpr int WAVES = WN * WM, BN = 32 * NF * WN, BM = 32 * MF * WM;
   constexpr bool GATED = RES != MX_STORE;
   using F = Feed<BN, BM, WAVES, GATED, kSwapped<RES, T>>;
@@ -365,69 +364,69 @@ __global__ __launch_bounds__(WN * WM * 64, WN * WM == 8 ? 2 : 1) void mx_tiled(M
   }
   int buf = 0;
   for (;;) {
-  f32x16 acc[NF][MF] = {};
-  for (int b = 0; b < kb; ++b) {
-    const int next = buf + 1 < STAGES ? buf + 1 : 0;
+    f32x16 acc[NF][MF] = {};
+    for (int b = 0; b < kb; ++b) {
+      const int next = buf + 1 < STAGES ? buf + 1 : 0;
 #pragma unroll
-    for (int i = 0; i < NF; ++i) sw[i] = sw2[i];
+      for (int i = 0; i < NF; ++i) sw[i] = sw2[i];
 #pragma unroll
-    for (int j = 0; j < MF; ++j) sx[j] = sx2[j];
-    // Product Q of all fragments, and between them what comes next.
-    auto products = [&](auto product, auto between) {
-      constexpr int Q = decltype(product)::value;
+      for (int j = 0; j < MF; ++j) sx[j] = sx2[j];
+      // Product Q of all fragments, and between them what comes next.
+      auto products = [&](auto product, auto between) {
+        constexpr int Q = decltype(product)::value;
 #pragma unroll
-      for (int p = 0; p < PRODUCTS; ++p) {
-        between(p);
-        acc[p / MF][p % MF] = mfma64<Q>(w[Q & 1][p / MF], x[Q & 1][p % MF], acc[p / MF][p % MF],
-                                        sw[p / MF], sx[p % MF]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
-    auto with_reads = [&](auto product) {
-      constexpr int Q = decltype(product)::value;
-      products(product, [&](int p) {
+        for (int p = 0; p < PRODUCTS; ++p) {
+          between(p);
+          acc[p / MF][p % MF] = mfma64<Q>(w[Q & 1][p / MF], x[Q & 1][p % MF], acc[p / MF][p % MF],
+                                          sw[p / MF], sx[p % MF]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      auto with_reads = [&](auto product) {
+        constexpr int Q = decltype(product)::value;
+        products(product, [&](int p) {
 #pragma unroll
-        for (int n = 0; n < TAKES; ++n)
-          take(buf, std::integral_constant<int, Q + 1>{}, p * TAKES + n);
+          for (int n = 0; n < TAKES; ++n)
+            take(buf, std::integral_constant<int, Q + 1>{}, p * TAKES + n);
+        });
+      };
+      with_reads(std::integral_constant<int, 0>{});
+      with_reads(std::integral_constant<int, 1>{});
+      with_reads(std::integral_constant<int, 2>{});
+      // This wave holds all that it needs of this buffer and of these scales; once every
+      // wave does, they are filled again.
+      landed<LEFT>();
+      feed.fetch_scales((b >> 2) + 2, (b & 3) == 3 || b + 1 == kb);
+      products(std::integral_constant<int, 3>{}, [&](int p) {
+#pragma unroll
+        for (int n = 0; n < COPIES; ++n) feed.fetch(b + STAGES, buf, p * COPIES + n);
+#pragma unroll
+        for (int n = 0; n < TAKES; ++n) {
+          take(next, std::integral_constant<int, 0>{}, p * TAKES + n);
+          take_scale(b + 1, p * TAKES + n);
+        }
       });
-    };
-    with_reads(std::integral_constant<int, 0>{});
-    with_reads(std::integral_constant<int, 1>{});
-    with_reads(std::integral_constant<int, 2>{});
-    // This wave holds all that it needs of this buffer and of these scales; once every
-    // wave does, they are filled again.
-    landed<LEFT>();
-    feed.fetch_scales((b >> 2) + 2, (b & 3) == 3 || b + 1 == kb);
-    products(std::integral_constant<int, 3>{}, [&](int p) {
-#pragma unroll
-      for (int n = 0; n < COPIES; ++n) feed.fetch(b + STAGES, buf, p * COPIES + n);
-#pragma unroll
-      for (int n = 0; n < TAKES; ++n) {
-        take(next, std::integral_constant<int, 0>{}, p * TAKES + n);
-        take_scale(b + 1, p * TAKES + n);
-      }
-    });
-    buf = next;
-  }
-#pragma unroll
-  for (int j = 0; j < MF; ++j) {
-    const int64_t row = feed.here.m0 + wm + 32 * j + r;
-    const bool have = wm + 32 * j + r < feed.here.rows;
-    if constexpr (GATED) {
-#pragma unroll
-      for (int i = 0; i < NF; i += 2)
-        store_gated<RES, T>(a, acc[i][j], acc[i + 1][j], row, feed.here.n0 + (wn + 32 * i) / 2, half, have);
-    } else {
-      if (!have) continue;
-#pragma unroll
-      for (int i = 0; i < NF; ++i) store_fragment<T>(a, acc[i][j], row, feed.here.n0 + wn + 32 * i, half);
+      buf = next;
     }
-  }
-  if (tile >= a.tiles) break;
-  feed.here = feed.then;
-  feed.base += feed.chunks;
-  tile += gridDim.x;
-  feed.place(tile, feed.then);
+#pragma unroll
+    for (int j = 0; j < MF; ++j) {
+      const int64_t row = feed.here.m0 + wm + 32 * j + r;
+      const bool have = wm + 32 * j + r < feed.here.rows;
+      if constexpr (GATED) {
+#pragma unroll
+        for (int i = 0; i < NF; i += 2)
+          store_gated<RES, T>(a, acc[i][j], acc[i + 1][j], row, feed.here.n0 + (wn + 32 * i) / 2, half, have);
+      } else {
+        if (!have) continue;
+#pragma unroll
+        for (int i = 0; i < NF; ++i) store_fragment<T>(a, acc[i][j], row, feed.here.n0 + wn + 32 * i, half);
+      }
+    }
+    if (tile >= a.tiles) break;
+    feed.here = feed.then;
+    feed.base += feed.chunks;
+    tile += gridDim.x;
+    feed.place(tile, feed.then);
   }
   landed<0>();  // the empty copies too, before the block's LDS is another's
 }
@@ -570,7 +569,7 @@ MxArgs args_of(const MxGemm& g) {
   a.ws = g.scales;
   a.x = g.xc;
   a.xs = g.xs;
-  a.n = a.ldy = g.n;
+  a.n = g.n;
   a.m = g.m;
   a.k = g.k;
   a.xfloat = g.x;
@@ -742,7 +741,7 @@ __global__ __launch_bounds__(kStreamWaves * 64, 2) void mx_stream(MxArgs a) {
         }
         float out = sum[0];
         if constexpr (GATED) gated<1>(&sum[0], &sum[1], &out);
-        store1((T*)a.y + t * a.ldy + col, out);
+        store1((T*)a.y + t * a.n + col, out);
       }
     }
     if (BUFS == 1 && MORE) lds_barrier();
@@ -816,8 +815,6 @@ hipError_t run_stream(const MxArgs& a, const MxGemm& g, hipStream_t stream) {
 //    128 4096  4096                       15.4     12.7     12.7      9.4
 //    128 4096 11008                       31.4     26.3     26.1     17.7
 // (256 x 128, weight rows first, loses to 128 x 256 by 2 to 5 in a hundred.)
-// A product whose last round is only partly filled may be cut in two along the weight rows,
-// the rest with smaller tiles.
 struct Shape {
   int bn, bm;    // weight rows x tokens of a tile
   int per_unit;  // tiles that a compute unit holds
@@ -825,7 +822,7 @@ struct Shape {
 };
 constexpr Shape kShapes[] = {
     {256, 256, 1, 14.0, 4.0, 0.85, 1.91, 1.91}, {128, 256, 1, 9.0, 5.0, 0.57, 1.13, 1.13},
-    {128, 128, 2, 6.0, 5.0, 0.57, 0.78, 1.19},  {128, 64, 2, 4.6, 2.5, 0.50, 0.58, 0.80},
+    {128, 128, 2, 6.0, 3.0, 0.57, 0.78, 1.15},  {128, 64, 2, 4.6, 2.5, 0.50, 0.58, 0.80},
     {64, 64, 4, 5.0, 2.5, 0.48, 0.50, 0.83},    {64, 64, 2, 4.5, 3.0, 0.29, 0.31, 0.48},
 };
 constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
@@ -848,41 +845,17 @@ double cost_of(const Shape& s, int64_t n, int64_t m, int kb) {
   return us;
 }
 
-int best_shape(int64_t n, int64_t m, int kb, double* cost) {
+int best_shape(int64_t n, int64_t m, int kb) {
   int best = 0;
-  *cost = 1e31;
+  double least = 1e31;
   for (int i = 0; i < kShapeCount; ++i) {
     const double c = cost_of(kShapes[i], n, m, kb);
-    if (c < *cost) {
-      *cost = c;
+    if (c < least) {
+      least = c;
       best = i;
     }
   }
   return best;
-}
-
-// How a product is run: with one shape, or (cut > 0) with `shape` up to weight row `cut` and
-// with `rest` from there on.
-struct Plan {
-  int shape, rest;
-  int64_t cut;
-};
-
-Plan plan_of(MxResult result, int64_t n, int64_t m, int kb) {
-  const int64_t wrows = result == MX_STORE ? n : 2 * n;
-  double cost;
-  const int shape = best_shape(wrows, m, kb, &cost);
-  const Shape& s = kShapes[shape];
-  const int64_t tiles_m = (m + s.bm - 1) / s.bm, tiles_n = (wrows + s.bn - 1) / s.bn;
-  const int64_t slots = kUnits * s.per_unit, cut = tiles_m * tiles_n / slots * slots / tiles_m * s.bn;
-  if (result == MX_STORE && cut > 0 && cut < n) {
-    double rest;
-    const int other = best_shape(n - cut, m, kb, &rest);
-    // what the estimate cannot tell apart stays whole (2048 x 5504 x 1024, 3 in a hundred by it:
-    // 19 us, cut in two 24)
-    if (cost_of(s, cut, m, kb) + rest < 0.94 * cost) return {shape, other, cut};
-  }
-  return {shape, 0, 0};
 }
 
 hipError_t run_shape(int shape, const MxArgs& a, const MxGemm& g, hipStream_t stream) {
@@ -924,16 +897,7 @@ hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t stream) {
   const MxArgs a = args_of(g);
   if (mx_gemm_streams(g.result, g.n, g.m, g.k))
     return g.result == MX_GATED ? run_stream<true>(a, g, stream) : run_stream<false>(a, g, stream);
-  const Plan plan = plan_of(g.result, g.n, g.m, a.kb);
-  if (plan.cut == 0) return run_shape(plan.shape, a, g, stream);
-  MxArgs head = a, tail = a;
-  head.n = plan.cut;
-  tail.n = g.n - plan.cut;
-  tail.w += plan.cut * a.kp2;
-  tail.ws += plan.cut * a.ksp;
-  tail.y = (char*)a.y + plan.cut * (g.y_type == QW_BF16 ? 2 : 4);
-  const hipError_t e = run_shape(plan.shape, head, g, stream);
-  return e != hipSuccess ? e : run_shape(plan.rest, tail, g, stream);
+  return run_shape(best_shape(g.result == MX_STORE ? g.n : 2 * g.n, g.m, a.kb), a, g, stream);
 }
 
 }  // namespace qw

@@ -916,6 +916,8 @@ int qw_mx_gemm(int64_t n, int64_t k, const uint8_t* codes, const uint8_t* scales
 
 int64_t qw_mx_matmul_work_bytes(int64_t m, int64_t k) {
   if (check_mx_rows(m, 1, k) != QW_OK) return -1;
+  // more rows or a longer k are not taken either, so that the size grows with both
+  if (qw::mx_gemm_fuses(qw::MX_STORE, m, k)) return 0;
   Carve c;
   c.take(m * (qw::mx_pitch(k) / 2));
   c.take(m * (qw::mx_pitch(k) / 32));
@@ -934,9 +936,9 @@ int qw_mx_matmul(int64_t n, int64_t k, const uint8_t* codes, const uint8_t* scal
   if (!codes_ok(codes, scales)) return QW_EARG;
   qw::MxGemm g = {qw::MX_STORE, n, k, m, codes, scales, nullptr, nullptr, y_type, y,
                   nullptr, nullptr, nullptr, x_type, x};
-  const int64_t need = qw_mx_matmul_work_bytes(m, k);
-  if (need > 0 && (!work || work_bytes < need || !qw::aligned(work, 16))) return QW_EWORK;
   if (!qw::mx_gemm_fuses(qw::MX_STORE, m, k)) {
+    const int64_t need = qw_mx_matmul_work_bytes(m, k);
+    if (need > 0 && (!work || work_bytes < need || !qw::aligned(work, 16))) return QW_EWORK;
     Carve c;
     uint8_t* const xc = (uint8_t*)work + c.take(m * (qw::mx_pitch(k) / 2));
     uint8_t* const xs = (uint8_t*)work + c.take(0);

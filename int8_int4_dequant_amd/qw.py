@@ -1281,10 +1281,22 @@ def _check_mx(rec, what="record"):
     if rec.get("bits") != 4 or rec.get("block") != MX_BLOCK:
         raise ValueError(f"{what}: not a record of 4-bit codes with a scale per {MX_BLOCK}")
     n, k = _nk(rec["shape"])
-    kp = _mx_pitch(k)
-    codes = _fits(rec["codes"], _CODES4, n * kp // 2, f"{what} codes")
-    scales = _fits(rec["scales"], _SCALES4, n * kp // MX_BLOCK, f"{what} scales")
-    return n, k, codes, scales
+    codes, scales = rec["codes"], rec["scales"]
+    bytes32 = n * ((k + 511) // 512 * 16)  # a scale and 16 bytes of codes for 32 values
+    if type(codes) is not torch.Tensor or codes.numel() != 16 * bytes32 or codes.dtype not in _CODES4 \
+            or not codes.is_contiguous():
+        _check_tensor(codes, _CODES4, 16 * bytes32, f"{what} codes")
+    if type(scales) is not torch.Tensor or scales.numel() != bytes32 or scales.dtype not in _SCALES4 \
+            or not scales.is_contiguous():
+        _check_tensor(scales, _SCALES4, bytes32, f"{what} scales")
+    return n, k, codes.data_ptr(), scales.data_ptr()
+
+
+def _result(out, rows, cols, dtype, like):
+    """_output, quick for a new tensor."""
+    if out is None and dtype in TYPES:
+        return like.new_empty((rows, cols), dtype=dtype), TYPES[dtype]
+    return _output(out, rows, cols, dtype, like)
 
 
 def _empty_mx(n, k, device):
@@ -1333,7 +1345,7 @@ def mx_gemm(rec, x, out=None, out_dtype=None, stream=None):
     of k values; of ``out``'s type, ``out_dtype`` or fp32."""
     n, k, codes, scales = _check_mx(rec)
     m, xc, xs = _check_x_mx(x, k)
-    out, yt = _output(out, m, n, out_dtype or (torch.float32 if out is None else None), x["codes"])
+    out, yt = _result(out, m, n, out_dtype or (torch.float32 if out is None else None), x["codes"])
     dev = _device_of(rec["codes"], rec["scales"], x["codes"], x["scales"], out)
     _run("qw_mx_gemm", dev, stream, lib().qw_mx_gemm, n, k, codes, scales, m, xc, xs, yt,
          out.data_ptr())
@@ -1347,7 +1359,7 @@ def mx_matmul(rec, x, out=None, out_dtype=None, work=None, stream=None):
     n, k, codes, scales = _check_mx(rec)
     xt = _check_matrix(x, "x", None, k)
     m = x.shape[0]
-    out, yt = _output(out, m, n, out_dtype or (x.dtype if out is None else None), x)
+    out, yt = _result(out, m, n, out_dtype or (x.dtype if out is None else None), x)
     dev = _device_of(rec["codes"], rec["scales"], x, out, work)
     work, wp, wb = _workspace(work, lib().qw_mx_matmul_work_bytes(m, k), x)
     _run("qw_mx_matmul", dev, stream, lib().qw_mx_matmul, n, k, codes, scales, m, xt,
@@ -1392,7 +1404,7 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6, out=None, out_dtype=None, 
         _run(name, dev, stream, getattr(lib(), name), *args, y["codes"].data_ptr(),
              y["scales"].data_ptr())
     else:
-        y, yt = _output(out, rows, d, out_dtype or (x.dtype if out is None else None), x)
+        y, yt = _result(out, rows, d, out_dtype or (x.dtype if out is None else None), x)
         _run("qw_rms_norm", dev, stream, lib().qw_rms_norm, *args, yt, y.data_ptr())
     return y, x if sum is None else sum
 
@@ -1449,7 +1461,7 @@ def mx_gated(gate_up, x, out=None, out_dtype=None, quantize=False, stream=None):
         _run("qw_mx_gated_codes", dev, stream, lib().qw_mx_gated_codes, f, k, codes, scales, m, xc,
              xs, h["codes"].data_ptr(), h["scales"].data_ptr())
         return h
-    out, ht = _output(out, m, f, out_dtype or (torch.float32 if out is None else None), x["codes"])
+    out, ht = _result(out, m, f, out_dtype or (torch.float32 if out is None else None), x["codes"])
     _run("qw_mx_gated", dev, stream, lib().qw_mx_gated, f, k, codes, scales, m, xc, xs, ht,
          out.data_ptr())
     return out
@@ -1489,7 +1501,7 @@ def mx_mlp(gate_up, down, x, out=None, out_dtype=None, work=None, stream=None):
         raise ValueError("gate_up must be a record of [2 f][d] and down of [d][f]")
     xt = _check_matrix(x, "x", None, d)
     m = x.shape[0]
-    out, yt = _output(out, m, d, out_dtype or (x.dtype if out is None else None), x)
+    out, yt = _result(out, m, d, out_dtype or (x.dtype if out is None else None), x)
     dev = _device_of(gate_up["codes"], gate_up["scales"], down["codes"], down["scales"], x, out,
                      work)
     work, kp, kb = _workspace(work, lib().qw_mx_mlp_work_bytes(m, d, f), x)

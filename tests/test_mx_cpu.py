@@ -77,7 +77,7 @@ def test_sizes():
     L = qw.lib()
     assert [L.qw_mx_pitch(k) for k in (0, 1, 512, 513, MAXE)] == [0, 512, 512, 1024, MAXE]
     assert L.qw_mx_pitch(-1) == L.qw_mx_pitch(I64) == L.qw_mx_pitch(MAXE + 1) == -1
-    assert L.qw_mx_matmul_work_bytes(100, 513) >= 100 * (512 + 32) and L.qw_mx_matmul_work_bytes(0, 513) == 0
+    assert L.qw_mx_matmul_work_bytes(100, 513) >= 100 * (512 + 32) and L.qw_mx_matmul_work_bytes(1, 4096) == L.qw_mx_matmul_work_bytes(0, 513) == 0
     for a in ((-1, 8), (8, -1), (8, I64), (I64, 8), (1, (1 << 22) + 1), (MAXE // 512 + 1, 1)):
         assert L.qw_mx_matmul_work_bytes(*a) == -1
     assert L.qw_rms_norm_backward_work_bytes(3, 100) >= 3 * 400
