@@ -22,6 +22,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32_la __attribute__((may_alias));
 
 struct MxArgs {
   const uint8_t *w, *ws, *x, *xs;
@@ -433,7 +434,7 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled(MxArgs a) {
 
 // The same for few tiles, which are bound by the latency of a step: a block's four waves
 // share the four products of each step of one tile of 64 x 64, and their sums meet in LDS.
-// (256 values of k take 0.31 us, with two waves above that walk them in turn 0.48.)
+// (256 values of k take 0.31 us; 0.48 with tiles of 64 x 64 above, of two waves.)
 template <int STAGES, MxResult RES, typename T>
 __global__ __launch_bounds__(256, 2) void mx_split(MxArgs a) {
   constexpr bool GATED = RES != MX_STORE;
@@ -627,15 +628,16 @@ __device__ __forceinline__ void quantize_part(const MxArgs& a, int unit0, uint8_
         const uint32_t s = mx_scale(top_among<4>(top_of<8>(v[i])));
         const uint32_t c = mx_codes8(v[i], s);
         if (row + i < m) {
-          *(uint32_t*)&codes[row + i][lane * 4] = c;
+          *(u32_la*)&codes[row + i][lane * 4] = c;
           if ((lane & 3) == 0) codes[row + i][256 + (lane >> 2)] = (uint8_t)s;
         }
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own writes, by other lanes
 #pragma unroll
-    for (int t = 0; t < 4; ++t) xf[u][t] = *(const i32x4*)&codes[r][(4 * t + q) * 16];
-    const i32x4 s = *(const i32x4*)&codes[r][256];
+    for (int t = 0; t < 4; ++t)
+      xf[u][t] = __builtin_bit_cast(i32x4, *(const u32x4_la*)&codes[r][(4 * t + q) * 16]);
+    const i32x4 s = __builtin_bit_cast(i32x4, *(const u32x4_la*)&codes[r][256]);
 #pragma unroll
     for (int t = 0; t < 4; ++t) sx[u][t] = s[t] >> 8 * q;
   }
@@ -806,24 +808,26 @@ hipError_t run_stream(const MxArgs& a, const MxGemm& g, hipStream_t stream) {
 // step being `lo` with hardly a tile on the chip, `mid` with one on every unit and `hi` with as
 // many as the units hold: a lone tile is bound by its own latencies, all together by the
 // clock that falls with the power.  From (us, bf16 results; tokens x weight rows x k):
-//                    256x256  128x256  128x128   128x64    64x64  64x64 split
-//   4096 4096 16384    133.0    156.6    164.0    214.9    229.7
-//   4096 4096  4096     43.7     48.5     50.0     66.2     70.0
-//   2048 2048  4096     30.9     21.7     18.9     19.4     20.5     23.8
-//   1024 4096  4096                       18.7     20.0     20.5     23.3
-//    512 4096  4096     29.1     19.5     16.2     14.1     17.3     12.6
-//    128 4096  4096                       15.4     12.7     12.7      9.4
-//    128 4096 11008                       31.4     26.3     26.1     17.7
-// (256 x 128, weight rows first, loses to 128 x 256 by 2 to 5 in a hundred.)
+//                    256x256  128x256  128x128   128x64  64x64 split
+//   4096 4096 16384    133.0    156.6    164.0    214.9
+//   4096 4096  4096     43.7     48.5     50.0     66.2
+//   2048 4096 11008     73.7     58.2     60.5     78.6     93.4
+//   2048 2048  4096     30.9     21.7     18.9     19.4     23.8
+//   1024 4096  4096                       18.7     20.0     23.3
+//    512 4096  4096     29.1     19.5     16.2     14.1     12.6
+//    128 4096  4096                       15.4     12.7      9.4
+//    128 4096 11008                       31.4     26.3     17.7
+// (256 x 128, weight rows first, loses to 128 x 256 by 2 to 5 in a hundred; 64 x 64 with two
+// waves one after the other in k takes 12.7 and 26.1 in the last two and leads nowhere.)
 struct Shape {
   int bn, bm;    // weight rows x tokens of a tile
   int per_unit;  // tiles that a compute unit holds
   double first, again, lo, mid, hi;
 };
 constexpr Shape kShapes[] = {
-    {256, 256, 1, 14.0, 4.0, 0.85, 1.91, 1.91}, {128, 256, 1, 9.0, 5.0, 0.57, 1.13, 1.13},
-    {128, 128, 2, 6.0, 3.0, 0.57, 0.78, 1.15},  {128, 64, 2, 4.6, 2.5, 0.50, 0.58, 0.80},
-    {64, 64, 4, 5.0, 2.5, 0.48, 0.50, 0.83},    {64, 64, 2, 4.5, 3.0, 0.29, 0.31, 0.48},
+    {256, 256, 1, 14.0, 4.0, 0.85, 1.91, 1.91}, {128, 256, 1, 8.5, 5.0, 0.57, 1.13, 1.13},
+    {128, 128, 2, 6.0, 3.0, 0.57, 0.78, 1.19},  {128, 64, 2, 4.6, 2.5, 0.50, 0.58, 0.80},
+    {64, 64, 2, 4.5, 3.0, 0.29, 0.31, 0.48},  // split
 };
 constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
 
@@ -864,7 +868,6 @@ hipError_t run_shape(int shape, const MxArgs& a, const MxGemm& g, hipStream_t st
     case 1: return run_tiled<2, 2, 2, 4, 2, 1>(a, g, stream);
     case 2: return run_tiled<2, 2, 2, 2, 2, 2>(a, g, stream);
     case 3: return run_tiled<2, 1, 2, 2, 2, 2>(a, g, stream);
-    case 4: return run_tiled<2, 1, 1, 2, 2, 4>(a, g, stream);
     default: return run_split(a, g, stream);
   }
 }
@@ -898,6 +901,12 @@ hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t stream) {
   if (mx_gemm_streams(g.result, g.n, g.m, g.k))
     return g.result == MX_GATED ? run_stream<true>(a, g, stream) : run_stream<false>(a, g, stream);
   return run_shape(best_shape(g.result == MX_STORE ? g.n : 2 * g.n, g.m, a.kb), a, g, stream);
+}
+
+int mx_gemm_path(MxResult result, int64_t n, int64_t m, int64_t k) {
+  if (mx_gemm_streams(result, n, m, k)) return 100 * (m <= 16 ? 1 : m <= 32 ? 2 : 4) + units_of_wave(k);
+  const int shape = best_shape(result == MX_STORE ? n : 2 * n, m, (int)((k + 255) / 256));
+  return shape == kShapeCount - 1 ? 2 : kShapes[shape].bn * 1000 + kShapes[shape].bm;
 }
 
 }  // namespace qw

@@ -1113,6 +1113,21 @@ int qw_mx_mlp(int64_t d, int64_t f, const uint8_t* gate_up, const uint8_t* gate_
   return record(qw::launch_mx_gemm(out, s));
 }
 
+int qw_mx_debug_path(int op, int64_t m, int64_t n, int64_t k) {
+  if (op < 0 || op > 4) return QW_EARG;
+  if (op == 0 || op == 4) {
+    if (!mx_fits(n, k)) return QW_ESHAPE;
+    const int st = check_mx_rows(m, n, k);
+    if (st != QW_OK) return st;
+    if (op == 4) return qw::mx_gemm_fuses(qw::MX_STORE, m, k) ? 1 : 2;
+    return qw::mx_gemm_path(qw::MX_STORE, n, m, k);
+  }
+  const int st = check_gated(n, k, m);
+  if (st != QW_OK) return st;
+  return qw::mx_gemm_path(op == 1 ? qw::MX_GATED : op == 2 ? qw::MX_GATED_CODES : qw::MX_GATED_BACKWARD,
+                          n, m, k);
+}
+
 // Which kernel family a call with these arguments would take (1 = fast,
 // 2 = block, 3 = generic, 4 = matrix-core GEMV; for op 5, 1 = GEMV and
 // 2 = GEMM; negative = invalid arguments).  Used by the tests to make sure

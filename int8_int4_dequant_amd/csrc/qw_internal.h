@@ -160,6 +160,8 @@ bool mx_gemm_streams(MxResult result, int64_t n, int64_t m, int64_t k);
 // Whether launch_mx_gemm takes float x of these sizes and quantizes it itself.
 bool mx_gemm_fuses(MxResult result, int64_t m, int64_t k);
 hipError_t launch_mx_gemm(const MxGemm& g, hipStream_t stream);
+// The kernel that launch_mx_gemm takes, as qw_mx_debug_path reports it.
+int mx_gemm_path(MxResult result, int64_t n, int64_t m, int64_t k);
 
 // RMS norm (norm.hip).
 struct RmsNorm {

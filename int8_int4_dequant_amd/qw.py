@@ -50,7 +50,7 @@ EXPORTS_MX = ["qw_mx_pitch", "qw_mx_quantize", "qw_mx_unpack", "qw_mx_gemm",
               "qw_mx_matmul_work_bytes", "qw_mx_matmul", "qw_rms_norm", "qw_rms_norm_block",
               "qw_rms_norm_mx", "qw_rms_norm_backward_work_bytes", "qw_rms_norm_backward",
               "qw_mx_gated", "qw_mx_gated_codes", "qw_mx_gated_backward",
-              "qw_mx_mlp_work_bytes", "qw_mx_mlp"]
+              "qw_mx_mlp_work_bytes", "qw_mx_mlp", "qw_mx_debug_path"]
 
 
 # Rows up to which qw_matmul runs the codes GEMV (QW_MATMUL_GEMV_MAX_M in qw.h).
@@ -231,6 +231,8 @@ def lib():
     L.qw_mx_mlp_work_bytes.restype = i64
     L.qw_mx_mlp.argtypes = [i64, i64, vp, vp, vp, vp, i64, i32, vp, i32, vp, vp, i64, vp]
     L.qw_mx_mlp.restype = i32
+    L.qw_mx_debug_path.argtypes = [i32, i64, i64, i64]
+    L.qw_mx_debug_path.restype = i32
     _lib = L
     return L
 
@@ -558,6 +560,10 @@ def qw_mx_mlp(d, f, gate_up, gate_up_scales, down, down_scales, m, x_type, x, y_
     return lib().qw_mx_mlp(d, f, _ptr(gate_up), _ptr(gate_up_scales), _ptr(down),
                            _ptr(down_scales), m, x_type, _ptr(x), y_type, _ptr(y), _ptr(work),
                            work_bytes, _stream(stream))
+
+
+def qw_mx_debug_path(op, m, n, k):
+    return lib().qw_mx_debug_path(op, m, n, k)
 
 
 # -------------------------------------------------------- convenience layer

@@ -163,7 +163,7 @@ static void fuzz(long iters, int launches_ok) {
     const int64_t n = MOSTLY(kDims, 2, 12), k = MOSTLY(kDims, 1, 14), m = MOSTLY(kMs, 1, 10);
     const int64_t bytes = rnd() % 2 ? INT64_MAX : ((int64_t)(rnd() % 5) - 1) * (1 << 20);
     void* const out = launches_ok ? ptr() : 0; /* without it every call with work to do fails */
-    const int op = (int)(rnd() % 16);
+    const int op = (int)(rnd() % 17);
     int st = 0;
     switch (op) {
       case 0:
@@ -206,8 +206,13 @@ static void fuzz(long iters, int launches_ok) {
           v = qw_mx_matmul_work_bytes(m, k);
         else if (op == 14)
           v = qw_mx_mlp_work_bytes(m, k, n);
-        else
+        else if (op == 15)
           v = qw_rms_norm_backward_work_bytes(m, k);
+        else {
+          v = qw_mx_debug_path((int)(rnd() % 7) - 1, m, n, k);
+          if (v < -10 || v > 256256) fail("qw_mx_debug_path", v);
+          continue;
+        }
         if (v < -1) fail("a size", v);
         continue;
       }

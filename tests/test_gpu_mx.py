@@ -80,8 +80,6 @@ SHAPES = [(1, 1), (1, 31), (3, 33), (5, 512), (7, 513), (130, 1000), (257, 72), 
 @pytest.mark.parametrize("transpose", [False, True])
 @pytest.mark.parametrize("dtype,offset", [(torch.float32, 0), (torch.float32, 1), (torch.bfloat16, 0), (torch.bfloat16, 3)])
 def test_quantize_and_unpack(n, k, transpose, dtype, offset):
-    if n * k > 300000 and offset:
-        pytest.skip("once is enough")
     w = as_type(wide([n, k], n, k), dtype, offset)
     rec = qw.mx_quantize(w, transpose=transpose)
     v = w.float().cpu().numpy()
@@ -367,3 +365,114 @@ def test_mlp_without_hidden_values():
         y = torch.full((m, 40), 7.0, device="cuda")
         qw.mx_mlp(gu, dn, torch.randn(m, 40, device="cuda"), out=y)
         assert not bool(y.any())
+
+
+# ---------------------------------------------------------------- every kernel
+
+MS = (1, 2, 8, 9, 16, 17, 32, 33, 64, 65, 130, 300, 700, 1500, 2500)
+NS = (5, 33, 300, 1100, 2300, 4200, 9000)
+KS = (70, 600, 1500, 4097, 8300, 12400, 17000, 21000)
+
+
+def sizes_of_paths(op):
+    """One call (m, n, k) for every kernel that the library reports, the cheapest first."""
+    found = {}
+    for m, n, k in sorted(((m, n, k) for m in MS for n in NS for k in KS), key=lambda s: s[0] * s[1] * s[2] + s[1] * s[2]):
+        found.setdefault(qw.qw_mx_debug_path(op, m, n, k), (m, n, k))
+    return found
+
+
+def gpu_check(y, xrec, rec, bar=None):
+    k = rec["shape"][1]
+    xv, wv = qw.mx_unpack(xrec).double(), qw.mx_unpack(rec).double()
+    ref, bar = xv @ wv.T, bar_of(k) * (xv.abs() @ wv.abs().T)
+    assert bool(((y.double() - ref).abs() <= bar + HALF[y.dtype] * (ref.abs() + bar)).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_every_kernel_of_the_product(dtype):
+    found = sizes_of_paths(0)
+    assert {2, 128064, 128128, 256256} <= set(found) and {101, 102, 103, 104, 105, 201, 202, 203, 401, 402} <= set(found)
+    for path, (m, n, k) in found.items():
+        print("product", path, m, n, k, dtype, flush=True)
+        g = torch.Generator(device="cuda").manual_seed(path)
+        w = torch.randn(n, k, generator=g, device="cuda") * torch.rand(k, generator=g, device="cuda").mul(3).exp()
+        x = torch.randn(m, k, generator=g, device="cuda")
+        rec, xrec = qw.mx_quantize(w), qw.mx_quantize(x)
+        y = torch.full((m + 1, n), 7.0, dtype=dtype, device="cuda")
+        qw.mx_gemm(rec, xrec, out=y[:m], out_dtype=dtype)
+        gpu_check(y[:m], xrec, rec)
+        assert bool((y[m] == 7).all())
+        z = qw.mx_matmul(rec, x.to(dtype), out_dtype=dtype)
+        gpu_check(z, qw.mx_quantize(x.to(dtype)), rec)
+
+
+@pytest.mark.parametrize("op", [1, 2, 3])
+def test_every_kernel_of_the_gated_product(op):
+    found = sizes_of_paths(op)
+    assert {2, 128064, 128128, 256256} <= set(found)
+    assert op > 1 or {101, 102, 103, 104, 201, 202, 401} <= set(found)
+    for path, (m, f, k) in found.items():
+        print("gated", op, path, m, f, k, flush=True)
+        g = torch.Generator(device="cuda").manual_seed(path)
+        rec = qw.mx_quantize(torch.randn(2 * f, k, generator=g, device="cuda") * k ** -0.5)
+        xrec = qw.mx_quantize(torch.randn(m, k, generator=g, device="cuda"))
+        xv, wv = qw.mx_unpack(xrec).double(), qw.mx_unpack(rec).double()
+        p, bar = xv @ wv.T, bar_of(k) * (xv.abs() @ wv.abs().T)
+        gate, up, eg, eu = p[:, :f], p[:, f:], bar[:, :f], bar[:, f:]
+        t = torch.sigmoid(gate)
+        silu = gate * t
+        want = silu * up
+        tol = 1.1 * eg * (up.abs() + eu) + silu.abs() * eu + 8 * 2.0 ** -23 * want.abs()
+        if op == 1:
+            h = qw.mx_gated(rec, xrec).double()
+            assert bool(((h - want).abs() <= tol + HALF[torch.float32] * want.abs()).all())
+        elif op == 2:
+            got = qw.mx_gated(rec, xrec, quantize=True)
+            s = torch.exp2(got["scales"].double() - 127).repeat_interleave(32, 1)[:, :f]
+            assert bool(((qw.mx_unpack(got).double() - want).abs() <= torch.maximum(want.abs(), s) / 4 * (1 + 1e-4) + tol).all())
+        else:
+            dh = torch.randn(m, f, generator=g, device="cuda")
+            d, h = qw.mx_gated_backward(rec, xrec, dh)
+            a = dh.double().abs()
+            assert bool(((h.double() - want).abs() <= tol + HALF[torch.float32] * want.abs()).all())
+            dg = dh.double() * up * t * (1 + gate * (1 - t))
+            tg = a * (1.1 * eu + 0.5 * eg * (up.abs() + eu) + 10 * 2.0 ** -23 * up.abs())
+            assert bool(((d[:, :f].double() - dg).abs() <= tg + HALF[torch.float32] * dg.abs()).all())
+            tu = a * (1.1 * eg + 8 * 2.0 ** -23 * gate.abs())
+            assert bool(((d[:, f:].double() - dh.double() * silu).abs() <= tu + HALF[torch.float32] * (dh.double() * silu).abs()).all())
+
+
+def test_matmul_quantizes_on_the_way_or_before():
+    """Both sides of the choice give the product of the same codes."""
+    found = {qw.qw_mx_debug_path(4, m, 300, k): (m, k) for m in (16, 9, 8, 4, 1) for k in (700, 4096, 9000)}
+    assert set(found) == {1, 2}
+    for m, k in ((1, 700), (8, 700), (9, 700), (16, 4096), (3, 9000), (4, 9000)):
+        rec, x = qw.mx_quantize(torch.randn(300, k, device="cuda")), torch.randn(m, k, device="cuda")
+        a, b = qw.mx_matmul(rec, x), qw.mx_gemm(rec, qw.mx_quantize(x))
+        assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- values far apart
+
+
+@pytest.mark.parametrize("m", [3, 20, 60, 100, 500])
+def test_far_scales(m):
+    """Blocks whose scales are up to 2^40 apart, and products near both ends of fp32."""
+    g = torch.Generator(device="cuda").manual_seed(m)
+    for shift in (0, -60, 50):
+        w = torch.randn(200, 1000, generator=g, device="cuda") * torch.exp2(torch.randint(-20, 21, (200, 1000 // 40), generator=g, device="cuda").float() + shift).repeat_interleave(40, 1)
+        x = torch.randn(m, 1000, generator=g, device="cuda") * 2.0 ** shift
+        rec, xrec = qw.mx_quantize(w), qw.mx_quantize(x)
+        gpu_check(qw.mx_gemm(rec, xrec), xrec, rec)
+
+
+def test_products_are_exact_where_fp32_holds_them():
+    """Integer codes whose sums need 20 bits: exact in every kernel."""
+    rng = np.random.default_rng(8)
+    for m in (1, 20, 60, 100, 600):
+        w, x = (rng.choice([-6, -4, -3, -2, -1, 0, 1, 2, 3, 4, 6], s).astype(np.float32) for s in ((400, 3100), (m, 3100)))
+        w[:, ::32] = 6
+        x[:, ::32] = 6
+        y = qw.mx_matmul(qw.mx_quantize(torch.from_numpy(w).cuda()), torch.from_numpy(x).cuda())
+        assert np.array_equal(host(y), x.astype(np.float64) @ w.T.astype(np.float64))
