@@ -179,6 +179,86 @@ __device__ __forceinline__ void store_gated(const MxArgs& a, f32x16 gate, f32x16
   }
 }
 
+// A tile's results through LDS: fragments of a wave (COLS = 32 or 64 weight rows of 32 tokens)
+// change lanes, so that 128 (or, 32 results of 2 bytes, 64) bytes of an output row are written
+// by lanes side by side.  Rows of RB bytes, the pieces of 16 bytes swapped as those of the
+// tiles below.  Against runs of 32 bytes from the registers: 4096 x 11008 x 2048 with fp32 results
+// 75 -> 71 us, 4096^3 with bf16 44.4 -> 42.2, 3001 x 6001 x 1000 (rows at any alignment) 33 -> 26.
+// (Past the caches: fp32 results 5 to 25 in a hundred slower, bf16 2 faster.)
+template <typename T, int COLS>
+struct Rows {
+  static constexpr int RB = COLS * (int)sizeof(T), PIECES = RB / 16, AT_ONCE = 64 / PIECES;
+  static constexpr int PER = 16 / (int)sizeof(T);  // results of a piece
+  static_assert(RB == 64 || RB == 128, "a wave's part of LDS is 4 KiB");
+  static __device__ __forceinline__ int place(int row, int piece) {
+    return row * RB + ((piece ^ (RB == 128 ? row >> 1 & 7 : row >> 2 & 3)) << 4);
+  }
+  // the lane's values of fragment I
+  static __device__ __forceinline__ void put(uint8_t* lds, int i, const float v[16], int r, int half) {
+#pragma unroll
+    for (int g = 0; g < 16 / PER; ++g) {
+      uint8_t* const p = lds + place(r, i * (32 / PER) + 2 * g + half);
+      if constexpr (sizeof(T) == 2)
+        *(u32x4_la*)p = u32x4_la{to_bf16x2(v[8 * g], v[8 * g + 1]), to_bf16x2(v[8 * g + 2], v[8 * g + 3]),
+                                 to_bf16x2(v[8 * g + 4], v[8 * g + 5]), to_bf16x2(v[8 * g + 6], v[8 * g + 7])};
+      else
+        *(u32x4_la*)p = u32x4_la{__float_as_uint(v[4 * g]), __float_as_uint(v[4 * g + 1]),
+                                 __float_as_uint(v[4 * g + 2]), __float_as_uint(v[4 * g + 3])};
+    }
+  }
+  // rows [0, rows) of `ld` values, from column 0 on of which `left` are there
+  static __device__ __forceinline__ void store(const uint8_t* lds, T* y, int64_t ld, int rows, int64_t left, int lane) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own writes, by other lanes
+#pragma unroll
+    for (int s = 0; s < 32 / AT_ONCE; ++s) {
+      const int row = s * AT_ONCE + lane / PIECES, piece = lane % PIECES;
+      const u32x4 v = *(const u32x4_la*)(lds + place(row, piece));
+      T* const to = y + row * ld + piece * PER;
+      const int64_t there = left - piece * PER;
+      if (row < rows) {
+        if (there >= PER) {
+          *(u32x4_u*)to = v;
+        } else {
+#pragma unroll
+          for (int c = 0; c < PER; ++c)
+            if (c < there) to[c] = __builtin_bit_cast(Parts, v).part[c];
+        }
+      }
+    }
+  }
+  // The reverse: the lane's 16 values of a fragment of x (COLS = 32).
+  static __device__ __forceinline__ void load(uint8_t* lds, const T* x, int64_t ld, int rows, int64_t left, int lane,
+                                              int r, int half, float v[16]) {
+#pragma unroll
+    for (int s = 0; s < 32 / AT_ONCE; ++s) {
+      const int row = s * AT_ONCE + lane / PIECES, piece = lane % PIECES;
+      const T* const from = x + min(row, rows - 1) * ld + piece * PER;
+      const int64_t there = left - piece * PER;
+      u32x4 t = {};
+      if (there >= PER) {
+        t = *(const u32x4_u*)from;
+      } else {
+        Parts p = {};
+#pragma unroll
+        for (int c = 0; c < PER; ++c)
+          if (c < there) p.part[c] = from[c];
+        t = __builtin_bit_cast(u32x4, p);
+      }
+      *(u32x4_la*)(lds + place(row, piece)) = t;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int g = 0; g < 16 / PER; ++g) {
+      const Parts t = __builtin_bit_cast(Parts, *(const u32x4_la*)(lds + place(r, 2 * g + half)));
+#pragma unroll
+      for (int c = 0; c < PER; ++c) v[PER * g + c] = load1(&t.part[c]);
+    }
+  }
+  struct Parts {
+    T part[PER];
+  };
+};
+
 // ---------------------------------------------------------------- tiled kernel
 //
 // A block of WN x WM waves, each with 32 NF weight rows x 32 MF tokens, 256 values of k (a
@@ -200,9 +280,11 @@ __device__ __forceinline__ void store_gated(const MxArgs& a, f32x16 gate, f32x16
 // that byte t of one word of its row's scales goes with it.
 //
 // A block takes tile after tile (in steps of the grid) and the copies run on: behind the
-// last step of a tile come the first ones of the next, which are on their way while the
-// results are written.  `chunks` of 4 steps and the two buffers of their scales are counted
-// through in the same way.
+// last step of a tile comes the first one of the next, which is on its way while the results
+// are written through the other buffer.  `chunks` of 4 steps and the two buffers of their scales
+// are counted through in the same way.  (With a second set of sums, results written a part
+// after every few of the next tile's steps: slower, 128 x 256 tiles of 2047 x 22016 x 4096 126 ->
+// 136 us, since every wait for a step's copies also waits for the writes before them.)
 //
 // Gated results: the tile's rows are 32 gate rows and their 32 up rows in turn, so that a
 // lane holds both values of a result.
@@ -356,7 +438,7 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled(MxArgs a) {
   // STAGES - 2 steps behind it.  Scales are issued before the copies of their step and at least
   // one step ahead of the wait before their use (a tile's last chunk may be one step).
   constexpr int LEFT = (STAGES - 2) * SEGS;
-  static_assert(STAGES == 2 || STAGES == 3, "scales have landed by then");
+  static_assert(STAGES == 2, "scales have landed by then, and all copies at a tile's end");
   landed<LEFT + SEGS>();
 #pragma unroll
   for (int n = 0; n < FRAGS; ++n) {
@@ -364,66 +446,120 @@ __global__ __launch_bounds__(WN * WM * 64, 2) void mx_tiled(MxArgs a) {
     take_scale(0, n);
   }
   int buf = 0;
-  for (;;) {
-    f32x16 acc[NF][MF] = {};
-    for (int b = 0; b < kb; ++b) {
-      const int next = buf + 1 < STAGES ? buf + 1 : 0;
+  f32x16 acc[NF][MF];
+  auto step = [&](int b, auto ends) {
+    constexpr bool LAST = decltype(ends)::value;  // of a tile
+    const int next = buf + 1 < STAGES ? buf + 1 : 0;
 #pragma unroll
-      for (int i = 0; i < NF; ++i) sw[i] = sw2[i];
+    for (int i = 0; i < NF; ++i) sw[i] = sw2[i];
 #pragma unroll
-      for (int j = 0; j < MF; ++j) sx[j] = sx2[j];
-      // Product Q of all fragments, and between them what comes next.
-      auto products = [&](auto product, auto between) {
-        constexpr int Q = decltype(product)::value;
+    for (int j = 0; j < MF; ++j) sx[j] = sx2[j];
+    // Product Q of all fragments, and between them what comes next.
+    auto products = [&](auto product, auto between) {
+      constexpr int Q = decltype(product)::value;
 #pragma unroll
-        for (int p = 0; p < PRODUCTS; ++p) {
-          between(p);
-          acc[p / MF][p % MF] = mfma64<Q>(w[Q & 1][p / MF], x[Q & 1][p % MF], acc[p / MF][p % MF],
-                                          sw[p / MF], sx[p % MF]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      };
-      auto with_reads = [&](auto product) {
-        constexpr int Q = decltype(product)::value;
-        products(product, [&](int p) {
+      for (int p = 0; p < PRODUCTS; ++p) {
+        between(p);
+        acc[p / MF][p % MF] = mfma64<Q>(w[Q & 1][p / MF], x[Q & 1][p % MF], acc[p / MF][p % MF],
+                                        sw[p / MF], sx[p % MF]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    auto with_reads = [&](auto product) {
+      constexpr int Q = decltype(product)::value;
+      products(product, [&](int p) {
 #pragma unroll
-          for (int n = 0; n < TAKES; ++n)
-            take(buf, std::integral_constant<int, Q + 1>{}, p * TAKES + n);
-        });
-      };
-      with_reads(std::integral_constant<int, 0>{});
-      with_reads(std::integral_constant<int, 1>{});
-      with_reads(std::integral_constant<int, 2>{});
-      // This wave holds all that it needs of this buffer and of these scales; once every
-      // wave does, they are filled again.
-      landed<LEFT>();
-      feed.fetch_scales((b >> 2) + 2, (b & 3) == 3 || b + 1 == kb);
-      products(std::integral_constant<int, 3>{}, [&](int p) {
-#pragma unroll
-        for (int n = 0; n < COPIES; ++n) feed.fetch(b + STAGES, buf, p * COPIES + n);
-#pragma unroll
-        for (int n = 0; n < TAKES; ++n) {
-          take(next, std::integral_constant<int, 0>{}, p * TAKES + n);
-          take_scale(b + 1, p * TAKES + n);
-        }
+        for (int n = 0; n < TAKES; ++n)
+          take(buf, std::integral_constant<int, Q + 1>{}, p * TAKES + n);
       });
-      buf = next;
-    }
+    };
+    with_reads(std::integral_constant<int, 0>{});
+    with_reads(std::integral_constant<int, 1>{});
+    with_reads(std::integral_constant<int, 2>{});
+    // This wave holds all that it needs of this buffer and of these scales; once every
+    // wave does, they are filled again (behind a tile's last step: the buffer takes its
+    // results first).
+    landed<LEFT>();
+    feed.fetch_scales((b >> 2) + 2, LAST || (b & 3) == 3);
+    products(std::integral_constant<int, 3>{}, [&](int p) {
+#pragma unroll
+      for (int n = 0; n < COPIES; ++n)
+        if (!LAST) feed.fetch(b + STAGES, buf, p * COPIES + n);
+#pragma unroll
+      for (int n = 0; n < TAKES; ++n) {
+        take(next, std::integral_constant<int, 0>{}, p * TAKES + n);
+        take_scale(b + 1, p * TAKES + n);
+      }
+    });
+    if (!LAST) buf = next;
+  };
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < MF; ++j) acc[i][j] = f32x16{};
+    for (int b = 0; b + 1 < kb; ++b) step(b, std::false_type{});
+    if (kb > 0) step(kb - 1, std::true_type{});
+    // nothing to add up: the empty copies of both buffers are not on their way any more
+    if (kb == 0) landed<0>();
+    uint8_t* const mine = lds[buf] + wave * (ROWS * 128 / WAVES);
+    static_assert(NF == 2 && ROWS * 128 / WAVES >= 4096, "a wave's part of a buffer");
 #pragma unroll
     for (int j = 0; j < MF; ++j) {
-      const int64_t row = feed.here.m0 + wm + 32 * j + r;
-      const bool have = wm + 32 * j + r < feed.here.rows;
-      if constexpr (GATED) {
+      const int64_t row0 = feed.here.m0 + wm + 32 * j;
+      const int there = feed.here.rows - wm - 32 * j;
+      auto values = [&](int i, float* v) {
 #pragma unroll
-        for (int i = 0; i < NF; i += 2)
-          store_gated<RES, T>(a, acc[i][j], acc[i + 1][j], row, feed.here.n0 + (wn + 32 * i) / 2, half, have);
+        for (int e = 0; e < 16; ++e) v[e] = acc[i][j][e];
+      };
+      if constexpr (RES == MX_STORE) {
+        // both fragments of 2 bytes a value, one of 4
+        constexpr int EACH = sizeof(T) == 2 ? 2 : 1;
+#pragma unroll
+        for (int i = 0; i < NF; i += EACH) {
+          const int64_t col = feed.here.n0 + wn + 32 * i;
+#pragma unroll
+          for (int e = 0; e < EACH; ++e) {
+            float v[16];
+            values(i + e, v);
+            Rows<T, 32 * EACH>::put(mine, e, v, r, half);
+          }
+          Rows<T, 32 * EACH>::store(mine, (T*)a.y + row0 * a.n + col, a.n, there, a.n - col, lane);
+        }
+      } else if constexpr (RES == MX_GATED_CODES) {
+        store_gated<RES, T>(a, acc[0][j], acc[1][j], row0 + r, feed.here.n0 + wn / 2, half, r < there);
       } else {
-        if (!have) continue;
+        const int64_t col = feed.here.n0 + wn / 2, left = a.n - col;
+        float p[16], q[16], v[16];
+        values(0, p);
+        values(1, q);
+        if constexpr (RES == MX_GATED) {
+          gated<16>(p, q, v);
+          Rows<T, 32>::put(mine, 0, v, r, half);
+          Rows<T, 32>::store(mine, (T*)a.y + row0 * a.n + col, a.n, there, left, lane);
+        } else if (there > 0 && left > 0) {
+          float d[16];
+          Rows<T, 32>::load(mine, (const T*)a.dh + row0 * a.n + col, a.n, there, left, lane, r, half, d);
 #pragma unroll
-        for (int i = 0; i < NF; ++i) store_fragment<T>(a, acc[i][j], row, feed.here.n0 + wn + 32 * i, half);
+          for (int e = 0; e < 16; ++e) gate_gradients(p[e], q[e], d[e], v[e], d[e], p[e]);  // p: h
+          T* const y = (T*)a.y + row0 * 2 * a.n + col;
+          Rows<T, 32>::put(mine, 0, v, r, half);
+          Rows<T, 32>::store(mine, y, 2 * a.n, there, left, lane);
+          Rows<T, 32>::put(mine, 0, d, r, half);
+          Rows<T, 32>::store(mine, y + a.n, 2 * a.n, there, left, lane);
+          if (a.h) {
+            Rows<T, 32>::put(mine, 0, p, r, half);
+            Rows<T, 32>::store(mine, (T*)a.h + row0 * a.n + col, a.n, there, left, lane);
+          }
+        }
       }
     }
     if (tile >= a.tiles) break;
+    // every wave's part of the buffer is free: the copies that its last step left out
+    lds_barrier();
+#pragma unroll
+    for (int s = 0; s < SEGS; ++s) feed.fetch(kb - 1 + STAGES, buf, s);
+    buf = buf + 1 < STAGES ? buf + 1 : 0;
     feed.here = feed.then;
     feed.base += feed.chunks;
     tile += gridDim.x;
