@@ -28,6 +28,34 @@ __global__ __launch_bounds__(256) void quantize_rows(const T* __restrict__ w,
   }
 }
 
+// The same for aligned fp32 rows of whole blocks: 8 lanes take a block, 4 values each, so that
+// a load of a wave is 1 KiB in one piece and may go past the caches; two of them a thread.
+template <bool NT>
+__global__ __launch_bounds__(256) void quantize_rows4(const float* __restrict__ w,
+                                                      uint8_t* __restrict__ codes,
+                                                      uint8_t* __restrict__ scales, int64_t k,
+                                                      int64_t kb, int64_t blocks) {
+  // blocks g and g + 32 of every 64
+  for (int64_t g0 = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 3); g0 < blocks;
+       g0 += (int64_t)gridDim.x * 64) {
+    f32x4 v[2];
+    int64_t g[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      g[i] = min(g0 + 32 * i, blocks - 1);
+      const int64_t row = g[i] / kb, j = (g[i] - row * kb) * QW_MX_BLOCK + (threadIdx.x & 7) * 4;
+      v[i] = j < k ? load_as<NT, f32x4>(w + row * k + j) : f32x4{};
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float t[8] = {v[i][0], v[i][1], v[i][2], v[i][3], 0.0f, 0.0f, 0.0f, 0.0f};
+      const uint32_t s = mx_scale(top_among<8>(top_of<4>(t)));
+      *(uint16_t*)(codes + g[i] * 16 + (threadIdx.x & 7) * 2) = (uint16_t)mx_codes8(t, s);
+      if ((threadIdx.x & 7) == 0) scales[g[i]] = (uint8_t)s;
+    }
+  }
+}
+
 // Down the columns: a thread block takes 256 rows of 64 columns, a thread 8 consecutive rows
 // of 8 columns, so that 8 lanes read a run of 64 values and 4 threads have the 32 rows of a
 // block.  The codes go through LDS (rows of 33 words: the 64 lanes of a write meet 64 banks),
@@ -123,6 +151,15 @@ hipError_t quantize(int transpose, int64_t n, int64_t k, const T* w, uint8_t* co
   } else {
     const int64_t kb = mx_pitch(k) / QW_MX_BLOCK, blocks = n * kb;
     const unsigned grid = grid_for(blocks, 64);
+    if constexpr (sizeof(T) == 4) {
+      if (k % 4 == 0 && aligned(w, 16)) {
+        if (n * k >= 16ll << 20)
+          quantize_rows4<true><<<grid, 256, 0, stream>>>(w, codes, scales, k, kb, blocks);
+        else
+          quantize_rows4<false><<<grid, 256, 0, stream>>>(w, codes, scales, k, kb, blocks);
+        return hipGetLastError();
+      }
+    }
     if (k % 8 == 0 && aligned(w, 16))
       quantize_rows<true><<<grid, 256, 0, stream>>>(w, codes, scales, k, kb, blocks);
     else

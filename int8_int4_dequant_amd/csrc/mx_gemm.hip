@@ -99,14 +99,22 @@ __device__ __forceinline__ void get(const T* p, float* v, int64_t left) {
 }
 
 // dgate and dup, h.  With e = exp(-|gate|) neither t nor 1 - t overflows or cancels;
-// beyond |gate| = 200 one of them is zero in fp32.
+// beyond |gate| = 200 one of them is zero in fp32.  e = 2^g as in gated(), the part of g that
+// 24 bits do not hold in a second step; below 2^-64 it is kept 2^64 times, so that t is right
+// down to fp32's subnormal values.
 __device__ __forceinline__ void gate_gradients(float gate, float up, float dh, float& dgate,
                                                float& dup, float& h) {
-  const float e = expf(-fabsf(gate));
-  const float one = 1.0f / (1.0f + e), other = e * one;
+#pragma clang fp contract(off)
+  const float a = -fabsf(gate), g = a * 0x1.715476p+0f;  // log2(e) to 24 bits, and the rest of it
+  const float l = __builtin_fmaf(a, 0x1.4ae0cp-26f, __builtin_fmaf(a, 0x1.715476p+0f, -g));
+  const bool far = g < -64.0f;
+  float e = __builtin_amdgcn_exp2f(far ? g + 64.0f : g);
+  e = __builtin_fmaf(e, g > -190.0f ? l * 0x1.62e43p-1f : 0.0f, e);
+  const float by = far ? 0x1p-64f : 1.0f;
+  const float one = __builtin_amdgcn_rcpf(__builtin_fmaf(e, by, 1.0f)), other = e * one * by;
   const bool neg = gate < 0.0f;
   const float t = neg ? other : one, u = neg ? one : other;
-  const float near = fminf(fmaxf(gate, -200.0f), 200.0f);
+  const float near = __builtin_amdgcn_fmed3f(gate, -200.0f, 200.0f);
   const float silu = gate * t;
   dgate = dh * up * (t * __builtin_fmaf(near, u, 1.0f));
   dup = dh * silu;
