@@ -152,18 +152,17 @@ hipError_t quantize(int transpose, int64_t n, int64_t k, const T* w, uint8_t* co
     const int64_t kb = mx_pitch(k) / QW_MX_BLOCK, blocks = n * kb;
     const unsigned grid = grid_for(blocks, 64);
     if constexpr (sizeof(T) == 4) {
-      if (k % 4 == 0 && aligned(w, 16)) {
-        if (n * k >= 16ll << 20)
-          quantize_rows4<true><<<grid, 256, 0, stream>>>(w, codes, scales, k, kb, blocks);
-        else
-          quantize_rows4<false><<<grid, 256, 0, stream>>>(w, codes, scales, k, kb, blocks);
-        return hipGetLastError();
-      }
-    }
-    if (k % 8 == 0 && aligned(w, 16))
+      if (k % 4 || !aligned(w, 16))
+        quantize_rows<false><<<grid, 256, 0, stream>>>(w, codes, scales, k, kb, blocks);
+      else if (n * k >= 16ll << 20)
+        quantize_rows4<true><<<grid, 256, 0, stream>>>(w, codes, scales, k, kb, blocks);
+      else
+        quantize_rows4<false><<<grid, 256, 0, stream>>>(w, codes, scales, k, kb, blocks);
+    } else if (k % 8 == 0 && aligned(w, 16)) {
       quantize_rows<true><<<grid, 256, 0, stream>>>(w, codes, scales, k, kb, blocks);
-    else
+    } else {
       quantize_rows<false><<<grid, 256, 0, stream>>>(w, codes, scales, k, kb, blocks);
+    }
   }
   return hipGetLastError();
 }
