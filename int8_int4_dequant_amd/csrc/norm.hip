@@ -146,7 +146,7 @@ __global__ __launch_bounds__(256) void norm(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float p = s[i] * rh, e = __builtin_fmaf(s[i], rl, __builtin_fmaf(s[i], rh, -p));
-        s[i] = __builtin_fmaf(p, w[i], e * w[i]);
+        s[i] = __builtin_isinf(w[i]) ? p * w[i] : __builtin_fmaf(p, w[i], e * w[i]);  // e may be 0
       }
       // behind the row: zeros, also of a row whose r is infinite
       if (FORM != FLOAT && j + 8 > a.d)

@@ -98,6 +98,18 @@ def test_rows_of_zeros_infinities_and_nan(d):
         assert torch.equal(rec["scales"].view(torch.uint8), want["scales"].view(torch.uint8))
 
 
+@pytest.mark.parametrize("d", [100, 2000, 17000])
+def test_infinite_weights(d):
+    """Infinities of the values' sign, NaN for a value of 0, and no harm to others."""
+    x, _, w = inputs(3, d, torch.float32)
+    x[1, 4], x[2] = 0.0, 1.0
+    plain, _ = qw.rms_norm(x, w, out_dtype=torch.float32)
+    w[4], w[d - 1] = np.inf, -np.inf
+    y, _ = qw.rms_norm(x, w, out_dtype=torch.float32)
+    assert torch.equal(y[:, :4], plain[:, :4]) and torch.equal(y[:, 5:-1], plain[:, 5:-1])
+    assert np.array_equal(host(y[:, [4, d - 1]]), host(x[:, [4, d - 1]] * w[[4, d - 1]]), equal_nan=True)
+
+
 @pytest.mark.parametrize("rows,d", SHAPES)
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("dsum,weight,offset", [(False, torch.float32, 0), (True, torch.bfloat16, 1), (True, None, 0)])
