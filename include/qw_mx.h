@@ -95,8 +95,8 @@ int qw_mx_matmul(int64_t n, int64_t k, const uint8_t* codes, const uint8_t* scal
  *        residual and the gradient start from).  It may be x or residual itself.
  *   weight [d] of weight_type, or NULL (all 1)   (read)
  *   y [rows][d] of y_type (written)
- * eps is finite and >= 0 (QW_EARG).  x, residual and sum have `type`.  Squares are
- * added 8 at a time in fp32 and then in 64 bits; y has one rounding to fp32 more than that.
+ * eps is finite and >= 0 (QW_EARG).  x, residual and sum have `type`.  Squares
+ * and their sum are held in 64 bits; y is rounded to fp32 and then to its type.
  */
 int qw_rms_norm(int64_t rows, int64_t d, int type, const void* x, const void* residual,
                 void* sum, int weight_type, const void* weight, float eps, int y_type, void* y,

@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256) void norm(NormArgs a) {
     const T* res = a.res ? (const T*)a.res + row * a.d : nullptr;
     T* sum = a.sum ? (T*)a.sum + row * a.d : nullptr;
     float v[N][8];
-    double sq[1] = {0.0};  // of sums of 8 squares in fp32
+    double sq[1] = {0.0};
     auto load = [&](int64_t j, float* s) {
       load8_of_row<false, NT>(x, j, a.d, s);
       if (res) {
@@ -123,10 +123,8 @@ __global__ __launch_bounds__(256) void norm(NormArgs a) {
     auto first = [&](int64_t j, float* s) {
       load(j, s);
       if (sum) store8_of_row<false, NT>(sum, j, a.d, s);
-      float q = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q = __builtin_fmaf(s[i], s[i], q);
-      sq[0] += (double)q;
+      for (int i = 0; i < 8; ++i) sq[0] = __builtin_fma((double)s[i], (double)s[i], sq[0]);
     };
     if (CH) {
 #pragma unroll
@@ -135,18 +133,19 @@ __global__ __launch_bounds__(256) void norm(NormArgs a) {
       for (int64_t j = lane * 8; j < a.d; j += LANES * 8) first(j, v[0]);
     }
     row_sum<LANES>(sq, part);
-    // r from a sum in 64 bits, in two parts, and s r with its rounding's rest: y is rounded
-    // once, so that no more of its codes are neighbours of the right ones than have to be
-    // (HBM leaves the time: 8192 x 8192 bf16 into e4m3 106 us so, 105 in fp32 with two roundings)
+    // squares and their sum in 64 bits, r in two parts, and s r with its rounding's rest: y is
+    // rounded once, so that hardly one of its codes is a neighbour of the right one (HBM leaves
+    // most of the time: 8192 x 8192 bf16 into e4m3 107 us so, 105 in fp32 with two roundings)
     const double r = 1.0 / __builtin_sqrt(sq[0] / (double)a.d + (double)a.eps);
-    const float rh = (float)r, rl = (float)(r - (double)rh);
+    const float rh = (float)r, rl = __builtin_isinf(rh) ? 0.0f : (float)(r - (double)rh);
     auto second = [&](int64_t j, float* s) {
       float w[8];
       load_weights(a.weight, a.w_type, j, a.d, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float p = s[i] * rh, e = __builtin_fmaf(s[i], rl, __builtin_fmaf(s[i], rh, -p));
-        s[i] = __builtin_isinf(w[i]) ? p * w[i] : __builtin_fmaf(p, w[i], e * w[i]);  // e may be 0
+        // (an infinite weight meets e = 0 as a finite one)
+        s[i] = __builtin_fmaf(p, w[i], e * __builtin_amdgcn_fmed3f(w[i], -__FLT_MAX__, __FLT_MAX__));
       }
       // behind the row: zeros, also of a row whose r is infinite
       if (FORM != FLOAT && j + 8 > a.d)

@@ -99,6 +99,16 @@ def test_rows_of_zeros_infinities_and_nan(d):
 
 
 @pytest.mark.parametrize("d", [100, 2000, 17000])
+@pytest.mark.parametrize("by", [2.0 ** -90, 2.0 ** 100])
+def test_squares_beyond_fp32(d, by):
+    """By a power of two, without eps: the same values."""
+    x, _, w = inputs(3, d, torch.float32)
+    want, _ = qw.rms_norm(x, w, eps=0.0)
+    got, _ = qw.rms_norm(x * by, w, eps=0.0)
+    assert bool(want.isfinite().all()) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("d", [100, 2000, 17000])
 def test_infinite_weights(d):
     """Infinities of the values' sign, NaN for a value of 0, and no harm to others."""
     x, _, w = inputs(3, d, torch.float32)
