@@ -181,6 +181,9 @@ struct NormBackArgs {
 
 // The rows of a block in turn; its share of dweight stays in registers (CH 0: in
 // memory, each lane adding to its own).
+// Bound by HBM: 8192 x 4096 bf16 66 us (4.1 TB/s), 4099 x 4096 fp32 57 (4.7), rows that start
+// anywhere in a line less (5003 fp32 3.75).  The row's sums are fp32: the registers are full, and
+// in 64 bits 8192 x 8192 bf16 would take 211 us, not 133.
 template <int LANES, int CH, typename T>
 __global__ __launch_bounds__(256) void norm_backward(NormBackArgs a) {
   constexpr int N = CH ? CH : 1, ROWS = 256 / LANES;
