@@ -65,7 +65,8 @@ int qw_mx_unpack(int64_t n, int64_t k, const uint8_t* codes, const uint8_t* scal
  *   codes, scales       the weight, n x k      (read)
  *   x_codes, x_scales   m rows of k values     (read)
  *   y                   [m][n]                 (written), m >= 0
- * k <= QW_BLOCK_MAX_K (QW_ESHAPE).  Sums are held in fp32: error <= (4 + k/64) *
+ * k <= QW_BLOCK_MAX_K and n <= 2^27 (QW_ESHAPE), m <= 2^27 (QW_EM), also for k = 0, where
+ * y is zeros.  Sums are held in fp32: error <= (4 + k/64) *
  * 2^-23 * sum_j |x[r][j] w[i][j]| and y's rounding, where no block's two scales
  * have a product below 2^-149 (a smaller one counts as zero).  Deterministic: the
  * same call gives the same bits, and rows of x do not influence each other.

@@ -829,8 +829,9 @@ bool mx_fits(int64_t n, int64_t k) {
 
 // x or y side of a product: m rows of n outputs and of k inputs.
 int check_mx_rows(int64_t m, int64_t n, int64_t k) {
-  if (k > QW_BLOCK_MAX_K) return QW_ESHAPE;
-  return within(m, n) && mx_fits(m, k) ? QW_OK : QW_EM;
+  // rows without values are as long as the shortest, so that a launch holds every product's tiles
+  if (k > QW_BLOCK_MAX_K || !mx_fits(n, k ? k : 1)) return QW_ESHAPE;
+  return within(m, n) && mx_fits(m, k ? k : 1) ? QW_OK : QW_EM;
 }
 
 // The weight of a gated product, 2 f x k, and its m rows of x and of results.

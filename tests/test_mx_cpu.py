@@ -142,6 +142,15 @@ def test_product_refusals(want, over):
         assert work(P, 1 << 40) == want
 
 
+@pytest.mark.parametrize("want,n,m", [(ESHAPE, MAXE // 512 + 2, 1), (ESHAPE, MAXE, 1), (EM, 2, MAXE // 512 + 1), (EM, 1, MAXE)])
+def test_sides_too_long_for_a_launch_without_any_k(want, n, m):
+    L = qw.lib()
+    assert L.qw_mx_gemm(n, 0, P, P, m, P, P, 0, P, None) == want
+    assert L.qw_mx_matmul(n, 0, P, P, m, 1, P, 0, P, P, 1 << 40, None) == want
+    assert L.qw_mx_gated(max(n // 2, 1), 0, P, P, m, P, P, 0, P, None) == want
+    assert L.qw_mx_debug_path(0, m, n, 0) == want
+
+
 def test_more_product_refusals():
     L = qw.lib()
     assert L.qw_mx_gated_backward(8, 64, P, P, 4, P, P, 0, None, P, P, None) == ENULL
