@@ -1,0 +1,78 @@
+"""RMS norm and its gradients on the GPU where tests/test_gpu_norm.py says nothing: blocks
+that take many rows, large rows past the caches, values rounded once.
+
+Bars of the gradients: those of tests/test_gpu_norm.py."""
+
+import numpy as np
+import pytest
+import torch
+
+from int8_int4_dequant_amd import qw
+from oracle import mx as om
+from tests.test_gpu_mx import HALF, as_type, host
+from tests.test_gpu_norm import TYPES, chain, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def check_backward(dy, s, w, t, eps, got, dw):
+    rows, d = s.shape
+    hy, hs, hw, ht = host(dy), host(s), None if w is None else host(w), None if t is None else host(t)
+    want, want_w = om.norm_backward(hy, hs, hw, eps, ht)
+    r = 1 / np.sqrt((hs * hs).mean(1, keepdims=True) + eps)
+    u = hy if hw is None else hy * hw
+    tol = (3 * chain(d) + 16) * 2.0 ** -24 * (np.abs(r * u) + np.abs(hs) * r ** 3 * np.abs(u * hs).mean(1, keepdims=True))
+    if ht is not None:
+        tol = tol + 2.0 ** -24 * np.abs(want)
+    assert np.all(np.abs(host(got) - want) <= tol + HALF[s.dtype] * (np.abs(want) + tol))
+    tol = (chain(d) / 2 + 16 + rows) * 2.0 ** -24 * np.abs(hy * hs * r).sum(0)
+    assert np.all(np.abs(host(dw) - want_w) <= tol)
+
+
+# more rows than the 768 or 1024 blocks, so that a block adds up the weight gradients of some
+@pytest.mark.parametrize("rows,d", [(2500, 1030), (1700, 1030), (1600, 2049), (1600, 5003), (900, 8192), (1600, 8200), (1100, 16392), (4099, 600)])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dsum,offset", [(False, 0), (True, 1)])
+def test_backward_of_many_rows(rows, d, dtype, dsum, offset):
+    print("norm backward", rows, d, dtype, dsum, flush=True)
+    s, t, w = inputs(rows, d, dtype, offset)
+    dy = as_type(np.random.default_rng(d).standard_normal((rows, d)).astype(np.float32), dtype, offset)
+    t = t if dsum else None
+    ds = as_type(np.full((rows + 1, d), 7, np.float32), dtype, offset)
+    got, dw = qw.rms_norm_backward(dy, s, w, eps=1e-5, dsum=t, ds=ds[:rows], dweight=torch.full((d,), 7.0, device="cuda"))
+    check_backward(dy, s, w, t, 1e-5, got, dw)
+    assert bool((ds[rows] == 7).all())
+    again, dw2 = qw.rms_norm_backward(dy, s, w, eps=1e-5, dsum=t)
+    assert torch.equal(again, got) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("rows,d", [(65600, 256), (16400, 1024), (8200, 2056), (4100, 4104), (2100, 8200), (1030, 16384)])
+def test_large_bf16_rows_as_their_parts(rows, d):
+    """16 million values and more, which go past the caches: the results of some rows in calls
+    of their own."""
+    print("norm", rows, d, flush=True)
+    assert rows * d >= 16 << 20
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x, res = (torch.randn(rows, d, generator=g, device="cuda").mul_(3).bfloat16() for _ in range(2))
+    w = 1 + 0.1 * torch.randn(d, generator=g, device="cuda")
+    for form in (None, "block", "mx"):
+        y, s = qw.rms_norm(x, w, residual=res, quantize=form)
+        for i in range(0, rows, rows // 5):
+            part = slice(i, i + rows // 5)
+            yp, sp = qw.rms_norm(x[part], w, residual=res[part], quantize=form)
+            assert torch.equal(s[part], sp)
+            if form is None:
+                assert torch.equal(y[part], yp)
+            else:
+                assert torch.equal(y["codes"][part].view(torch.uint8), yp["codes"].view(torch.uint8)) and torch.equal(y["scales"][part], yp["scales"])
+
+
+@pytest.mark.parametrize("rows,d", [(3, 7), (5, 500), (4, 1000), (7, 1030), (3, 4096), (4, 5003), (2, 16384), (2, 40001), (1030, 96)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_values_are_rounded_once(rows, d, dtype):
+    """y in fp32: half a step of it, and what s r's rest and its product with the weight leave, 2^-47."""
+    x, res, w = inputs(rows, d, dtype)
+    for weight in (w, w.bfloat16(), None):
+        y, s = qw.rms_norm(x, weight, residual=res, eps=1e-5, out_dtype=torch.float32)
+        want = om.norm(host(s), None if weight is None else host(weight), 1e-5)
+        assert np.all(np.abs(host(y) - want) <= 2.0 ** -24 * (1 + 2.0 ** -20) * np.abs(want))
