@@ -172,7 +172,8 @@ __device__ __forceinline__ void store_gated(const MxArgs& a, f32x16 gate, f32x16
         put<RUN>((T*)a.y + row * a.n + col, v + RUN * g, a.n - col);
       }
     } else {
-      // The 32 values are one block: half of them in the lane 32 away.
+      // The 32 values are one block: half of them in the lane 32 away.  Behind the last output
+      // they are zeros, or NaN in a row of x that has a NaN scale: code 0, and there the scale 1.
       uint32_t top = top_of<16>(v);
       top = max(top, (uint32_t)__shfl_xor((int)top, 32));
       const uint32_t s = mx_scale(top);
@@ -181,7 +182,7 @@ __device__ __forceinline__ void store_gated(const MxArgs& a, f32x16 gate, f32x16
         uint8_t* const to = (uint8_t*)a.y + (row * a.yp + col0) / 2 + 4 * half;
         *(uint32_t*)to = lo;
         *(uint32_t*)(to + 8) = hi;
-        if (half == 0) a.ys[(row * a.yp + col0) / 32] = (uint8_t)s;
+        if (half == 0) a.ys[(row * a.yp + col0) / 32] = (uint8_t)(col0 < a.n ? s : 127u);
       }
     }
   }

@@ -1,5 +1,5 @@
-"""4-bit codes and gated products on the GPU where tests/test_gpu_mx.py says nothing: large
-weights of the quantizer, the gated product's sums beyond 32-bit
+"""4-bit codes and gated products on the GPU where tests/test_gpu_mx.py says nothing: rows of
+codes behind NaN, large weights of the quantizer, the gated product's sums beyond 32-bit
 offsets, gates far from zero within a few ulp."""
 
 import numpy as np
@@ -11,6 +11,26 @@ from oracle import mx as om
 from tests.test_gpu_mx import HALF, bar_of, bytes_of, host, value
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("m,f,k", [(5, 700, 300), (9, 1, 40), (70, 33, 640), (300, 700, 513), (1030, 600, 260), (700, 1300, 1100), (2500, 4200, 70), (2051, 515, 2100)])
+def test_gated_codes_of_rows_with_nan(m, f, k):
+    """A row of NaN, one of infinities: NaN blocks up to f, and the padding that every row has."""
+    print("gated codes", m, f, k, qw.qw_mx_debug_path(2, m, f, k), flush=True)
+    g = torch.Generator(device="cuda").manual_seed(m + f + k)
+    rec = qw.mx_quantize(torch.randn(2 * f, k, generator=g, device="cuda") * k ** -0.5)
+    x = torch.randn(m, k, generator=g, device="cuda")
+    x[1, ::32] = float("nan")
+    x[m - 1, 3] = float("inf")
+    xrec = qw.mx_quantize(x)
+    got = qw.mx_gated(rec, xrec, quantize=True)
+    scales, codes, blocks = bytes_of(got["scales"]), bytes_of(got["codes"]), -(-f // 32)
+    for row in (1, m - 1):
+        assert np.all(scales[row, :blocks] == 255) and not codes[row].any()
+    assert np.all(scales[:, blocks:] == 127) and not codes[:, 16 * blocks:].any()
+    if m > 64:  # the same sums as the values'
+        want = qw.mx_quantize(qw.mx_gated(rec, xrec))
+        assert torch.equal(got["scales"], want["scales"]) and torch.equal(got["codes"], want["codes"])
 
 
 @pytest.mark.parametrize("n,k", [(4100, 4100), (1030, 16388), (131101, 132)])
