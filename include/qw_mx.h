@@ -126,8 +126,10 @@ int qw_rms_norm_mx(int64_t rows, int64_t d, int type, const void* x, const void*
  *   dweight fp32 [d] (written; NULL: not)
  *   work: qw_rms_norm_backward_work_bytes(rows, d) bytes, 16-byte aligned (QW_EWORK),
  *   needed for dweight only; a buffer for the largest call is enough for all smaller.
- * A row's sums are held in fp32, which |s| > 1e17 or so leaves.  The rows' sum has
- * a fixed order: the same call gives the same bits.
+ * A row's sums are held in fp32, of s by a power of two where its squares would leave
+ * it, so that rows of any magnitude with sqrt(mean(s^2) + eps) from 2^-126 on have their
+ * gradients (below that r is infinite).  The rows' sum has a fixed order: the same call
+ * gives the same bits.
  */
 int64_t qw_rms_norm_backward_work_bytes(int64_t rows, int64_t d);
 int qw_rms_norm_backward(int64_t rows, int64_t d, int type, const void* dy, const void* s,

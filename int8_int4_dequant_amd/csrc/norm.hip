@@ -182,10 +182,12 @@ struct NormBackArgs {
 // The rows of a block in turn; its share of dweight stays in registers (CH 0: in
 // memory, each lane adding to its own).
 // Bound by HBM: 8192 x 4096 bf16 66 us (4.1 TB/s), 4099 x 4096 fp32 57 (4.7), rows that start
-// anywhere in a line less (5003 fp32 3.75).  The row's sums are fp32: the registers are full, and
-// in 64 bits 8192 x 8192 bf16 would take 211 us, not 133.
+// anywhere in a line less (4099 x 5003 fp32 89 us, 3.7).  The row's sums are fp32: the registers are
+// full, and in 64 bits 8192 x 8192 bf16 would take 211 us, not 132.  Rows whose squares fp32 may not
+// hold are summed a second time; for its code four chunks keep up to 6 registers in scratch,
+// since one more than 168 would leave two blocks a compute unit (209 us; 131 without that code).
 template <int LANES, int CH, typename T>
-__global__ __launch_bounds__(256) void norm_backward(NormBackArgs a) {
+__global__ __launch_bounds__(256, CH == 4 ? 3 : 1) void norm_backward(NormBackArgs a) {
   constexpr int N = CH ? CH : 1, ROWS = 256 / LANES;
   __shared__ float part[4][2];
   __shared__ float join[LANES == 64 && CH ? N * 512 : 1];
@@ -199,10 +201,8 @@ __global__ __launch_bounds__(256) void norm_backward(NormBackArgs a) {
     const T* dy = (const T*)a.dy + row * a.d;
     const T* s = (const T*)a.s + row * a.d;
     float u[N][8], v[N][8], sums[2] = {0.0f, 0.0f};
-    auto first = [&](int64_t j, float* g, float* h) {
+    auto add = [&](int64_t j, const float* g, const float* h) {
       float w[8];
-      load8_of_row<false>(dy, j, a.d, g);
-      load8_of_row<false>(s, j, a.d, h);
       load_weights(a.weight, a.w_type, j, a.d, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -210,14 +210,45 @@ __global__ __launch_bounds__(256) void norm_backward(NormBackArgs a) {
         sums[1] = __builtin_fmaf(g[i] * w[i], h[i], sums[1]);
       }
     };
-    if (CH) {
+    int e = 0;  // s is taken 2^-e times
+    auto load = [&](int64_t j, float* g, float* h) {
+      load8_of_row<false>(dy, j, a.d, g);
+      load8_of_row<false>(s, j, a.d, h);
+    };
+    auto scale = [&](float* h) {
 #pragma unroll
-      for (int c = 0; c < N; ++c) first((int64_t)(c * LANES + lane) * 8, u[c], v[c]);
-    } else {
-      for (int64_t j = lane * 8; j < a.d; j += LANES * 8) first(j, u[0], v[0]);
+      for (int i = 0; i < 8; ++i) h[i] = __builtin_ldexpf(h[i], -e);
+    };
+    // The row's sums, of values from memory or (CH) as they are held.
+    auto sum_up = [&](bool held) {
+      sums[0] = sums[1] = 0.0f;
+      if (CH) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          if (held)
+            scale(v[c]);
+          else
+            load((int64_t)(c * LANES + lane) * 8, u[c], v[c]);
+          add((int64_t)(c * LANES + lane) * 8, u[c], v[c]);
+        }
+      } else {
+        for (int64_t j = lane * 8; j < a.d; j += LANES * 8) {
+          load(j, u[0], v[0]);
+          if (held) scale(v[0]);
+          add(j, u[0], v[0]);
+        }
+      }
+      row_sum<LANES>(sums, part);
+      return sums[0] / (float)a.d + __builtin_ldexpf(a.eps, -2 * e);
+    };
+    float mean = sum_up(false);
+    // Squares that fp32 may not have held: again with s by a power of two, which leaves a root of
+    // the mean from 2^-126 on between 2^-46 and 2^44.
+    if (__builtin_expect(mean < 0x1p-80f || mean > 0x1p80f, 0)) {
+      e = mean > 1.0f ? 84 : -80;
+      mean = sum_up(true);
     }
-    row_sum<LANES>(sums, part);
-    const float r = 1.0f / __builtin_sqrtf(sums[0] / (float)a.d + a.eps);
+    const float r = 1.0f / __builtin_sqrtf(mean), rs = __builtin_ldexpf(r, -e);  // of s 2^-e, of s
     const float f = sums[1] / (float)a.d * r * r;
     auto second = [&](int64_t j, const float* g, const float* h, float* share) {
       if (a.ds) {
@@ -228,7 +259,7 @@ __global__ __launch_bounds__(256) void norm_backward(NormBackArgs a) {
         if (a.dsum) load8_of_row<false>((const T*)a.dsum + row * a.d, j, a.d, t);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          t[i] = __builtin_fmaf(r, __builtin_fmaf(-h[i], f, g[i] * w[i]), t[i]);
+          t[i] = __builtin_fmaf(rs, __builtin_fmaf(-h[i], f, g[i] * w[i]), t[i]);
         store8_of_row<false>((T*)a.ds + row * a.d, j, a.d, t);
       }
 #pragma unroll
@@ -239,8 +270,8 @@ __global__ __launch_bounds__(256) void norm_backward(NormBackArgs a) {
       for (int c = 0; c < N; ++c) second((int64_t)(c * LANES + lane) * 8, u[c], v[c], dw[c]);
     } else {
       for (int64_t j = lane * 8; j < a.d; j += LANES * 8) {
-        load8_of_row<false>(dy, j, a.d, u[0]);
-        load8_of_row<false>(s, j, a.d, v[0]);
+        load(j, u[0], v[0]);
+        if (e != 0) scale(v[0]);
         float share[8] = {};
         if (mine && !fresh) load8_of_row<false>(mine, j, a.d, share);
         second(j, u[0], v[0], share);
@@ -343,7 +374,7 @@ hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
 
 // Blocks of the backward kernel, each with a share of dweight: as many as are on the chip at
 // once, since each takes as many rows (registers: three of a compute unit from three chunks
-// on, four below; 4099 x 5003 fp32 104 us with 1024 blocks, 87 with 768).
+// on, four below; 4099 x 5003 fp32 104 us with 1024 blocks, 89 with 768).
 int64_t shares_of(int64_t rows, int64_t d) {
   const int64_t most = (d + 7) / 8 > 512 ? 768 : 1024;
   return rows < most ? rows : most;

@@ -1,5 +1,6 @@
 """RMS norm and its gradients on the GPU where tests/test_gpu_norm.py says nothing: blocks
-that take many rows, large rows past the caches, values rounded once.
+that take many rows, large rows past the caches, values rounded once, rows of any
+magnitude.
 
 Bars of the gradients: those of tests/test_gpu_norm.py."""
 
@@ -24,7 +25,9 @@ def check_backward(dy, s, w, t, eps, got, dw):
     tol = (3 * chain(d) + 16) * 2.0 ** -24 * (np.abs(r * u) + np.abs(hs) * r ** 3 * np.abs(u * hs).mean(1, keepdims=True))
     if ht is not None:
         tol = tol + 2.0 ** -24 * np.abs(want)
-    assert np.all(np.abs(host(got) - want) <= tol + HALF[s.dtype] * (np.abs(want) + tol))
+    # below 2^-126 a step is the type's smallest value, 2^-149 or 2^-133, however small the result
+    step = 2.0 ** -149 if s.dtype == torch.float32 else 2.0 ** -133
+    assert np.all(np.abs(host(got) - want) <= tol + HALF[s.dtype] * (np.abs(want) + tol) + step / 2)
     tol = (chain(d) / 2 + 16 + rows) * 2.0 ** -24 * np.abs(hy * hs * r).sum(0)
     assert np.all(np.abs(host(dw) - want_w) <= tol)
 
@@ -76,3 +79,58 @@ def test_values_are_rounded_once(rows, d, dtype):
         y, s = qw.rms_norm(x, weight, residual=res, eps=1e-5, out_dtype=torch.float32)
         want = om.norm(host(s), None if weight is None else host(weight), 1e-5)
         assert np.all(np.abs(host(y) - want) <= 2.0 ** -24 * (1 + 2.0 ** -20) * np.abs(want))
+
+
+def rows_of_any_size(d, dtype, powers, seed):
+    """Rows of normal values times a power of two each, as dtype holds them."""
+    rng = np.random.default_rng([d, seed])
+    return torch.from_numpy((rng.standard_normal((len(powers), d)) * 2.0 ** np.array(powers, float)[:, None]).astype(np.float32)).cuda().to(dtype)
+
+
+# fp32's subnormal values begin below 2^-126; normal ones times 2^125 end below its largest
+POWERS = [0, -146, -140, -132, -128, -120, -90, -60, -30, 30, 60, 90, 124, 125]
+
+
+@pytest.mark.parametrize("d", [100, 900, 2000, 5003, 17000])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("times", [1, 100])
+def test_gradients_of_rows_of_any_magnitude(d, dtype, times):
+    """dy 2^-12 of normal values, so that the gradients of the smallest rows are in fp32's range.  A
+    row's squares as fp32 holds them would be zero from 2^-75 down and infinite from 2^64 up."""
+    powers = [p for p in POWERS if p >= -120] * times
+    s = rows_of_any_size(d, dtype, powers, 2)
+    dy = rows_of_any_size(d, dtype, [-12] * len(powers), 3)
+    w = torch.linspace(0.5, 1.5, d, device="cuda")
+    got, dw = qw.rms_norm_backward(dy, s, w, eps=0.0)
+    check_backward(dy, s, w, None, 0.0, got, dw)
+    # the gradient past the norm of the gradient's own size, in its place
+    t = (got.float() * 0.75).to(dtype)
+    want, _ = qw.rms_norm_backward(dy, s, w, eps=0.0, dsum=t)
+    check_backward(dy, s, w, t, 0.0, want, dw)
+    again, dw2 = qw.rms_norm_backward(dy, s, w, eps=0.0, dsum=t, ds=t)
+    assert again is t and torch.equal(again, want) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("d", [100, 2000, 17000])
+@pytest.mark.parametrize("eps", [2.0 ** -100, 2.0 ** -149, 2.0 ** 120])
+def test_gradients_with_eps_of_any_magnitude(d, eps):
+    """Rows of zeros, rows whose squares are far below eps, near it and above it."""
+    e = int(np.log2(eps)) // 2
+    powers = [e - 40, e - 3, e, e + 3, e + 40] if e > -70 else [e - 10, e - 3, e, e + 3, e + 40]
+    s = rows_of_any_size(d, torch.float32, powers + [0], 4)
+    s[-1] = 0.0
+    dy = rows_of_any_size(d, torch.float32, [-12] * len(s), 5)
+    w = torch.linspace(0.5, 1.5, d, device="cuda")
+    got, dw = qw.rms_norm_backward(dy, s, w, eps=eps)
+    check_backward(dy, s, w, None, eps, got, dw)
+
+
+@pytest.mark.parametrize("d", [100, 2000, 17000])
+def test_gradients_of_rows_without_values_of_their_own(d):
+    """A row of zeros without eps, of an infinity, of a NaN: NaN as the definition has it, and no harm to others."""
+    s, _, w = inputs(6, d, torch.float32)
+    dy = torch.randn(6, d, device="cuda")
+    clean, _ = qw.rms_norm_backward(dy, s, w, eps=0.0)
+    s[1], s[2, d // 2], s[4, 3] = 0.0, float("nan"), float("inf")
+    got, _ = qw.rms_norm_backward(dy, s, w, eps=0.0)
+    assert torch.equal(got[[0, 3, 5]], clean[[0, 3, 5]]) and bool(torch.isnan(got[[1, 2, 4]]).all())
