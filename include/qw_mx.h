@@ -97,7 +97,10 @@ int qw_mx_matmul(int64_t n, int64_t k, const uint8_t* codes, const uint8_t* scal
  *   weight [d] of weight_type, or NULL (all 1)   (read)
  *   y [rows][d] of y_type (written)
  * eps is finite and >= 0 (QW_EARG).  x, residual and sum have `type`.  Squares
- * and their sum are held in 64 bits; y is rounded to fp32 and then to its type.
+ * and their sum are held in 64 bits; y is rounded to fp32 and then to its type, for
+ * rows with sqrt(mean(s^2) + eps) from 2^-126 to 2^100.  (Beyond 2^100 the factor of a
+ * row has fewer bits, y is off by 2^-21 of itself at most; below 2^-128, which takes
+ * subnormal values and such an eps, the factor and y are infinite.)
  */
 int qw_rms_norm(int64_t rows, int64_t d, int type, const void* x, const void* residual,
                 void* sum, int weight_type, const void* weight, float eps, int y_type, void* y,

@@ -91,6 +91,28 @@ def rows_of_any_size(d, dtype, powers, seed):
 POWERS = [0, -146, -140, -132, -128, -120, -90, -60, -30, 30, 60, 90, 124, 125]
 
 
+@pytest.mark.parametrize("d", [100, 900, 2000, 17000])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_over_the_range_of_r(d, dtype):
+    """Without eps, so that y has no magnitude of its own left.  Rounded once up to 2^100; beyond, r's
+    second part and then bits of its first are below fp32's smallest value, 2^-150 of 2^-128 at
+    most; below 2^-128 r is infinite."""
+    x = rows_of_any_size(d, dtype, POWERS, 1)
+    w = torch.linspace(0.5, 1.5, d, device="cuda")
+    y, _ = qw.rms_norm(x, w, eps=0.0, out_dtype=torch.float32)
+    want = om.norm(host(x), host(w), 0.0)
+    for i, p in enumerate(POWERS):
+        if -126 < p < 128:
+            bar = (2.0 ** -24 + (2.0 ** -22 if p > 100 else 0.0)) * (1 + 2.0 ** -20) * np.abs(want[i])
+            assert np.all(np.abs(host(y[i]) - want[i]) <= bar)
+        elif p < -130:
+            assert not bool(y[i].isfinite().any())
+    for form, quantize in (("block", lambda v: qw.block_quantize(v, 1)), ("mx", qw.mx_quantize)):
+        got, want = qw.rms_norm(x, w, eps=0.0, quantize=form)[0], quantize(y)
+        assert torch.equal(got["scales"].view(torch.uint8), want["scales"].view(torch.uint8))
+        assert torch.equal(got["codes"].view(torch.uint8), want["codes"].view(torch.uint8))
+
+
 @pytest.mark.parametrize("d", [100, 900, 2000, 5003, 17000])
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("times", [1, 100])
