@@ -189,7 +189,8 @@ int qw_mx_mlp(int64_t d, int64_t f, const uint8_t* gate_up, const uint8_t* gate_
  * Diagnostic: which kernel a call of these sizes would take, or a negative status;
  * `op`: 0 qw_mx_gemm, 1 qw_mx_gated, 2 qw_mx_gated_codes, 3 qw_mx_gated_backward (n = f):
  *     100 t + u = the kernel whose waves share k, with 16 t rows of x and u units of 512
- *     values of k a wave; 2 = tiles of 64 x 64 whose waves share every step of k;
+ *     values of k a wave (105: run by the kernel of 6 units, with the last one empty);
+ *     2 = tiles of 64 x 64 whose waves share every step of k;
  *     otherwise 1000 * weight rows + tokens of a tile
  *   4 qw_mx_matmul: 1 = the product quantizes x, 2 = a kernel before it does
  * Enqueues nothing.
