@@ -965,6 +965,15 @@ hipError_t run_stream(const MxArgs& a, const MxGemm& g, hipStream_t stream) {
 //    512 4096  4096     29.1     19.5     16.2     14.1     12.6
 //    128 4096  4096                       15.4     12.7      9.4
 //    128 4096 11008                       31.4     26.3     17.7
+// and, the same choice, for other results (4096 11008 2048 with fp32 results; 2047 tokens, 2 x 11008
+// weight rows, k = 4096 gated):
+//   fp32 results         74.5     84       79        96
+//   gated codes         111.5    128      126       180
+//   gated bf16, fp32    112.5    127      125       167
+//   gradients, bf16     150.5    157      150       190
+//   gradients, fp32     239      221      221       295
+// The last row is the one that the choice has wrong by 8 in a hundred: with fp32 gradients 256 x 256
+// tiles keep 28 registers in scratch (9 with bf16; no other tile or result any).
 // (256 x 128, weight rows first, loses to 128 x 256 by 2 to 5 in a hundred; 64 x 64 with two
 // waves one after the other in k takes 12.7 and 26.1 in the last two and leads nowhere.)
 struct Shape {

@@ -14,7 +14,9 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
          (int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32;
 }
 
-// A buffer descriptor of `bytes` from `base`: reads beyond give zeros.
+// A buffer descriptor of `bytes` from `base`: reads beyond give zeros.  The scalar offset of a
+// load counts (measured: voff + soff >= bytes reads nothing, an empty buffer at any soff), on
+// which copies behind a row's last scales and behind the last tile rely.
 __device__ __forceinline__ i32x4 buffer_of(const void* base, uint32_t bytes) {
   const uint64_t p = (uint64_t)base;
   return i32x4{(int)(uint32_t)p, (int)(uint32_t)(p >> 32), (int)bytes, 0x00020000};
