@@ -100,7 +100,8 @@ def test_rows_over_the_range_of_r(d, dtype):
     x = rows_of_any_size(d, dtype, POWERS, 1)
     w = torch.linspace(0.5, 1.5, d, device="cuda")
     y, _ = qw.rms_norm(x, w, eps=0.0, out_dtype=torch.float32)
-    want = om.norm(host(x), host(w), 0.0)
+    with np.errstate(divide="ignore", invalid="ignore"):  # bf16 has no values in the smallest rows
+        want = om.norm(host(x), host(w), 0.0)
     for i, p in enumerate(POWERS):
         if -126 < p < 128:
             bar = (2.0 ** -24 + (2.0 ** -22 if p > 100 else 0.0)) * (1 + 2.0 ** -20) * np.abs(want[i])
